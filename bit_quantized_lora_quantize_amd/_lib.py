@@ -130,6 +130,8 @@ def lib() -> ctypes.CDLL:
         L.qlora_linear_bwd_dropout.argtypes = [ctypes.POINTER(_Nf4), _P, _P, _I64, _P, _P, _I64,
                                                ctypes.c_float, ctypes.POINTER(_Dropout), _P, _P,
                                                _P, _P, _P, ctypes.c_size_t, _P]
+        from . import _train
+        _train.declare(L)
         _lib = L
     return _lib
 

@@ -1,0 +1,347 @@
+"""ctypes binding of libqlora's entry points around the linear layers
+(include/qlora.h): norms, token log-probabilities, the preference loss and the
+clipped policy loss.  Argument marshalling only, as in _lib.py.
+
+Outputs that are not passed in are allocated on the inputs' device; work goes
+to the current stream of that device."""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import _lib
+from ._lib import _check, _need
+
+QLORA_BF16, QLORA_F32 = 0, 1
+QLORA_NORM_LAYER, QLORA_NORM_RMS = 0, 1
+QLORA_PREF_SIGMOID, QLORA_PREF_HINGE, QLORA_PREF_SQUARED = 0, 1, 2
+QLORA_POLICY_TOKEN_MEAN, QLORA_POLICY_SEQUENCE_MEAN = 0, 1
+IGNORE_INDEX = -100
+
+_TYPES = {torch.bfloat16: QLORA_BF16, torch.float32: QLORA_F32}
+_P = ctypes.c_void_p
+_I64 = ctypes.c_int64
+_F = ctypes.c_float
+
+
+class _Logits(ctypes.Structure):
+    _fields_ = [("logits", _P), ("targets", _P), ("rows", _I64), ("vocab", _I64), ("ld", _I64),
+                ("ignore_index", _I64), ("type", ctypes.c_int), ("scale", _F)]
+
+
+class _Preference(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("length_normalize", ctypes.c_int), ("beta", _F),
+                ("label_smoothing", _F), ("margin", _F), ("weight", _F)]
+
+
+class _Policy(ctypes.Structure):
+    _fields_ = [("reduction", ctypes.c_int), ("per_token", ctypes.c_int), ("clip_low", _F),
+                ("clip_high", _F), ("kl_coef", _F), ("weight", _F)]
+
+
+def declare(L: ctypes.CDLL) -> None:
+    """Argument types of this module's entry points."""
+    i, sz, lp = ctypes.c_int, ctypes.c_size_t, ctypes.POINTER(_Logits)
+    L.qlora_norm_fwd.argtypes = [i, i, _P, _P, _I64, _I64, i, _P, _P, _F, _P, _P, _P, _P, _P]
+    L.qlora_norm_bwd.argtypes = [i, i, _P, _P, _P, _I64, _I64, i, _P, _P, _P, _P, _P, _P, _P, sz,
+                                 _P]
+    L.qlora_norm_workspace_bytes.restype = sz
+    L.qlora_norm_workspace_bytes.argtypes = [_I64, _I64]
+    L.qlora_token_logp.argtypes = [lp, _P, _P, _P]
+    L.qlora_token_logp_bwd.argtypes = [lp, _P, _P, _P, _I64, _P]
+    L.qlora_preference_workspace_bytes.restype = sz
+    L.qlora_preference_workspace_bytes.argtypes = [_I64]
+    L.qlora_preference_loss.argtypes = [lp, _P, _I64, _P, ctypes.POINTER(_Preference), _P, _P, _P,
+                                        _P, _I64, _P, sz, _P]
+    L.qlora_policy_workspace_bytes.restype = sz
+    L.qlora_policy_workspace_bytes.argtypes = [_I64, _I64]
+    L.qlora_policy_loss.argtypes = [lp, _P, _I64, _P, _P, _P, ctypes.POINTER(_Policy), _P, _P, _P,
+                                    _I64, _P, sz, _P]
+
+
+def _raw_stream(device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _out(t, shape, dtype, device, name):
+    """The caller's output after a check, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, dtype, shape, name)
+    return t
+
+
+# ---------------------------------------------------------------------- norms
+
+class NormOut(NamedTuple):
+    Y: torch.Tensor
+    H: torch.Tensor                 # X + residual (X itself without one)
+    mean: Optional[torch.Tensor]    # FP32 [M], layer norm only
+    rstd: Optional[torch.Tensor]    # FP32 [M]
+
+
+class NormGrads(NamedTuple):
+    dX: torch.Tensor
+    dgamma: Optional[torch.Tensor]
+    dbeta: Optional[torch.Tensor]
+
+
+def _weight_type(gamma, beta, d):
+    wt = _TYPES.get(gamma.dtype)
+    if wt is None:
+        raise ValueError(f"gamma: expected bfloat16 or float32, got {gamma.dtype}")
+    _need(gamma, gamma.dtype, (d,), "gamma")
+    if beta is not None:
+        _need(beta, gamma.dtype, (d,), "beta")
+    return wt
+
+
+def _matrix_type(X, name):
+    t = _TYPES.get(X.dtype)
+    if t is None or X.dim() != 2:
+        raise ValueError(f"{name}: expected a bfloat16 or float32 matrix, got {X.dtype} "
+                         f"{tuple(X.shape)}")
+    return t
+
+
+def qlora_norm_fwd(X: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tensor] = None,
+                   eps: float = 1e-5, kind: int = QLORA_NORM_LAYER,
+                   residual: Optional[torch.Tensor] = None, H: Optional[torch.Tensor] = None,
+                   Y: Optional[torch.Tensor] = None, save_stats: bool = True) -> NormOut:
+    """Norm of X, or of H = X + residual, over the last axis.  H and Y may be
+    given; H may be X or the residual.  save_stats=False leaves out what only
+    the backward needs."""
+    ty = _matrix_type(X, "X")
+    M, d = X.shape
+    dev = X.device
+    _need(X, X.dtype, (M, d), "X")
+    wt = _weight_type(gamma, beta, d)
+    if residual is not None:
+        _need(residual, X.dtype, (M, d), "residual")
+        H = _out(H, (M, d), X.dtype, dev, "H")
+    Y = _out(Y, (M, d), X.dtype, dev, "Y")
+    mean = rstd = None
+    if save_stats:
+        rstd = torch.empty(M, dtype=torch.float32, device=dev)
+        if kind == QLORA_NORM_LAYER:
+            mean = torch.empty(M, dtype=torch.float32, device=dev)
+    _check(_lib.lib().qlora_norm_fwd(kind, ty, X.data_ptr(), _addr(residual), M, d, wt,
+                                     gamma.data_ptr(), _addr(beta), eps,
+                                     H.data_ptr() if residual is not None else None, Y.data_ptr(),
+                                     _addr(mean), _addr(rstd), _raw_stream(dev)),
+           "qlora_norm_fwd")
+    return NormOut(Y, H if residual is not None else X, mean, rstd)
+
+
+def qlora_norm_workspace_bytes(M: int, d: int) -> int:
+    return int(_lib.lib().qlora_norm_workspace_bytes(M, d))
+
+
+def qlora_norm_bwd(dY: torch.Tensor, H: torch.Tensor, gamma: torch.Tensor,
+                   mean: Optional[torch.Tensor], rstd: torch.Tensor,
+                   kind: int = QLORA_NORM_LAYER, dH: Optional[torch.Tensor] = None,
+                   need_dgamma: bool = True, need_dbeta: bool = False,
+                   dX: Optional[torch.Tensor] = None, dgamma: Optional[torch.Tensor] = None,
+                   dbeta: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None) -> NormGrads:
+    """Backward of qlora_norm_fwd for its H, mean and rstd; dH is the gradient
+    that reaches H past the norm.  dX may be dY or dH."""
+    ty = _matrix_type(H, "H")
+    M, d = H.shape
+    dev = H.device
+    _need(H, H.dtype, (M, d), "H")
+    _need(dY, H.dtype, (M, d), "dY")
+    wt = _weight_type(gamma, None, d)
+    _need(rstd, torch.float32, (M,), "rstd")
+    if kind == QLORA_NORM_LAYER:
+        if mean is None:
+            raise ValueError("mean: the layer norm's backward needs it")
+        _need(mean, torch.float32, (M,), "mean")
+    if dH is not None:
+        _need(dH, H.dtype, (M, d), "dH")
+    dX = _out(dX, (M, d), H.dtype, dev, "dX")
+    ws = None
+    if need_dgamma or need_dbeta:
+        dgamma = _out(dgamma, (d,), torch.float32, dev, "dgamma") if need_dgamma else None
+        dbeta = _out(dbeta, (d,), torch.float32, dev, "dbeta") if need_dbeta else None
+        ws = workspace
+        if ws is None:
+            ws = _lib._workspace(qlora_norm_workspace_bytes(M, d), dev)
+    else:
+        dgamma = dbeta = None
+    _check(_lib.lib().qlora_norm_bwd(kind, ty, dY.data_ptr(), H.data_ptr(), _addr(dH), M, d, wt,
+                                     gamma.data_ptr(), _addr(mean), rstd.data_ptr(),
+                                     dX.data_ptr(), _addr(dgamma), _addr(dbeta), _addr(ws),
+                                     0 if ws is None else ws.numel(), _raw_stream(dev)),
+           "qlora_norm_bwd")
+    return NormGrads(dX, dgamma, dbeta)
+
+
+# ---------------------------------------------------------- losses on logits
+
+def _logits(logits, targets, ignore_index, scale):
+    """The C description of a logits batch.  Rows may be strided (a padded
+    vocabulary); their elements are contiguous."""
+    ty = _matrix_type(logits, "logits")
+    rows, vocab = logits.shape
+    ld = logits.stride(0)
+    if rows <= 1:
+        ld = max(ld, vocab)
+    if not logits.is_cuda or (vocab > 1 and logits.stride(1) != 1) or ld < vocab:
+        raise ValueError(f"logits: expected rows of contiguous elements on the GPU, got strides "
+                         f"{logits.stride()} on {logits.device}")
+    _need(targets, torch.int64, (rows,), "targets")
+    return _Logits(logits.data_ptr(), targets.data_ptr(), rows, vocab, ld, ignore_index, ty, scale)
+
+
+def _dlogits(dlogits, logits, l):
+    """The gradient's buffer (by default laid out as the logits) and its row
+    stride."""
+    if dlogits is None:
+        dlogits = torch.empty_strided((l.rows, l.vocab), (l.ld, 1), dtype=logits.dtype,
+                                      device=logits.device)
+        return dlogits, l.ld
+    ldd = dlogits.stride(0) if l.rows > 1 else max(dlogits.stride(0), l.vocab)
+    if (dlogits.dtype != logits.dtype or dlogits.shape != logits.shape or not dlogits.is_cuda or
+            (l.vocab > 1 and dlogits.stride(1) != 1) or ldd < l.vocab):
+        raise ValueError(f"dlogits: expected {logits.dtype} {tuple(logits.shape)} with contiguous "
+                         f"elements in a row, got {dlogits.dtype} {tuple(dlogits.shape)} with "
+                         f"strides {dlogits.stride()}")
+    return dlogits, ldd
+
+
+def qlora_token_logp(logits: torch.Tensor, targets: torch.Tensor,
+                     ignore_index: int = IGNORE_INDEX, scale: float = 1.0,
+                     logp: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
+    """(logp, lse), FP32 [rows]: log-probability of each row's target under
+    softmax(scale * logits) and the log of the row's summed exponentials."""
+    l = _logits(logits, targets, ignore_index, scale)
+    dev = logits.device
+    logp = _out(logp, (l.rows,), torch.float32, dev, "logp")
+    lse = _out(lse, (l.rows,), torch.float32, dev, "lse")
+    _check(_lib.lib().qlora_token_logp(l, logp.data_ptr(), lse.data_ptr(), _raw_stream(dev)),
+           "qlora_token_logp")
+    return logp, lse
+
+
+def qlora_token_logp_bwd(logits: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                         dlogp: torch.Tensor, ignore_index: int = IGNORE_INDEX, scale: float = 1.0,
+                         dlogits: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of the logits from upstream gradients of qlora_token_logp's
+    log-probabilities; dlogits may be the logits themselves."""
+    l = _logits(logits, targets, ignore_index, scale)
+    _need(lse, torch.float32, (l.rows,), "lse")
+    _need(dlogp, torch.float32, (l.rows,), "dlogp")
+    dlogits, ldd = _dlogits(dlogits, logits, l)
+    _check(_lib.lib().qlora_token_logp_bwd(l, lse.data_ptr(), dlogp.data_ptr(),
+                                           dlogits.data_ptr(), ldd, _raw_stream(logits.device)),
+           "qlora_token_logp_bwd")
+    return dlogits
+
+
+class PreferenceOut(NamedTuple):
+    loss: torch.Tensor                # FP32 [pairs]
+    seq_logp: torch.Tensor            # FP32 [2 pairs]
+    logp: torch.Tensor                # FP32 [rows]
+    dlogits: Optional[torch.Tensor]   # like the logits
+
+
+def qlora_preference_workspace_bytes(rows: int) -> int:
+    return int(_lib.lib().qlora_preference_workspace_bytes(rows))
+
+
+def qlora_preference_loss(logits: torch.Tensor, targets: torch.Tensor, offsets: torch.Tensor,
+                          ref_logp: Optional[torch.Tensor] = None, kind: int = QLORA_PREF_SIGMOID,
+                          beta: float = 0.1, label_smoothing: float = 0.0, margin: float = 0.0,
+                          length_normalize: bool = False, weight: Optional[float] = None,
+                          ignore_index: int = IGNORE_INDEX, scale: float = 1.0,
+                          need_grad: bool = True, dlogits: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None) -> PreferenceOut:
+    """Preference loss of the pairs (sequence p preferred to sequence pairs +
+    p; offsets int64 [2 pairs + 1] are the sequences' first rows) and the
+    gradient of weight * sum of the losses (weight None: 1 / pairs, the mean).
+    dlogits may be the logits themselves."""
+    l = _logits(logits, targets, ignore_index, scale)
+    dev = logits.device
+    n = offsets.numel()
+    if n % 2 == 0:
+        raise ValueError(f"offsets: expected 2 pairs + 1 of them, got {n}")
+    pairs = n // 2
+    _need(offsets, torch.int64, (n,), "offsets")
+    if ref_logp is not None:
+        _need(ref_logp, torch.float32, (l.rows,), "ref_logp")
+    par = _Preference(kind, 1 if length_normalize else 0, beta, label_smoothing, margin,
+                      1.0 / max(1, pairs) if weight is None else weight)
+    logp = torch.empty(l.rows, dtype=torch.float32, device=dev)
+    seq_logp = torch.empty(2 * pairs, dtype=torch.float32, device=dev)
+    loss = torch.empty(pairs, dtype=torch.float32, device=dev)
+    ldd = 0
+    if need_grad:
+        dlogits, ldd = _dlogits(dlogits, logits, l)
+    else:
+        dlogits = None
+    ws = workspace
+    if ws is None:
+        ws = _lib._workspace(qlora_preference_workspace_bytes(l.rows), dev)
+    _check(_lib.lib().qlora_preference_loss(l, offsets.data_ptr(), pairs, _addr(ref_logp), par,
+                                            logp.data_ptr(), seq_logp.data_ptr(), loss.data_ptr(),
+                                            _addr(dlogits), ldd, ws.data_ptr(), ws.numel(),
+                                            _raw_stream(dev)), "qlora_preference_loss")
+    return PreferenceOut(loss, seq_logp, logp, dlogits)
+
+
+class PolicyOut(NamedTuple):
+    stats: torch.Tensor               # FP32 [4]: loss, policy term, KL, clipped share
+    logp: torch.Tensor                # FP32 [rows]
+    dlogits: Optional[torch.Tensor]   # like the logits
+
+
+def qlora_policy_workspace_bytes(rows: int, sequences: int) -> int:
+    return int(_lib.lib().qlora_policy_workspace_bytes(rows, sequences))
+
+
+def qlora_policy_loss(logits: torch.Tensor, targets: torch.Tensor, offsets: torch.Tensor,
+                      advantages: torch.Tensor, old_logp: Optional[torch.Tensor] = None,
+                      ref_logp: Optional[torch.Tensor] = None, clip_low: float = 0.2,
+                      clip_high: float = 0.2, kl_coef: float = 0.0, per_token: bool = False,
+                      reduction: int = QLORA_POLICY_TOKEN_MEAN, weight: float = 1.0,
+                      ignore_index: int = IGNORE_INDEX, scale: float = 1.0,
+                      need_grad: bool = True, dlogits: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None) -> PolicyOut:
+    """Clipped policy loss with a KL term over the sequences whose first rows
+    are offsets (int64 [sequences + 1]), and the gradient of weight * loss.
+    advantages: FP32 [sequences], or [rows] with per_token.  dlogits may be
+    the logits themselves."""
+    l = _logits(logits, targets, ignore_index, scale)
+    dev = logits.device
+    seqs = offsets.numel() - 1
+    if seqs < 0:
+        raise ValueError("offsets: expected sequences + 1 of them")
+    _need(offsets, torch.int64, (seqs + 1,), "offsets")
+    _need(advantages, torch.float32, (l.rows if per_token else seqs,), "advantages")
+    if old_logp is not None:
+        _need(old_logp, torch.float32, (l.rows,), "old_logp")
+    if ref_logp is not None:
+        _need(ref_logp, torch.float32, (l.rows,), "ref_logp")
+    par = _Policy(reduction, 1 if per_token else 0, clip_low, clip_high, kl_coef, weight)
+    logp = torch.empty(l.rows, dtype=torch.float32, device=dev)
+    stats = torch.empty(4, dtype=torch.float32, device=dev)
+    ldd = 0
+    if need_grad:
+        dlogits, ldd = _dlogits(dlogits, logits, l)
+    else:
+        dlogits = None
+    ws = workspace
+    if ws is None:
+        ws = _lib._workspace(qlora_policy_workspace_bytes(l.rows, seqs), dev)
+    _check(_lib.lib().qlora_policy_loss(l, offsets.data_ptr(), seqs, advantages.data_ptr(),
+                                        _addr(old_logp), _addr(ref_logp), par, logp.data_ptr(),
+                                        stats.data_ptr(), _addr(dlogits), ldd, ws.data_ptr(),
+                                        ws.numel(), _raw_stream(dev)), "qlora_policy_loss")
+    return PolicyOut(stats, logp, dlogits)

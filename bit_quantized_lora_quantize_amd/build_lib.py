@@ -12,8 +12,8 @@ Also builds two variants from the same sources:
                      qlora_time_next_weight_kernel (include/qlora_timing.h),
                      an event pair around the next weight-kernel launch; the
                      library proper keeps no such state;
-  libqlora_san.so    a test build whose host code in api.cpp and noalloc.hip
-                     (argument checks, plans, workspace carving) is built with
+  libqlora_san.so    a test build whose host code in api.cpp, api_train.cpp
+                     and noalloc.hip (argument checks, plans, workspace carving) is built with
                      AddressSanitizer and UndefinedBehaviorSanitizer; the GPU
                      code is the same.  Loaded with the clang ASan runtime
                      preloaded (tests/test_sanitized.py).
@@ -40,13 +40,14 @@ LIB_PEAKS = os.path.join(PKG, "libqlora_peaks.so")
 LIB_SAN = os.path.join(PKG, "libqlora_san.so")
 # host code built with sanitizers in libqlora_san.so (each -fsanitize= applies
 # to the host pass only)
-SAN_SOURCES = ["api.cpp", "noalloc.hip"]
+SAN_SOURCES = ["api.cpp", "api_train.cpp", "noalloc.hip"]
 SAN_FLAGS = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
              "-Xarch_host", "-fno-sanitize-recover=undefined", "-fno-omit-frame-pointer", "-g"]
 # sources that hold the timing hook or launch a weight kernel
 TIMED_SOURCES = ["quant.hip", "gemv.hip", "gemm.hip", "api.cpp"]
 
-SOURCES = ["quant.hip", "quant_blocked.hip", "lora.hip", "gemv.hip", "gemm.hip", "merge.hip", "optim.hip", "dropout.hip", "noalloc.hip", "api.cpp"]
+SOURCES = ["quant.hip", "quant_blocked.hip", "lora.hip", "gemv.hip", "gemm.hip", "merge.hip", "optim.hip", "dropout.hip", "noalloc.hip",
+           "norm.hip", "logits.hip", "api.cpp", "api_train.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

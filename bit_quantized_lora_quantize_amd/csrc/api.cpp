@@ -9,6 +9,7 @@
 #include <cstring>
 #include <vector>
 
+#include "api_util.h"
 #include "qlora.h"
 #include "qlora_device.h"
 #include "qlora_kernels.h"
@@ -49,29 +50,6 @@ namespace {
 
 constexpr int64_t kMaxRank = 256;
 constexpr int64_t kSmallM = 16;      // M <= 16 streams the weight (GEMV path)
-// Layer sizes and token counts per call: every device byte offset the kernels
-// form within one tile, split or transposed copy then stays below 2^31.
-constexpr int64_t kMaxLinearDim = int64_t(1) << 21;
-constexpr int64_t kMaxTokens = int64_t(1) << 21;
-
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-inline int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
-
-// Sequential carving of a workspace into 256-byte aligned pieces; with a null
-// base it only measures.
-struct Carver {
-  char* base;
-  size_t off = 0;
-  explicit Carver(void* b) : base(static_cast<char*>(b)) {}
-  template <class T>
-  T* take(int64_t count) {
-    off = (off + 255) & ~size_t(255);
-    T* p = base ? reinterpret_cast<T*>(base + off) : nullptr;
-    off += size_t(std::max<int64_t>(count, 0)) * sizeof(T);
-    return p;
-  }
-};
 
 bool shape_ok(int64_t d_out, int64_t d_in) {
   return d_out >= 1 && d_in >= kBlock && d_in % kBlock == 0 && d_out <= (int64_t(1) << 31) &&
@@ -322,8 +300,6 @@ const IndexLut& lut() {
   static const IndexLut l = make_lut();
   return l;
 }
-
-inline int hip_status(hipError_t e) { return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP; }
 
 // ------------------------------------------------------------- rank-r products
 // v = scale * P Q^T (P [M][K], Q [N][ldq]) with the outputs of RankRowsArgs;
@@ -635,7 +611,7 @@ const char* qlora_status_string(int status) {
   }
 }
 
-int qlora_abi_version(void) { return (1 << 16) | 1; }
+int qlora_abi_version(void) { return (1 << 16) | 2; }
 
 int qlora_nf4_sizes(int64_t d_out, int64_t d_in, size_t* codes_bytes, size_t* scale_codes_bytes,
                     size_t* scale2_bytes, size_t* scale_mean_bytes) {

@@ -468,6 +468,94 @@ struct GemmArgs {
 hipError_t launch_gemm_fwd(const GemmArgs& a, hipStream_t st);
 hipError_t launch_gemm_bwd(const GemmArgs& a, hipStream_t st);
 
+// ------------------------------------------------- norms
+// Element types are QLORA_BF16 / QLORA_F32; the operations are stated at
+// qlora_norm_fwd and qlora_norm_bwd.
+struct NormFwdArgs {
+  const void* x;
+  const void* r;      // residual or NULL
+  const void* gamma;
+  const void* beta;   // or NULL
+  void* h;            // X + R, written when r is given
+  void* y;
+  float* mean;        // or NULL
+  float* rstd;        // or NULL
+  int64_t rows, d;
+  float eps;
+  int kind, type, w_type;
+};
+hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t st);
+
+struct NormBwdArgs {
+  const void* dy;
+  const void* h;
+  const void* dh;     // or NULL
+  const void* gamma;
+  const float* mean;  // NULL for RMS
+  const float* rstd;
+  void* dx;
+  float* dgamma;      // or NULL
+  float* dbeta;       // or NULL
+  float* part;        // [norm_parts(rows, d)][2][d] partial weight gradients
+  int64_t rows, d;
+  int kind, type, w_type;
+};
+// Row groups whose weight gradients are summed apart (rows >= 1).
+int norm_parts(int64_t rows, int64_t d);
+hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t st);
+
+// ------------------------------------------------- losses on logits
+struct LogitsArgs {
+  const void* logits;
+  const int64_t* targets;
+  int64_t rows, vocab, ld;
+  int64_t ignore;
+  int type;
+  float scale;
+};
+// What a gradient needs of a row's softmax: p = exp(scale * (l - max) - logsum).
+struct RowStat {
+  float max, logsum;
+};
+// logp (and lse, stat: either may be NULL) of every row.
+hipError_t launch_logp(const LogitsArgs& l, float* logp, float* lse, RowStat* stat,
+                       hipStream_t st);
+// dlogits from per-row coefficients; the softmax comes from stat, or from
+// lse where stat is NULL.
+hipError_t launch_dlogits(const LogitsArgs& l, const RowStat* stat, const float* lse,
+                          const float* dlogp, void* dlogits, int64_t ldd, hipStream_t st);
+
+struct PreferenceArgs {
+  const int64_t* targets;
+  const int64_t* offsets;  // [2 pairs + 1]
+  const float* logp;
+  const float* ref;        // or NULL
+  int64_t rows, pairs, ignore;
+  int kind, length_normalize;
+  float beta, smoothing, margin, weight;
+  float* seq_logp;         // [2 pairs]
+  float* loss;             // [pairs]
+  float* dlogp;            // [rows], or NULL for the loss alone
+};
+hipError_t launch_preference(const PreferenceArgs& a, hipStream_t st);
+
+struct PolicyArgs {
+  const int64_t* offsets;  // [seqs + 1]
+  const float* adv;
+  const float* old_logp;   // or NULL
+  const float* ref;        // or NULL
+  int64_t seqs;
+  int reduction, per_token;
+  float clip_low, clip_high, kl_coef, weight;
+  float* logp;
+  float* stats;            // [4]
+  int32_t* count;          // [seqs] rows of each sequence that count
+  int32_t* row_seq;        // [rows] sequence of each row, -1 without one
+  float4* terms;           // [rows] w, policy, kl, clipped
+};
+hipError_t launch_policy(const LogitsArgs& l, const PolicyArgs& a, void* dlogits, int64_t ldd,
+                         RowStat* stat, float* dlogp, hipStream_t st);
+
 // ------------------------------------------------- host-side checks
 // qlora_linear_fwd's argument checks for a workspace of ws_bytes bytes (not
 // dereferenced): QLORA_ERR_WORKSPACE when the call needs more.

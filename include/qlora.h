@@ -14,13 +14,15 @@
  *     qlora_linear_fwd_noalloc works in); it never synchronizes.  Work is
  *     enqueued on `stream` (a
  *     hipStream_t; NULL means the null stream) and the call returns at once.
- *   - All matrices are dense row-major.  BF16 values are passed as their
+ *   - All matrices are dense row-major (logits and their gradients: rows of
+ *     stride ld).  BF16 values are passed as their
  *     uint16_t bit patterns.
  *   - Arguments are checked on the host before anything is enqueued; on any
  *     error the call returns a negative qlora_status and enqueues nothing.
  *     A failing kernel launch returns QLORA_ERR_HIP (work enqueued before it
  *     on the same call may have run).  Non-finite inputs are a precondition
- *     violation and are not detected.
+ *     violation and are not detected, except where an entry point says
+ *     otherwise.
  *   - Pointers marked (16B) must be 16-byte aligned.
  *   - Calls that share a workspace buffer must be ordered (same stream or
  *     explicit events); calls on different buffers may overlap freely.
@@ -460,6 +462,204 @@ int qlora_adamw_step(int count, const qlora_adamw_param *params, float lr,
                      float beta1, float beta2, float eps, float weight_decay,
                      int64_t step, const double *grad_sumsq,
                      float max_grad_norm, void *stream);
+
+/*
+ * The operators around the linear layers of a fine-tuning step: the norm in
+ * front of the projections, and the losses on the head's logits.
+ *
+ * Element types of their arrays.  Arrays of these entry points need the
+ * alignment of their element type only (rows of odd length start anywhere);
+ * 16-byte aligned rows are fastest, with the same results.  Infinities and
+ * NaN in their inputs are allowed and propagate as IEEE arithmetic has it
+ * (a logit of -inf is a token that cannot be drawn).
+ */
+#define QLORA_BF16 0
+#define QLORA_F32 1
+
+/*
+ * Norm over the last axis, with the residual addition in front of it:
+ *     H = RN(X + R)                    (R given; else H = X)
+ *     LAYER:  Y = (H - mean) * rstd * gamma + beta,  mean = sum(H) / d,
+ *             rstd = 1 / sqrt(sum((H - mean)^2) / d + eps)
+ *     RMS:    Y = H * rstd * gamma,    rstd = 1 / sqrt(sum(H^2) / d + eps)
+ * Sums and statistics are FP32 (the variance from the centred values); H is
+ * rounded to its type first and the norm is that of the rounded H, so the
+ * backward, which reads H, sees the same values.  Y is rounded once.
+ *   kind    QLORA_NORM_LAYER or QLORA_NORM_RMS
+ *   X, R    [M, d] of `type`; R NULL for no residual.  0 <= M <= 2^21,
+ *           1 <= d <= 2^21.
+ *   gamma   [d] of `w_type`; beta [d] of `w_type` or NULL (RMS: NULL, else
+ *           QLORA_ERR_SHAPE)
+ *   eps     finite, >= 0
+ *   H       [M, d] output, needed with R (may be X or R); NULL without
+ *   Y       [M, d] output (may be X when R is NULL)
+ *   mean    FP32 [M] or NULL (not written for RMS); rstd FP32 [M] or NULL:
+ *           saved for the backward
+ */
+#define QLORA_NORM_LAYER 0
+#define QLORA_NORM_RMS 1
+int qlora_norm_fwd(int kind, int type, const void *X, const void *R, int64_t M,
+                   int64_t d, int w_type, const void *gamma, const void *beta,
+                   float eps, void *H, void *Y, float *mean, float *rstd,
+                   void *stream);
+
+/*
+ * Backward of qlora_norm_fwd: with n = (H - mean) * rstd and u = dY * gamma,
+ *     dX = (u - sum(u) / d - n * sum(u * n) / d) * rstd + dH
+ *     dgamma = sum over rows of dY * n,   dbeta = sum over rows of dY
+ * (RMS: mean = 0 and no sum(u) term).  dH is the gradient that reaches H past
+ * the norm (the residual stream); dX is the gradient of X and of R.
+ *   dY, H   [M, d] of `type` (H: the forward's H, or its X without residual)
+ *   dH      [M, d] of `type` or NULL
+ *   mean    FP32 [M] (LAYER), rstd FP32 [M]: from the forward
+ *   dX      [M, d] output of `type` (may be dY or dH)
+ *   dgamma  FP32 [d] or NULL, dbeta FP32 [d] or NULL: overwritten (M = 0
+ *           writes zeros).  With both NULL (frozen norm) no workspace is used.
+ * workspace (16B) >= qlora_norm_workspace_bytes(M, d) when dgamma or dbeta
+ * is given.  Sums over rows are taken in a fixed order: deterministic.
+ */
+int qlora_norm_bwd(int kind, int type, const void *dY, const void *H,
+                   const void *dH, int64_t M, int64_t d, int w_type,
+                   const void *gamma, const float *mean, const float *rstd,
+                   void *dX, float *dgamma, float *dbeta, void *workspace,
+                   size_t workspace_bytes, void *stream);
+/* Host only; 0 for sizes the call would reject. */
+size_t qlora_norm_workspace_bytes(int64_t M, int64_t d);
+
+/*
+ * Logits of a batch of tokens and the tokens they are judged by.  Row i's
+ * distribution is softmax(scale * logits[i]); a row whose target is
+ * ignore_index does not count (its log-probability is 0, its gradient row is
+ * 0, its logits are not read).  Any other target outside [0, vocab) gives
+ * NaN in its row (log-probability and gradient); nothing is read for it.
+ *   logits  [rows, ld] of `type`, ld >= vocab (columns vocab .. ld - 1 are
+ *           neither read nor written).  0 <= rows <= 2^21,
+ *           1 <= vocab <= 2^24.
+ *   scale   finite, > 0 (1 / temperature)
+ */
+typedef struct {
+  const void *logits;
+  const int64_t *targets;  /* [rows] */
+  int64_t rows, vocab, ld;
+  int64_t ignore_index;
+  int type;                /* QLORA_BF16 or QLORA_F32 */
+  float scale;
+} qlora_logits_t;
+
+/*
+ * Log-probability of each row's target, and the log of the row's summed
+ * exponentials:
+ *     lse = log(sum_j exp(scale * l_j)),   logp = scale * l_target - lse.
+ * Taken from the row's maximum on, sums in FP32.
+ *   logp, lse  FP32 [rows] outputs, lse NULL when no backward follows; both
+ *              0 in rows that do not count.
+ */
+int qlora_token_logp(const qlora_logits_t *l, float *logp, float *lse,
+                     void *stream);
+
+/*
+ * Gradient of the logits for upstream gradients of the log-probabilities:
+ *     dlogits[i][j] = scale * dlogp[i] * ((j == target_i) - p_ij),
+ *     p_ij = exp(scale * l_ij - lse_i).
+ * Rows that do not count and rows with dlogp = 0 are written as zeros without
+ * being read.  p carries the rounding of the FP32 lse.
+ *   lse, dlogp  FP32 [rows]; dlogits [rows, ldd] output of l->type,
+ *               ldd >= vocab; may be the logits' own buffer (ldd = ld).
+ */
+int qlora_token_logp_bwd(const qlora_logits_t *l, const float *lse,
+                         const float *dlogp, void *dlogits, int64_t ldd,
+                         void *stream);
+
+/*
+ * Preference loss over pairs of answers, from the logits to their gradient.
+ * Sequence i is the rows offsets[i] .. offsets[i + 1] - 1; sequences 0 ..
+ * pairs - 1 are the preferred answers and pairs .. 2 pairs - 1, in the same
+ * order, the others.  With s_i = sum of logp over the sequence's rows that
+ * count, and g_i = sum of (logp - ref_logp) over them (ref_logp NULL: g_i =
+ * s_i), each divided by the number of such rows when length_normalize is set
+ * (an empty sequence gives 0):
+ *     h = g_p - g_(pairs + p),   z = beta * h - margin
+ *     SIGMOID  loss_p = (1 - e) softplus(-z) + e softplus(z), e = label_smoothing
+ *     HINGE    loss_p = max(0, 1 - z)
+ *     SQUARED  loss_p = (h - 1 / (2 beta))^2
+ * and dlogits is the gradient of weight * sum_p loss_p.  (On one frozen base,
+ * ref_logp is qlora_token_logp on the logits of the same layers without
+ * their adapter.)  Sums over a sequence are FP64.
+ *   l          the logits of all sequences
+ *   offsets    int64 [2 pairs + 1], nondecreasing, in [0, rows] (device
+ *              memory: values outside are clamped to that range); rows that
+ *              no sequence holds get zero gradients.  pairs >= 0
+ *   ref_logp   FP32 [rows] or NULL
+ *   logp       FP32 [rows] output; seq_logp FP32 [2 pairs] output (s_i);
+ *   loss       FP32 [pairs] output
+ *   dlogits    [rows, ldd] output of l->type, as in qlora_token_logp_bwd, or
+ *              NULL for the loss alone
+ * QLORA_ERR_SHAPE for beta not finite and > 0, label_smoothing outside
+ * [0, 1) or with another kind than SIGMOID, margin or weight not finite, a
+ * margin with SQUARED.  workspace (16B) >=
+ * qlora_preference_workspace_bytes(rows).  Deterministic.
+ */
+#define QLORA_PREF_SIGMOID 0
+#define QLORA_PREF_HINGE 1
+#define QLORA_PREF_SQUARED 2
+typedef struct {
+  int kind;
+  int length_normalize;
+  float beta, label_smoothing, margin, weight;
+} qlora_preference_t;
+
+int qlora_preference_loss(const qlora_logits_t *l, const int64_t *offsets,
+                          int64_t pairs, const float *ref_logp,
+                          const qlora_preference_t *par, float *logp,
+                          float *seq_logp, float *loss, void *dlogits,
+                          int64_t ldd, void *workspace, size_t workspace_bytes,
+                          void *stream);
+/* Host only; 0 for rows outside the documented range. */
+size_t qlora_preference_workspace_bytes(int64_t rows);
+
+/*
+ * Clipped policy loss with a KL term, from the logits to their gradient.
+ * For every row t that counts and lies in a sequence s (rows offsets[s] ..
+ * offsets[s + 1] - 1), with a its advantage:
+ *     ratio = exp(logp - old_logp)          (old_logp NULL: 1, on-policy)
+ *     policy = max(-a ratio, -a clamp(ratio, 1 - clip_low, 1 + clip_high))
+ *     kl     = exp(ref_logp - logp) - (ref_logp - logp) - 1  (ref NULL: 0)
+ *     loss   = sum over t of w_t (policy_t + kl_coef kl_t)
+ *     TOKEN_MEAN     w_t = 1 / (number of such rows)
+ *     SEQUENCE_MEAN  w_t = 1 / (sequences * number of such rows of s)
+ * dlogits is the gradient of weight * loss; where the clipped branch is the
+ * larger one the policy term has no gradient, at equality the unclipped
+ * branch's counts.  The gradient comes from the same pass over the logits
+ * as the loss: they are read once where a row fits a workgroup's registers.
+ *   offsets     int64 [sequences + 1] as in qlora_preference_loss
+ *   advantages  FP32 [rows] with per_token, else FP32 [sequences]
+ *   old_logp, ref_logp  FP32 [rows] or NULL (ref_logp NULL needs kl_coef 0,
+ *               else QLORA_ERR_NULL)
+ *   logp        FP32 [rows] output
+ *   stats       FP32 [4] output: loss, sum w policy, sum w kl, sum w [the
+ *               clipped branch is the larger one]
+ *   dlogits     [rows, ldd] output of l->type, as in qlora_token_logp_bwd, or
+ *               NULL for the loss alone
+ * QLORA_ERR_SHAPE for clip_low outside [0, 1], clip_high or kl_coef not
+ * finite or < 0, weight not finite.  workspace (16B) >=
+ * qlora_policy_workspace_bytes(rows, sequences).  Deterministic.
+ */
+#define QLORA_POLICY_TOKEN_MEAN 0
+#define QLORA_POLICY_SEQUENCE_MEAN 1
+typedef struct {
+  int reduction;
+  int per_token;
+  float clip_low, clip_high, kl_coef, weight;
+} qlora_policy_t;
+
+int qlora_policy_loss(const qlora_logits_t *l, const int64_t *offsets,
+                      int64_t sequences, const float *advantages,
+                      const float *old_logp, const float *ref_logp,
+                      const qlora_policy_t *par, float *logp, float *stats,
+                      void *dlogits, int64_t ldd, void *workspace,
+                      size_t workspace_bytes, void *stream);
+/* Host only; 0 for sizes outside the documented range. */
+size_t qlora_policy_workspace_bytes(int64_t rows, int64_t sequences);
 
 /* Static English text for a qlora_status value. */
 const char *qlora_status_string(int status);
