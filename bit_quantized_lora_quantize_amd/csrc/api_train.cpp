@@ -74,8 +74,6 @@ PreferencePlan plan_preference(int64_t rows, void* ws) {
 }
 
 struct PolicyPlan {
-  RowStat* stat;
-  float* dlogp;
   int32_t* count;
   int32_t* row_seq;
   float4* terms;
@@ -84,8 +82,6 @@ struct PolicyPlan {
 PolicyPlan plan_policy(int64_t rows, int64_t seqs, void* ws) {
   PolicyPlan p{};
   Carver c(ws);
-  p.stat = c.take<RowStat>(rows);
-  p.dlogp = c.take<float>(rows);
   p.count = c.take<int32_t>(seqs);
   p.row_seq = c.take<int32_t>(rows);
   p.terms = c.take<float4>(rows);
@@ -267,7 +263,7 @@ int qlora_policy_loss(const qlora_logits_t* l, const int64_t* offsets, int64_t s
                      sequences,      par->reduction, par->per_token, par->clip_low,
                      par->clip_high, par->kl_coef,   par->weight,    logp,
                      stats,          p.count,        p.row_seq,      p.terms};
-  return hip_status(launch_policy(logits_args(l), a, dlogits, ldd, p.stat, p.dlogp,
+  return hip_status(launch_policy(logits_args(l), a, dlogits, ldd,
                                   static_cast<hipStream_t>(stream)));
 }
 

@@ -318,30 +318,183 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& a, int64_t row
   return o;
 }
 
-// Weight of a row of sequence s (counts of all sequences summed by the
-// workgroup for the mean over tokens).
-template <int THREADS>
-__device__ __forceinline__ float policy_total(const PolicyArgs& a, int* lds) {
-  int n = 0;
-  if (a.reduction == QLORA_POLICY_TOKEN_MEAN)
-    for (int64_t i = threadIdx.x; i < a.seqs; i += THREADS) n += a.count[i];
-  return (float)block_sum<THREADS>(n, lds);
-}
+// Weight of a row of sequence s; `total` counts the rows of all sequences.
 __device__ __forceinline__ float policy_weight(const PolicyArgs& a, int s, float total) {
   if (s < 0) return 0.0f;
   return a.reduction == QLORA_POLICY_TOKEN_MEAN ? 1.0f / total
                                                 : 1.0f / ((float)a.seqs * (float)a.count[s]);
 }
 
-__global__ __launch_bounds__(256) void k_policy_rows(LogitsArgs l, PolicyArgs a, float* dlogp) {
-  __shared__ int lds[4];
-  const float total = policy_total<256>(a, lds);
-  const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (row >= l.rows) return;
-  const int s = a.row_seq[row];
-  const PolicyRow o = policy_row(a, row, s, policy_weight(a, s, total), a.logp[row]);
-  a.terms[row] = o.terms;
-  if (dlogp) dlogp[row] = o.dlogp;
+// Sum of the sequences' counts for the mean over tokens, by one wavefront
+// (every lane gets it).
+__device__ __forceinline__ float policy_total(const PolicyArgs& a) {
+  if (a.reduction != QLORA_POLICY_TOKEN_MEAN) return 0.0f;
+  int n = 0;
+  for (int64_t i = threadIdx.x & 63; i < a.seqs; i += 64) n += a.count[i];
+  return (float)wave_sum(n);
+}
+
+// A row's gradient where no logit is read: zeros, or NaN for a bad target.
+template <typename T, int THREADS>
+__device__ __forceinline__ void fill_row(T* out, int vocab, float value) {
+  constexpr int N = kVec<T>;
+  float f[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) f[j] = value;
+  const u32x4 v = pack<T>(f);
+  const int nvec = vocab / N;
+  for (int i = threadIdx.x; i < nvec; i += THREADS) store_vec(out + (int64_t)i * N, v);
+  const int i = nvec * N + (int)threadIdx.x;
+  if (i < vocab) from_f32(value, out[i]);
+}
+
+// Loss and gradient of one row in one pass: the row's logits stay in
+// registers (E of them a thread, as FP32 terms once the maximum is known),
+// so they are read once and their exponentials taken once.  dlogits NULL:
+// the loss alone, with the same bits.
+template <typename T, int THREADS, int E, int MIN_WAVES>
+__global__ __launch_bounds__(THREADS, MIN_WAVES) void k_policy(LogitsArgs l, PolicyArgs a,
+                                                               T* dlogits, int64_t ldd) {
+  constexpr int N = kVec<T>, V = E / N;
+  __shared__ float lds_m[THREADS / 64], lds_s[THREADS / 64], lds_g;
+  const int64_t row = blockIdx.x;
+  const int vocab = (int)l.vocab, nvec = vocab / N;
+  const int64_t t = l.targets[row];
+  const int seq = a.row_seq[row];
+  T* out = dlogits ? dlogits + row * ldd : nullptr;
+  const bool lead = threadIdx.x < 64;
+  if (t == l.ignore || t < 0 || t >= l.vocab) {
+    const float lp = t == l.ignore ? 0.0f : __builtin_nanf("");
+    if (lead) {
+      const float total = policy_total(a);
+      if (threadIdx.x == 0) {
+        a.logp[row] = lp;
+        a.terms[row] = policy_row(a, row, seq, policy_weight(a, seq, total), lp).terms;
+      }
+    }
+    if (out) fill_row<T, THREADS>(out, vocab, seq < 0 ? 0.0f : lp);
+    return;
+  }
+  const T* x = static_cast<const T*>(l.logits) + row * l.ld;
+  const float xt = to_f32(x[t]);
+  u32x4 d[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int v = i * THREADS + (int)threadIdx.x;
+    d[i] = vec_neg_inf<T>();
+    if (v < nvec) d[i] = load_vec(x + (int64_t)v * N);
+  }
+  const int last = nvec * N + (int)threadIdx.x;   // the last, partial vector
+  float el = last < vocab ? to_f32(x[last]) : -kInf;
+  float e[E], m = el;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    unpack<T>(d[i], e + i * N);
+#pragma unroll
+    for (int j = 0; j < N; ++j) m = fmaxf(m, e[i * N + j]);
+  }
+  m = shift(block_max<THREADS>(m, lds_m));
+  const float k = l.scale * kLog2e;
+  float s = el = term(el, m, k);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    unpack<T>(d[i], e + i * N);
+#pragma unroll
+    for (int j = 0; j < N; ++j) s += e[i * N + j] = term(e[i * N + j], m, k);
+  }
+  s = block_sum<THREADS>(s, lds_s);
+  if (lead) {
+    const float total = policy_total(a);
+    if (threadIdx.x == 0) {
+      const float lp = (xt - m) * l.scale - logf(s);
+      const PolicyRow o = policy_row(a, row, seq, policy_weight(a, seq, total), lp);
+      a.logp[row] = lp;
+      a.terms[row] = o.terms;
+      lds_g = o.dlogp * l.scale;
+    }
+  }
+  if (!out) return;
+  __syncthreads();
+  const float g = lds_g, c = -g / s;
+  if (g == 0.0f) {
+    fill_row<T, THREADS>(out, vocab, 0.0f);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int v = i * THREADS + (int)threadIdx.x;
+    float* f = e + i * N;
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[j] *= c;
+    if ((uint32_t)((int)t - v * N) < (uint32_t)N) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) f[j] += v * N + j == (int)t ? g : 0.0f;
+    }
+    if (v < nvec) store_vec(out + (int64_t)v * N, pack<T>(f));
+  }
+  if (last < vocab) from_f32(el * c + (last == (int)t ? g : 0.0f), out[last]);
+}
+
+// The same where a row does not fit the registers: it is read a second time,
+// from the caches as far as they reach.
+template <typename T, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_policy_long(LogitsArgs l, PolicyArgs a, T* dlogits,
+                                                         int64_t ldd) {
+  constexpr int N = kVec<T>, kU = 2;
+  __shared__ MaxSum lds[THREADS / 64];
+  __shared__ float lds_g;
+  const int64_t row = blockIdx.x;
+  const int vocab = (int)l.vocab, nvec = vocab / N;
+  const int64_t t = l.targets[row];
+  const int seq = a.row_seq[row];
+  T* out = dlogits ? dlogits + row * ldd : nullptr;
+  const bool lead = threadIdx.x < 64;
+  const bool skip = t == l.ignore || t < 0 || t >= l.vocab;
+  const T* x = static_cast<const T*>(l.logits) + row * l.ld;
+  const float k = l.scale * kLog2e;
+  MaxSum v{0.0f, 1.0f};
+  if (!skip) v = block_join<THREADS>(stream_row<T, THREADS>(x, vocab, k), k, lds);
+  const float m = shift(v.m), ls = logf(v.s);
+  if (lead) {
+    const float total = policy_total(a);
+    if (threadIdx.x == 0) {
+      const float lp = t == l.ignore ? 0.0f
+                       : skip        ? __builtin_nanf("")
+                                     : (to_f32(x[t]) - m) * l.scale - ls;
+      const PolicyRow o = policy_row(a, row, seq, policy_weight(a, seq, total), lp);
+      a.logp[row] = lp;
+      a.terms[row] = o.terms;
+      lds_g = skip ? (seq < 0 ? 0.0f : lp) : o.dlogp * l.scale;
+    }
+  }
+  if (!out) return;
+  __syncthreads();
+  const float g = lds_g;
+  if (skip || g == 0.0f) {
+    fill_row<T, THREADS>(out, vocab, g);
+    return;
+  }
+  const RowGrad q{g, m, ls * kLog2e, k, (int)t};
+  for (int v0 = threadIdx.x; v0 < nvec; v0 += THREADS * kU) {
+    u32x4 d[kU];
+#pragma unroll
+    for (int i = 0; i < kU; ++i)
+      if (v0 + i * THREADS < nvec) d[i] = load_vec(x + (int64_t)(v0 + i * THREADS) * N);
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      if (v0 + i * THREADS >= nvec) continue;
+      float f[N];
+      unpack<T>(d[i], f);
+      grad_terms<N>(q, (v0 + i * THREADS) * N, f);
+      store_vec(out + (int64_t)(v0 + i * THREADS) * N, pack<T>(f));
+    }
+  }
+  const int i = nvec * N + (int)threadIdx.x;
+  if (i < vocab) {
+    float f = to_f32(x[i]);
+    grad_terms<1>(q, i, &f);
+    from_f32(f, out[i]);
+  }
 }
 
 __global__ __launch_bounds__(1024) void k_policy_stats(PolicyArgs a, int64_t rows) {
@@ -412,18 +565,36 @@ hipError_t launch_preference(const PreferenceArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// E logits a thread and THREADS a row, the smallest that hold the row.
+template <typename T>
+static void policy_by_width(const LogitsArgs& l, const PolicyArgs& a, T* dlogits, int64_t ldd,
+                            hipStream_t st) {
+  const dim3 grid((unsigned)l.rows);
+  if (l.vocab <= 512)
+    hipLaunchKernelGGL((k_policy<T, 64, 8, 8>), grid, dim3(64), 0, st, l, a, dlogits, ldd);
+  else if (l.vocab <= 2048)
+    hipLaunchKernelGGL((k_policy<T, 64, 32, 6>), grid, dim3(64), 0, st, l, a, dlogits, ldd);
+  else if (l.vocab <= 8192)
+    hipLaunchKernelGGL((k_policy<T, 256, 32, 8>), grid, dim3(256), 0, st, l, a, dlogits, ldd);
+  else if (l.vocab <= 16384)
+    hipLaunchKernelGGL((k_policy<T, 512, 32, 8>), grid, dim3(512), 0, st, l, a, dlogits, ldd);
+  else if (l.vocab <= 32768)
+    hipLaunchKernelGGL((k_policy<T, 1024, 32, 8>), grid, dim3(1024), 0, st, l, a, dlogits, ldd);
+  else if (l.vocab <= 65536)
+    hipLaunchKernelGGL((k_policy<T, 1024, 64, 4>), grid, dim3(1024), 0, st, l, a, dlogits, ldd);
+  else
+    hipLaunchKernelGGL((k_policy_long<T, 1024>), grid, dim3(1024), 0, st, l, a, dlogits, ldd);
+}
+
 hipError_t launch_policy(const LogitsArgs& l, const PolicyArgs& a, void* dlogits, int64_t ldd,
-                         RowStat* stat, float* dlogp, hipStream_t st) {
+                         hipStream_t st) {
   if (l.rows > 0) {
     const unsigned seqs = (unsigned)std::max<int64_t>(a.seqs, 1);
     hipLaunchKernelGGL(k_policy_count, dim3(seqs), dim3(256), 0, st, l, a);
-    hipError_t e = launch_logp(l, a.logp, nullptr, stat, st);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_policy_rows, dim3((unsigned)((l.rows + 255) / 256)), dim3(256), 0, st, l,
-                       a, dlogits ? dlogp : nullptr);
-    if (dlogits) {
-      e = launch_dlogits(l, stat, nullptr, dlogp, dlogits, ldd, st);
-      if (e != hipSuccess) return e;
+    if (l.type == QLORA_BF16) {
+      policy_by_width(l, a, static_cast<uint16_t*>(dlogits), ldd, st);
+    } else {
+      policy_by_width(l, a, static_cast<float*>(dlogits), ldd, st);
     }
   }
   hipLaunchKernelGGL(k_policy_stats, dim3(1), dim3(1024), 0, st, a, l.rows);

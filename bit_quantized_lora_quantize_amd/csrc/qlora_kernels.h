@@ -553,8 +553,9 @@ struct PolicyArgs {
   int32_t* row_seq;        // [rows] sequence of each row, -1 without one
   float4* terms;           // [rows] w, policy, kl, clipped
 };
+// dlogits NULL: the loss alone.
 hipError_t launch_policy(const LogitsArgs& l, const PolicyArgs& a, void* dlogits, int64_t ldd,
-                         RowStat* stat, float* dlogp, hipStream_t st);
+                         hipStream_t st);
 
 // ------------------------------------------------- host-side checks
 // qlora_linear_fwd's argument checks for a workspace of ws_bytes bytes (not
