@@ -62,7 +62,8 @@ def declare(L: ctypes.CDLL) -> None:
 
 
 def _raw_stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    """The current stream's handle, without building a Stream object."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _addr(t: Optional[torch.Tensor]):

@@ -15,6 +15,7 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kInf = __builtin_huge_valf();
+constexpr int kPrefThreads = 1024;
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
@@ -192,11 +193,13 @@ __global__ __launch_bounds__(256) void k_dlogits(LogitsArgs l, const RowStat* st
   }
 }
 
-// One workgroup per pair: both sequences' sums in FP64, the loss and its
-// slope, the gradient of every log-probability.  The first and the last
-// workgroup also clear the rows before and after all sequences.
-__global__ __launch_bounds__(256) void k_preference(PreferenceArgs a) {
-  __shared__ double lds[6][4];
+// One workgroup per pair, half of it per sequence: the sequences' sums in
+// FP64, the loss and its slope, the gradient of every log-probability (also of
+// rows that do not count: their logits' gradient is 0 whatever it is).  The
+// first and the last workgroup clear the rows before and after all sequences.
+__global__ __launch_bounds__(kPrefThreads) void k_preference(PreferenceArgs a) {
+  constexpr int kSide = kPrefThreads / 2, W = kSide / 64;
+  __shared__ double lds[3][2 * W];
   const int64_t p = blockIdx.x;
   if (a.dlogp) {
     int64_t b0 = 0, e1 = 0, skip;
@@ -205,64 +208,74 @@ __global__ __launch_bounds__(256) void k_preference(PreferenceArgs a) {
       seq_rows(a.offsets, 2 * a.pairs - 1, a.rows, skip, e1);
     }
     if (p == 0)
-      for (int64_t i = threadIdx.x; i < b0; i += 256) a.dlogp[i] = 0.0f;
+      for (int64_t i = threadIdx.x; i < b0; i += kPrefThreads) a.dlogp[i] = 0.0f;
     if (p == gridDim.x - 1)
-      for (int64_t i = e1 + threadIdx.x; i < a.rows; i += 256) a.dlogp[i] = 0.0f;
+      for (int64_t i = e1 + threadIdx.x; i < a.rows; i += kPrefThreads) a.dlogp[i] = 0.0f;
   }
   if (a.pairs == 0) return;
-  double s[2], g[2], n[2];
+  const int side = threadIdx.x / kSide, lane = threadIdx.x % kSide;
+  int64_t b, e;
+  seq_rows(a.offsets, p + side * a.pairs, a.rows, b, e);
+  double vs = 0.0, vg = 0.0, vn = 0.0;
+  for (int64_t i = b + lane; i < e; i += kSide) {
+    const float lp = a.logp[i], rf = a.ref ? a.ref[i] : 0.0f;
+    if (a.targets[i] == a.ignore) continue;
+    vs += (double)lp;
+    vg += (double)lp - (double)rf;
+    vn += 1.0;
+  }
+  vs = wave_sum(vs);
+  vg = wave_sum(vg);
+  vn = wave_sum(vn);
+  const int wave = threadIdx.x / 64;
+  if ((threadIdx.x & 63) == 0) {
+    lds[0][wave] = vs;
+    lds[1][wave] = vg;
+    lds[2][wave] = vn;
+  }
+  __syncthreads();
+  double s[2] = {0.0, 0.0}, g[2] = {0.0, 0.0}, n[2] = {0.0, 0.0};
 #pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    int64_t b, e;
-    seq_rows(a.offsets, p + side * a.pairs, a.rows, b, e);
-    double vs = 0.0, vg = 0.0, vn = 0.0;
-    for (int64_t i = b + threadIdx.x; i < e; i += 256) {
-      if (a.targets[i] == a.ignore) continue;
-      const float lp = a.logp[i];
-      vs += (double)lp;
-      vg += a.ref ? (double)lp - (double)a.ref[i] : (double)lp;
-      vn += 1.0;
-    }
-    s[side] = block_sum<256>(vs, lds[3 * side]);
-    g[side] = block_sum<256>(vg, lds[3 * side + 1]);
-    n[side] = block_sum<256>(vn, lds[3 * side + 2]);
-    if (a.length_normalize) {
-      n[side] = n[side] < 1.0 ? 1.0 : n[side];
-      s[side] /= n[side];
-      g[side] /= n[side];
+  for (int w = 0; w < 2 * W; ++w) {
+    s[w / W] += lds[0][w];
+    g[w / W] += lds[1][w];
+    n[w / W] += lds[2][w];
+  }
+  if (a.length_normalize) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      n[i] = n[i] < 1.0 ? 1.0 : n[i];
+      s[i] /= n[i];
+      g[i] /= n[i];
     }
   }
-  const double h = g[0] - g[1], beta = a.beta, z = beta * h - a.margin;
-  double loss, slope;
+  // the sums need 64 bits; the loss of their small difference does not
+  const double h = g[0] - g[1];
+  const float beta = a.beta, z = (float)((double)beta * h - (double)a.margin);
+  float loss, slope;
   if (a.kind == QLORA_PREF_SIGMOID) {
-    const double e = a.smoothing, x = exp(-fabs(z));
-    const double low = log1p(x), tail = x / (1.0 + x);   // tail = sigmoid(-|z|)
-    loss = (1.0 - e) * ((z < 0.0 ? -z : 0.0) + low);     // softplus(-z)
-    if (e > 0.0) loss += e * ((z > 0.0 ? z : 0.0) + low);
-    slope = beta * (z > 0.0 ? e - tail : tail - (1.0 - e));
+    const float sm = a.smoothing, x = expf(-fabsf(z));
+    const float low = log1pf(x), tail = x / (1.0f + x);   // tail = sigmoid(-|z|)
+    loss = (1.0f - sm) * ((z < 0.0f ? -z : 0.0f) + low);  // softplus(-z)
+    if (sm > 0.0f) loss += sm * ((z > 0.0f ? z : 0.0f) + low);
+    slope = beta * (z > 0.0f ? sm - tail : tail - (1.0f - sm));
   } else if (a.kind == QLORA_PREF_HINGE) {
-    loss = z < 1.0 ? 1.0 - z : (z == z ? 0.0 : z);
-    slope = z < 1.0 ? -beta : (z == z ? 0.0 : z);
+    loss = z < 1.0f ? 1.0f - z : (z == z ? 0.0f : z);
+    slope = z < 1.0f ? -beta : (z == z ? 0.0f : z);
   } else {
-    const double off = h - 0.5 / beta;
+    const float off = (float)(h - 0.5 / (double)beta);
     loss = off * off;
-    slope = 2.0 * off;
+    slope = 2.0f * off;
   }
   if (threadIdx.x == 0) {
-    a.loss[p] = (float)loss;
+    a.loss[p] = loss;
     a.seq_logp[p] = (float)s[0];
     a.seq_logp[p + a.pairs] = (float)s[1];
   }
   if (!a.dlogp) return;
-#pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    int64_t b, e;
-    seq_rows(a.offsets, p + side * a.pairs, a.rows, b, e);
-    double c = (side ? -slope : slope) * (double)a.weight;
-    if (a.length_normalize) c /= n[side];
-    for (int64_t i = b + threadIdx.x; i < e; i += 256)
-      a.dlogp[i] = a.targets[i] == a.ignore ? 0.0f : (float)c;
-  }
+  float c = (side ? -slope : slope) * a.weight;
+  if (a.length_normalize) c /= (float)n[side];
+  for (int64_t i = b + lane; i < e; i += kSide) a.dlogp[i] = c;
 }
 
 // One workgroup per sequence: the rows that count, and each row's sequence.
@@ -561,7 +574,7 @@ hipError_t launch_dlogits(const LogitsArgs& l, const RowStat* stat, const float*
 
 hipError_t launch_preference(const PreferenceArgs& a, hipStream_t st) {
   const unsigned grid = (unsigned)std::max<int64_t>(a.pairs, 1);
-  hipLaunchKernelGGL(k_preference, dim3(grid), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(k_preference, dim3(grid), dim3(kPrefThreads), 0, st, a);
   return hipGetLastError();
 }
 

@@ -131,6 +131,9 @@ __device__ __forceinline__ void write_partial(const Part<T, ROW, E>& p, int grou
   }
 }
 
+constexpr int kBwdThreads = 1024;
+constexpr int kFinishCols = 16;
+
 }  // namespace
 
 // THREADS / ROW rows per workgroup, each by ROW of its threads.
@@ -296,26 +299,41 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(NormBwdArgs a, int parts) 
   }
 }
 
-// Weight gradients from the partials: 64 columns per workgroup, 16 slices of
-// the partials summed apart and added in order.
+// Weight gradients from the partials: kFinishCols columns per workgroup, the
+// partials in slices summed apart, eight loads in flight, and added
+// in order.
 __global__ __launch_bounds__(1024) void k_norm_wgrad_finish(const float* part, int parts,
                                                             int64_t d, float* dgamma,
                                                             float* dbeta) {
-  __shared__ float lds[16][64];
-  const int col = threadIdx.x & 63, slice = threadIdx.x >> 6;
-  const int64_t i = (int64_t)blockIdx.x * 64 + col;
+  constexpr int S = 1024 / kFinishCols, U = 8;
+  __shared__ float lds[S][kFinishCols];
+  const int col = threadIdx.x % kFinishCols, slice = threadIdx.x / kFinishCols;
+  const int64_t i = (int64_t)blockIdx.x * kFinishCols + col;
   const bool beta = blockIdx.y == 1 || !dgamma;
   float* out = beta ? dbeta : dgamma;
   const float* src = part + (beta ? d : 0);
   float s = 0.0f;
-  if (i < d)
-    for (int p = slice; p < parts; p += 16) s += src[(int64_t)p * 2 * d + i];
+  if (i < d) {
+    for (int p0 = slice; p0 < parts; p0 += S * U) {
+      float f[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int p = p0 + u * S;
+        f[u] = p < parts ? src[(int64_t)p * 2 * d + i] : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) s += f[u];
+    }
+  }
   lds[slice][col] = s;
   __syncthreads();
-  if (slice || i >= d) return;
+  // the slices' sums: added by halves, in a fixed order
 #pragma unroll
-  for (int k = 1; k < 16; ++k) s += lds[k][col];
-  out[i] = s;
+  for (int half = S / 2; half >= 1; half /= 2) {
+    if (slice < half) lds[slice][col] += lds[slice + half][col];
+    __syncthreads();
+  }
+  if (slice == 0 && i < d) out[i] = lds[0][col];
 }
 
 // ------------------------------------------------- rows of any width
@@ -408,7 +426,6 @@ __global__ __launch_bounds__(256) void k_norm_wgrad_wide(NormBwdArgs a, int64_t 
 // ------------------------------------------------- launches
 constexpr int64_t kFwdHeld = 32768;   // widest row held in registers, forward
 constexpr int64_t kBwdHeld = 16384;   // backward: twice the arrays, and the sums
-constexpr int kBwdThreads = 1024;
 
 // Threads that hold a row of the backward: 8 values each (16 above 8192).
 static int bwd_row_threads(int64_t d) {
@@ -420,7 +437,10 @@ static int bwd_row_threads(int64_t d) {
 int norm_parts(int64_t rows, int64_t d) {
   if (d > kBwdHeld) return (int)std::min<int64_t>(rows, 64);
   const int64_t g = kBwdThreads / bwd_row_threads(d);
-  return (int)std::min<int64_t>((rows + g - 1) / g, 512);
+  const int64_t turns = (rows + g - 1) / g;   // rounds of g rows
+  // a partial costs 16 bytes a column (written and read, twice), a round 6 to
+  // 16 times g: at least four rounds each, once every compute unit has one
+  return (int)std::min<int64_t>(std::max<int64_t>(std::min<int64_t>(turns, 256), turns / 4), 512);
 }
 
 template <typename T, int ROW, int E, int THREADS>
@@ -490,7 +510,7 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t st) {
   }
   if (a.dgamma || a.dbeta) {
     const int parts = a.rows > 0 ? norm_parts(a.rows, a.d) : 0;
-    const dim3 grid((unsigned)((a.d + 63) / 64), a.dgamma && a.dbeta ? 2 : 1);
+    const dim3 grid((unsigned)((a.d + kFinishCols - 1) / kFinishCols), a.dgamma && a.dbeta ? 2 : 1);
     hipLaunchKernelGGL(k_norm_wgrad_finish, grid, dim3(1024), 0, st, a.part, parts, a.d, a.dgamma,
                        a.dbeta);
   }
