@@ -141,9 +141,14 @@ __device__ __forceinline__ void grad_terms(const RowGrad& r, int first, float* f
   }
 }
 
-// One vector of one row per thread, `chunks` workgroups a row; row r of the
-// launch is row last - r, so that the rows that a forward pass read last,
-// still cached, come first.
+// One vector of one row per thread, `chunks` workgroups a row.
+//
+// A forward pass has just read the same logits, and the last-level cache (256
+// MB) still holds what it read last: row r of the launch is row last - r, and
+// neither the gradient's stores nor this second and last read stay in the
+// caches, where they would drive out logits yet to be read.  Against plain
+// accesses: 129 to 97 us at 2048 x 32000 FP32 with a quarter of the rows
+// ignored, 943 to 880 us at 8349 x 131072 BF16 (893 us first row to last).
 template <typename T>
 __global__ __launch_bounds__(256) void k_dlogits(LogitsArgs l, const RowStat* stat,
                                                  const float* lse, const float* dlogp, T* dlogits,
@@ -174,7 +179,7 @@ __global__ __launch_bounds__(256) void k_dlogits(LogitsArgs l, const RowStat* st
     float f[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) f[j] = to_f32(e);
-    if (v < nvec) store_vec(out + (int64_t)v * N, pack<T>(f));
+    if (v < nvec) store_vec_once(out + (int64_t)v * N, pack<T>(f));
     else if (v - nvec < rest) out[(int64_t)nvec * N + (v - nvec)] = e;
     return;
   }
@@ -182,9 +187,9 @@ __global__ __launch_bounds__(256) void k_dlogits(LogitsArgs l, const RowStat* st
   const T* x = static_cast<const T*>(l.logits) + row * l.ld;
   if (v < nvec) {
     float f[N];
-    unpack<T>(load_vec(x + (int64_t)v * N), f);
+    unpack<T>(load_vec_once(x + (int64_t)v * N), f);
     grad_terms<N>(q, v * N, f);
-    store_vec(out + (int64_t)v * N, pack<T>(f));
+    store_vec_once(out + (int64_t)v * N, pack<T>(f));
   } else if (v - nvec < rest) {          // the last, partial vector: a thread per element
     const int i = nvec * N + (v - nvec);
     float f = to_f32(x[i]);
@@ -356,7 +361,7 @@ __device__ __forceinline__ void fill_row(T* out, int vocab, float value) {
   for (int j = 0; j < N; ++j) f[j] = value;
   const u32x4 v = pack<T>(f);
   const int nvec = vocab / N;
-  for (int i = threadIdx.x; i < nvec; i += THREADS) store_vec(out + (int64_t)i * N, v);
+  for (int i = threadIdx.x; i < nvec; i += THREADS) store_vec_once(out + (int64_t)i * N, v);
   const int i = nvec * N + (int)threadIdx.x;
   if (i < vocab) from_f32(value, out[i]);
 }
@@ -443,7 +448,7 @@ __global__ __launch_bounds__(THREADS, MIN_WAVES) void k_policy(LogitsArgs l, Pol
 #pragma unroll
       for (int j = 0; j < N; ++j) f[j] += v * N + j == (int)t ? g : 0.0f;
     }
-    if (v < nvec) store_vec(out + (int64_t)v * N, pack<T>(f));
+    if (v < nvec) store_vec_once(out + (int64_t)v * N, pack<T>(f));
   }
   if (last < vocab) from_f32(el * c + (last == (int)t ? g : 0.0f), out[last]);
 }
@@ -499,7 +504,7 @@ __global__ __launch_bounds__(THREADS) void k_policy_long(LogitsArgs l, PolicyArg
       float f[N];
       unpack<T>(d[i], f);
       grad_terms<N>(q, (v0 + i * THREADS) * N, f);
-      store_vec(out + (int64_t)(v0 + i * THREADS) * N, pack<T>(f));
+      store_vec_once(out + (int64_t)(v0 + i * THREADS) * N, pack<T>(f));
     }
   }
   const int i = nvec * N + (int)threadIdx.x;

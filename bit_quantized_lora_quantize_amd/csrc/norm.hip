@@ -55,15 +55,21 @@ struct Part {
   __device__ __forceinline__ int64_t at(int q) const { return (int64_t)(lane + q * ROW) * N; }
 };
 
-template <typename T, int ROW, int E>
+template <bool ONCE, typename T, int ROW, int E>
 __device__ __forceinline__ void load_part(const Part<T, ROW, E>& p, const T* x, u32x4* v, T& rest) {
 #pragma unroll
   for (int q = 0; q < Part<T, ROW, E>::V; ++q) {
     v[q] = u32x4{0, 0, 0, 0};
-    if (p.has(q)) v[q] = load_vec(x + p.at(q));
+    if (p.has(q)) v[q] = ONCE ? load_vec_once(x + p.at(q)) : load_vec(x + p.at(q));
   }
   rest = T(0);
   if (p.rest >= 0) rest = x[p.rest];
+}
+
+template <bool ONCE, typename T>
+__device__ __forceinline__ void put_vec(T* p, u32x4 v) {
+  if constexpr (ONCE) store_vec_once(p, v);
+  else store_vec(p, v);
 }
 
 // The weights of a thread's part (0 past the row's end).
@@ -82,20 +88,26 @@ __device__ __forceinline__ void weight_part(const Part<T, ROW, E>& p, const void
 
 // Sums over the ROW threads of each row of a workgroup; the rows of a
 // workgroup go through it together.
-template <int ROW, int THREADS>
-__device__ __forceinline__ float row_sum(float v, float* lds) {
-  v = wave_sum(v);
+template <int ROW, int THREADS, int COUNT>
+__device__ __forceinline__ void row_sums(float (&v)[COUNT], float (*lds)[COUNT]) {
+#pragma unroll
+  for (int c = 0; c < COUNT; ++c) v[c] = wave_sum(v[c]);
   if constexpr (ROW > 64) {
     constexpr int W = ROW / 64;
     const int wave = threadIdx.x / 64;
-    if ((threadIdx.x & 63) == 0) lds[wave] = v;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int c = 0; c < COUNT; ++c) lds[wave][c] = v[c];
+    }
     __syncthreads();
-    v = 0.0f;
     const int first = wave / W * W;
 #pragma unroll
-    for (int w = 0; w < W; ++w) v += lds[first + w];
+    for (int c = 0; c < COUNT; ++c) {
+      v[c] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) v[c] += lds[first + w][c];
+    }
   }
-  return v;
 }
 
 // The sums of a workgroup's row groups, added in order, as one row of d
@@ -133,13 +145,18 @@ __device__ __forceinline__ void write_partial(const Part<T, ROW, E>& p, int grou
 
 constexpr int kBwdThreads = 1024;
 constexpr int kFinishCols = 16;
+// Arrays of this size and more go past the caches' retention: the two to four
+// of a call would drive each other out of the 256 MB of the last level anyway.
+// Backward of 16384 x 8192 BF16: 199 us kept, 187 us past; smaller outputs stay
+// for the layer that reads them next.
+constexpr int64_t kOnceBytes = int64_t(128) << 20;
 
 }  // namespace
 
 // THREADS / ROW rows per workgroup, each by ROW of its threads.
-template <typename T, int ROW, int E, int THREADS>
+template <typename T, int ROW, int E, int THREADS, bool ONCE>
 __global__ __launch_bounds__(THREADS) void k_norm_fwd(NormFwdArgs a) {
-  __shared__ float lds[2][THREADS / 64];
+  __shared__ float lds[2][THREADS / 64][1];
   const int64_t row = (int64_t)blockIdx.x * (THREADS / ROW) + threadIdx.x / ROW;
   const bool live = row < a.rows;
   const int64_t base = (live ? row : a.rows - 1) * a.d;
@@ -147,12 +164,12 @@ __global__ __launch_bounds__(THREADS) void k_norm_fwd(NormFwdArgs a) {
   constexpr int N = Part<T, ROW, E>::N, V = Part<T, ROW, E>::V;
   u32x4 v[V];
   T rest;
-  load_part(p, static_cast<const T*>(a.x) + base, v, rest);
+  load_part<ONCE>(p, static_cast<const T*>(a.x) + base, v, rest);
   float h[E], hr;
   if (a.r) {
     u32x4 w[V];
     T rr;
-    load_part(p, static_cast<const T*>(a.r) + base, w, rr);
+    load_part<ONCE>(p, static_cast<const T*>(a.r) + base, w, rr);
     T* out = static_cast<T*>(a.h) + base;
     float f[N];
 #pragma unroll
@@ -162,7 +179,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_fwd(NormFwdArgs a) {
 #pragma unroll
       for (int j = 0; j < N; ++j) f[j] += h[q * N + j];
       v[q] = pack<T>(f);                       // the one rounding of H
-      if (live && p.has(q)) store_vec(out + p.at(q), v[q]);
+      if (live && p.has(q)) put_vec<ONCE>(out + p.at(q), v[q]);
     }
     from_f32(to_f32(rest) + to_f32(rr), rest);
     if (live && p.rest >= 0) out[p.rest] = rest;
@@ -181,23 +198,25 @@ __global__ __launch_bounds__(THREADS) void k_norm_fwd(NormFwdArgs a) {
   const float inv = 1.0f / (float)a.d;
   float mean = 0.0f;
   if (a.kind == QLORA_NORM_LAYER) {
-    float s = hr;                              // 0 in threads without a rest
+    float s[1] = {hr};                         // 0 in threads without a rest
 #pragma unroll
-    for (int j = 0; j < E; ++j) s += h[j];
-    mean = row_sum<ROW, THREADS>(s, lds[0]) * inv;
+    for (int j = 0; j < E; ++j) s[0] += h[j];
+    row_sums<ROW, THREADS>(s, lds[0]);
+    mean = s[0] * inv;
     hr -= mean;
 #pragma unroll
     for (int j = 0; j < E; ++j) h[j] -= mean;
   }
-  float s = p.rest >= 0 ? hr * hr : 0.0f;
+  float s[1] = {p.rest >= 0 ? hr * hr : 0.0f};
 #pragma unroll
   for (int q = 0; q < V; ++q) {
     float t = 0.0f;
 #pragma unroll
     for (int j = 0; j < N; ++j) t += h[q * N + j] * h[q * N + j];
-    if (p.has(q)) s += t;
+    if (p.has(q)) s[0] += t;
   }
-  const float rstd = 1.0f / sqrtf(row_sum<ROW, THREADS>(s, lds[1]) * inv + a.eps);
+  row_sums<ROW, THREADS>(s, lds[1]);
+  const float rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
   if (!live) return;
   T* y = static_cast<T*>(a.y) + base;
 #pragma unroll
@@ -207,7 +226,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_fwd(NormFwdArgs a) {
       const int e = q * N + j;
       h[e] = h[e] * rstd * g[e] + b[e];
     }
-    if (p.has(q)) store_vec(y + p.at(q), pack<T>(h + q * N));
+    if (p.has(q)) put_vec<ONCE>(y + p.at(q), pack<T>(h + q * N));
   }
   if (p.rest >= 0) from_f32(hr * rstd * gr + br, y[p.rest]);
   if (p.lane == 0) {
@@ -220,10 +239,10 @@ __global__ __launch_bounds__(THREADS) void k_norm_fwd(NormFwdArgs a) {
 // that a workgroup takes: G = THREADS / ROW at a time, each by ROW threads
 // that keep the sums of their own columns in registers; at the end the G
 // sums of a column are added in order and written as one partial.
-template <typename T, int ROW, int E, int THREADS, bool WEIGHTS>
+template <typename T, int ROW, int E, int THREADS, bool WEIGHTS, bool ONCE>
 __global__ __launch_bounds__(THREADS) void k_norm_bwd(NormBwdArgs a, int parts) {
   constexpr int N = Part<T, ROW, E>::N, V = Part<T, ROW, E>::V, G = THREADS / ROW;
-  __shared__ float lds[2][2][THREADS / 64];
+  __shared__ float lds[2][THREADS / 64][2];
   const Part<T, ROW, E> p(threadIdx.x % ROW, (int)a.d);
   const int group = threadIdx.x / ROW;
   const bool layer = a.kind == QLORA_NORM_LAYER;
@@ -244,10 +263,10 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(NormBwdArgs a, int parts) 
     const float rstd = a.rstd[live ? row : a.rows - 1];
     u32x4 vy[V], vh[V], vd[V];
     T ry, rh, rd = T(0);
-    load_part(p, static_cast<const T*>(a.dy) + base, vy, ry);
-    load_part(p, static_cast<const T*>(a.h) + base, vh, rh);
-    if (a.dh) load_part(p, static_cast<const T*>(a.dh) + base, vd, rd);
-    float su = 0.0f, sn = 0.0f;
+    load_part<ONCE>(p, static_cast<const T*>(a.dy) + base, vy, ry);
+    load_part<ONCE>(p, static_cast<const T*>(a.h) + base, vh, rh);
+    if (a.dh) load_part<ONCE>(p, static_cast<const T*>(a.dh) + base, vd, rd);
+    float s[2] = {0.0f, 0.0f};                 // sum(u), sum(u n)
     float y[N], n[N];
 #pragma unroll
     for (int q = 0; q < V; ++q) {
@@ -262,8 +281,8 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(NormBwdArgs a, int parts) 
           db[e] += live ? y[j] : 0.0f;
         }
         const float u = y[j] * g[e];           // 0 past the row's end
-        su += u;
-        sn += u * n[j];
+        s[0] += u;
+        s[1] += u * n[j];
       }
     }
     const float yr = to_f32(ry), nr = (to_f32(rh) - mean) * rstd, ur = yr * gr;
@@ -271,8 +290,10 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(NormBwdArgs a, int parts) 
       dgr += live ? yr * nr : 0.0f;
       dbr += live ? yr : 0.0f;
     }
-    const float mu = layer ? row_sum<ROW, THREADS>(su + ur, lds[turn][0]) * inv : 0.0f;
-    const float mn = row_sum<ROW, THREADS>(sn + ur * nr, lds[turn][1]) * inv;
+    s[0] += ur;
+    s[1] += ur * nr;
+    row_sums<ROW, THREADS>(s, lds[turn]);
+    const float mu = layer ? s[0] * inv : 0.0f, mn = s[1] * inv;
     if (live) {
       T* dx = static_cast<T*>(a.dx) + base;
 #pragma unroll
@@ -287,7 +308,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(NormBwdArgs a, int parts) 
 #pragma unroll
           for (int j = 0; j < N; ++j) y[j] += n[j];
         }
-        if (p.has(q)) store_vec(dx + p.at(q), pack<T>(y));
+        if (p.has(q)) put_vec<ONCE>(dx + p.at(q), pack<T>(y));
       }
       if (p.rest >= 0) from_f32((ur - mu - nr * mn) * rstd + to_f32(rd), dx[p.rest]);
     }
@@ -438,16 +459,18 @@ int norm_parts(int64_t rows, int64_t d) {
   if (d > kBwdHeld) return (int)std::min<int64_t>(rows, 64);
   const int64_t g = kBwdThreads / bwd_row_threads(d);
   const int64_t turns = (rows + g - 1) / g;   // rounds of g rows
-  // a partial costs 16 bytes a column (written and read, twice), a round 6 to
-  // 16 times g: at least four rounds each, once every compute unit has one
-  return (int)std::min<int64_t>(std::max<int64_t>(std::min<int64_t>(turns, 256), turns / 4), 512);
+  // one workgroup on each of the 256 compute units at most (the
+  // registers allow no second one)
+  return (int)std::min<int64_t>(turns, 256);
 }
 
 template <typename T, int ROW, int E, int THREADS>
 static void run_fwd(const NormFwdArgs& a, hipStream_t st) {
   constexpr int64_t g = THREADS / ROW;
-  hipLaunchKernelGGL((k_norm_fwd<T, ROW, E, THREADS>), dim3((unsigned)((a.rows + g - 1) / g)),
-                     dim3(THREADS), 0, st, a);
+  const dim3 grid((unsigned)((a.rows + g - 1) / g));
+  if (a.rows * a.d * (int64_t)sizeof(T) < kOnceBytes)
+    hipLaunchKernelGGL((k_norm_fwd<T, ROW, E, THREADS, false>), grid, dim3(THREADS), 0, st, a);
+  else hipLaunchKernelGGL((k_norm_fwd<T, ROW, E, THREADS, true>), grid, dim3(THREADS), 0, st, a);
 }
 
 template <typename T>
@@ -469,18 +492,24 @@ hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <typename T, int ROW, int E>
-static void run_bwd(const NormBwdArgs& a, hipStream_t st) {
+template <typename T, int ROW, int E, bool ONCE>
+static void run_bwd_as(const NormBwdArgs& a, hipStream_t st) {
   constexpr int64_t g = kBwdThreads / ROW;
   if (a.dgamma || a.dbeta) {
     const int parts = norm_parts(a.rows, a.d);
-    hipLaunchKernelGGL((k_norm_bwd<T, ROW, E, kBwdThreads, true>), dim3((unsigned)parts),
+    hipLaunchKernelGGL((k_norm_bwd<T, ROW, E, kBwdThreads, true, ONCE>), dim3((unsigned)parts),
                        dim3(kBwdThreads), 0, st, a, parts);
   } else {
     const int grid = (int)((a.rows + g - 1) / g);
-    hipLaunchKernelGGL((k_norm_bwd<T, ROW, E, kBwdThreads, false>), dim3((unsigned)grid),
+    hipLaunchKernelGGL((k_norm_bwd<T, ROW, E, kBwdThreads, false, ONCE>), dim3((unsigned)grid),
                        dim3(kBwdThreads), 0, st, a, grid);
   }
+}
+
+template <typename T, int ROW, int E>
+static void run_bwd(const NormBwdArgs& a, hipStream_t st) {
+  if (a.rows * a.d * (int64_t)sizeof(T) < kOnceBytes) run_bwd_as<T, ROW, E, false>(a, st);
+  else run_bwd_as<T, ROW, E, true>(a, st);
 }
 
 template <typename T>

@@ -44,6 +44,16 @@ template <typename T>
 __device__ __forceinline__ void store_vec(T* p, u32x4 v) {
   *reinterpret_cast<typename VecAt<T>::type*>(p) = v;
 }
+// The same past the caches' retention, for data that no kernel here reads
+// again.
+template <typename T>
+__device__ __forceinline__ u32x4 load_vec_once(const T* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const typename VecAt<T>::type*>(p));
+}
+template <typename T>
+__device__ __forceinline__ void store_vec_once(T* p, u32x4 v) {
+  __builtin_nontemporal_store(v, reinterpret_cast<typename VecAt<T>::type*>(p));
+}
 
 template <typename T>
 __device__ __forceinline__ void unpack(u32x4 v, float* f) {
@@ -78,16 +88,47 @@ __device__ __forceinline__ u32x4 vec_neg_inf() {
   return u32x4{w, w, w, w};
 }
 
-// Sum over a wavefront; every lane gets it.
+// Values moved between the lanes of a wavefront inside the VALU (data-parallel
+// primitives): lane i takes lane i - 1, 2, 4 or 8 of its row of 16, then rows
+// 1 and 3 take lane 15 of the row before them and rows 2 and 3 lane 31.  Lanes
+// without a source take `none`.  After the six steps lane 63 has combined all.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float lane_move(float none, float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(none), __float_as_int(v), CTRL,
+                                                    ROWS, 0xF, false));
+}
+constexpr int kRowShr1 = 0x111, kRowShr2 = 0x112, kRowShr4 = 0x114, kRowShr8 = 0x118;
+constexpr int kRowBcast15 = 0x142, kRowBcast31 = 0x143;
+
+__device__ __forceinline__ float last_lane(float v) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// Sum over a wavefront, all of whose lanes are active; every lane gets it.
+__device__ __forceinline__ float wave_sum(float v) {
+  v += lane_move<kRowShr1, 0xF>(0.0f, v);
+  v += lane_move<kRowShr2, 0xF>(0.0f, v);
+  v += lane_move<kRowShr4, 0xF>(0.0f, v);
+  v += lane_move<kRowShr8, 0xF>(0.0f, v);
+  v += lane_move<kRowBcast15, 0xA>(0.0f, v);
+  v += lane_move<kRowBcast31, 0xC>(0.0f, v);
+  return last_lane(v);
+}
+__device__ __forceinline__ float wave_max(float v) {
+  const float none = -__builtin_huge_valf();
+  v = fmaxf(v, lane_move<kRowShr1, 0xF>(none, v));
+  v = fmaxf(v, lane_move<kRowShr2, 0xF>(none, v));
+  v = fmaxf(v, lane_move<kRowShr4, 0xF>(none, v));
+  v = fmaxf(v, lane_move<kRowShr8, 0xF>(none, v));
+  v = fmaxf(v, lane_move<kRowBcast15, 0xA>(none, v));
+  v = fmaxf(v, lane_move<kRowBcast31, 0xC>(none, v));
+  return last_lane(v);
+}
+// Other types.
 template <typename V>
 __device__ __forceinline__ V wave_sum(V v) {
 #pragma unroll
   for (int half = 32; half >= 1; half >>= 1) v += __shfl_xor(v, half, 64);
-  return v;
-}
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int half = 32; half >= 1; half >>= 1) v = fmaxf(v, __shfl_xor(v, half, 64));
   return v;
 }
 
