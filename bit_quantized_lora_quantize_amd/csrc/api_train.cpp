@@ -208,20 +208,13 @@ int qlora_preference_loss(const qlora_logits_t* l, const int64_t* offsets, int64
     return QLORA_ERR_ALIGN;
   const PreferencePlan p = plan_preference(l->rows, workspace);
   if (l->rows > 0 && workspace_bytes < p.bytes) return QLORA_ERR_WORKSPACE;
-  const hipStream_t st = static_cast<hipStream_t>(stream);
-  const LogitsArgs la = logits_args(l);
-  if (l->rows > 0) {
-    s = hip_status(launch_logp(la, logp, nullptr, dlogits ? p.stat : nullptr, st));
-    if (s) return s;
-  }
   const bool grad = dlogits && l->rows > 0;
   const PreferenceArgs a{l->targets, offsets,   logp,  ref_logp,  l->rows,
                          pairs,      l->ignore_index,  par->kind, par->length_normalize,
                          par->beta,  par->label_smoothing, par->margin, par->weight,
                          seq_logp,   loss,      grad ? p.dlogp : nullptr};
-  s = hip_status(launch_preference(a, st));
-  if (s || !grad) return s;
-  return hip_status(launch_dlogits(la, p.stat, nullptr, p.dlogp, dlogits, ldd, st));
+  return hip_status(launch_preference(logits_args(l), a, p.stat, logp, grad ? dlogits : nullptr,
+                                      ldd, static_cast<hipStream_t>(stream)));
 }
 
 size_t qlora_policy_workspace_bytes(int64_t rows, int64_t sequences) {

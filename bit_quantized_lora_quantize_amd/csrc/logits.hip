@@ -53,11 +53,11 @@ __device__ __forceinline__ MaxSum block_join(MaxSum v, float k, MaxSum* lds) {
 // vectors are loaded together, their maximum joins the running one and the
 // running sum is rescaled once.  Empty threads hold m = -inf, s = 0.
 template <typename T, int THREADS>
-__device__ __forceinline__ MaxSum stream_row(const T* x, int vocab, float k) {
+__device__ __forceinline__ MaxSum stream_row(const T* x, int vocab, float k, int lane) {
   constexpr int N = kVec<T>, kU = 32 / N;
   const int nvec = vocab / N;
   MaxSum r{-kInf, 0.0f};
-  for (int v0 = threadIdx.x; v0 < nvec; v0 += THREADS * kU) {
+  for (int v0 = lane; v0 < nvec; v0 += THREADS * kU) {
     u32x4 d[kU];
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
@@ -82,7 +82,7 @@ __device__ __forceinline__ MaxSum stream_row(const T* x, int vocab, float k) {
     }
     r = {m, s};
   }
-  const int i = nvec * N + (int)threadIdx.x;   // the last, partial vector
+  const int i = nvec * N + lane;   // the last, partial vector
   if (i < vocab) {
     const float f = to_f32(x[i]), m = fmaxf(r.m, f), z = shift(m);
     r = {m, r.s * term(r.m, z, k) + term(f, z, k)};
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(THREADS) void k_logp(LogitsArgs l, float* logp, flo
   }
   const T* x = static_cast<const T*>(l.logits) + row * l.ld;
   const float k = l.scale * kLog2e, xt = to_f32(x[t]);
-  const MaxSum v = block_join<THREADS>(stream_row<T, THREADS>(x, (int)l.vocab, k), k, lds);
+  const MaxSum v = block_join<THREADS>(stream_row<T, THREADS>(x, (int)l.vocab, k, threadIdx.x), k, lds);
   if (threadIdx.x == 0) {
     const float m = shift(v.m), ls = logf(v.s);
     logp[row] = (xt - m) * l.scale - ls;
@@ -138,6 +138,49 @@ __device__ __forceinline__ void grad_terms(const RowGrad& r, int first, float* f
   if ((uint32_t)(r.t - first) < (uint32_t)N) {
 #pragma unroll
     for (int j = 0; j < N; ++j) f[j] += first + j == r.t ? r.g : 0.0f;
+  }
+}
+
+// A row's gradient where no logit is read, by THREADS threads: zeros, or NaN
+// for a bad target.
+template <typename T, int THREADS>
+__device__ __forceinline__ void fill_row(T* out, int vocab, float value, int lane) {
+  constexpr int N = kVec<T>;
+  float f[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) f[j] = value;
+  const u32x4 v = pack<T>(f);
+  const int nvec = vocab / N;
+  for (int i = lane; i < nvec; i += THREADS) store_vec_once(out + (int64_t)i * N, v);
+  const int i = nvec * N + lane;
+  if (i < vocab) from_f32(value, out[i]);
+}
+
+// A row's gradient by THREADS threads, from its logits read again.
+template <typename T, int THREADS>
+__device__ __forceinline__ void grad_row(const T* x, T* out, int vocab, const RowGrad& q,
+                                         int lane) {
+  constexpr int N = kVec<T>, kU = 2;
+  const int nvec = vocab / N;
+  for (int v0 = lane; v0 < nvec; v0 += THREADS * kU) {
+    u32x4 d[kU];
+#pragma unroll
+    for (int i = 0; i < kU; ++i)
+      if (v0 + i * THREADS < nvec) d[i] = load_vec(x + (int64_t)(v0 + i * THREADS) * N);
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      if (v0 + i * THREADS >= nvec) continue;
+      float f[N];
+      unpack<T>(d[i], f);
+      grad_terms<N>(q, (v0 + i * THREADS) * N, f);
+      store_vec_once(out + (int64_t)(v0 + i * THREADS) * N, pack<T>(f));
+    }
+  }
+  const int i = nvec * N + lane;
+  if (i < vocab) {
+    float f = to_f32(x[i]);
+    grad_terms<1>(q, i, &f);
+    from_f32(f, out[i]);
   }
 }
 
@@ -198,31 +241,20 @@ __global__ __launch_bounds__(256) void k_dlogits(LogitsArgs l, const RowStat* st
   }
 }
 
-// One workgroup per pair, half of it per sequence: the sequences' sums in
-// FP64, the loss and its slope, the gradient of every log-probability (also of
-// rows that do not count: their logits' gradient is 0 whatever it is).  The
-// first and the last workgroup clear the rows before and after all sequences.
-__global__ __launch_bounds__(kPrefThreads) void k_preference(PreferenceArgs a) {
+// Sums, loss and slope of one pair, half of a workgroup per sequence: the
+// sequences' sums in FP64.  Returns the gradient of a log-probability of each
+// of the two sequences, to every thread.
+struct PairSlope {
+  float c[2];
+};
+__device__ __forceinline__ PairSlope pair_loss(const PreferenceArgs& a, int64_t p,
+                                               double (*lds)[kPrefThreads / 64]) {
   constexpr int kSide = kPrefThreads / 2, W = kSide / 64;
-  __shared__ double lds[3][2 * W];
-  const int64_t p = blockIdx.x;
-  if (a.dlogp) {
-    int64_t b0 = 0, e1 = 0, skip;
-    if (a.pairs > 0) {
-      seq_rows(a.offsets, 0, a.rows, b0, skip);
-      seq_rows(a.offsets, 2 * a.pairs - 1, a.rows, skip, e1);
-    }
-    if (p == 0)
-      for (int64_t i = threadIdx.x; i < b0; i += kPrefThreads) a.dlogp[i] = 0.0f;
-    if (p == gridDim.x - 1)
-      for (int64_t i = e1 + threadIdx.x; i < a.rows; i += kPrefThreads) a.dlogp[i] = 0.0f;
-  }
-  if (a.pairs == 0) return;
-  const int side = threadIdx.x / kSide, lane = threadIdx.x % kSide;
+  const int side = threadIdx.x / kSide;
   int64_t b, e;
   seq_rows(a.offsets, p + side * a.pairs, a.rows, b, e);
   double vs = 0.0, vg = 0.0, vn = 0.0;
-  for (int64_t i = b + lane; i < e; i += kSide) {
+  for (int64_t i = b + threadIdx.x % kSide; i < e; i += kSide) {
     const float lp = a.logp[i], rf = a.ref ? a.ref[i] : 0.0f;
     if (a.targets[i] == a.ignore) continue;
     vs += (double)lp;
@@ -277,25 +309,139 @@ __global__ __launch_bounds__(kPrefThreads) void k_preference(PreferenceArgs a) {
     a.seq_logp[p] = (float)s[0];
     a.seq_logp[p + a.pairs] = (float)s[1];
   }
+  PairSlope r{{slope * a.weight, -slope * a.weight}};
+  if (a.length_normalize) {
+    r.c[0] /= (float)n[0];
+    r.c[1] /= (float)n[1];
+  }
+  return r;
+}
+
+// The rows before and after all sequences, [0, begin) and [end, rows).
+struct Outside {
+  int64_t begin, end;
+};
+__device__ __forceinline__ Outside outside_rows(const int64_t* offsets, int64_t seqs,
+                                                int64_t rows) {
+  Outside o{0, 0};
+  int64_t skip;
+  if (seqs > 0) {
+    seq_rows(offsets, 0, rows, o.begin, skip);
+    seq_rows(offsets, seqs - 1, rows, skip, o.end);
+  }
+  return o;
+}
+
+// One workgroup per pair: its loss, and the gradient of every log-probability
+// (also of rows that do not count: their logits' gradient is 0 whatever it
+// is).  The first and the last workgroup clear the rows outside.
+__global__ __launch_bounds__(kPrefThreads) void k_preference(PreferenceArgs a) {
+  __shared__ double lds[3][kPrefThreads / 64];
+  const int64_t p = blockIdx.x;
+  if (a.dlogp) {
+    const Outside o = outside_rows(a.offsets, 2 * a.pairs, a.rows);
+    if (p == 0)
+      for (int64_t i = threadIdx.x; i < o.begin; i += kPrefThreads) a.dlogp[i] = 0.0f;
+    if (p == gridDim.x - 1)
+      for (int64_t i = o.end + threadIdx.x; i < a.rows; i += kPrefThreads) a.dlogp[i] = 0.0f;
+  }
+  if (a.pairs == 0) return;
+  const PairSlope s = pair_loss(a, p, lds);
   if (!a.dlogp) return;
-  float c = (side ? -slope : slope) * a.weight;
-  if (a.length_normalize) c /= (float)n[side];
-  for (int64_t i = b + lane; i < e; i += kSide) a.dlogp[i] = c;
+  constexpr int kSide = kPrefThreads / 2;
+  const int side = threadIdx.x / kSide;
+  int64_t b, e;
+  seq_rows(a.offsets, p + side * a.pairs, a.rows, b, e);
+  const float c = side ? s.c[1] : s.c[0];
+  for (int64_t i = b + threadIdx.x % kSide; i < e; i += kSide) a.dlogp[i] = c;
+}
+
+// Log-probability of one row by one wavefront.
+template <typename T>
+__device__ __forceinline__ void wave_logp(const LogitsArgs& l, int64_t row, float* logp,
+                                          RowStat* stat) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = l.targets[row];
+  float lp = t == l.ignore ? 0.0f : __builtin_nanf("");
+  RowStat q{lp, lp};
+  if (t != l.ignore && t >= 0 && t < l.vocab) {
+    const T* x = static_cast<const T*>(l.logits) + row * l.ld;
+    const float k = l.scale * kLog2e;
+    const MaxSum v = block_join<64>(stream_row<T, 64>(x, (int)l.vocab, k, lane), k, nullptr);
+    q = {shift(v.m), logf(v.s)};
+    lp = (to_f32(x[t]) - q.max) * l.scale - q.logsum;
+  }
+  if (lane == 0) {
+    logp[row] = lp;
+    stat[row] = q;
+  }
+}
+
+// Gradient of one row by one wavefront.
+template <typename T>
+__device__ __forceinline__ void wave_grad(const LogitsArgs& l, int64_t row, RowStat s, float dlogp,
+                                          T* dlogits, int64_t ldd) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = l.targets[row];
+  const float g = dlogp * l.scale;
+  T* out = dlogits + row * ldd;
+  const bool none = t == l.ignore || g == 0.0f;
+  if (none || t < 0 || t >= l.vocab) {
+    fill_row<T, 64>(out, (int)l.vocab, none ? 0.0f : __builtin_nanf(""), lane);
+    return;
+  }
+  const RowGrad q{g, s.max, s.logsum * kLog2e, l.scale * kLog2e, (int)t};
+  grad_row<T, 64>(static_cast<const T*>(l.logits) + row * l.ld, out, (int)l.vocab, q, lane);
+}
+
+// A small batch in one launch: a workgroup per pair, a wavefront per row.  The
+// rows' results pass between the wavefronts through memory, at the barriers.
+template <typename T>
+__global__ __launch_bounds__(kPrefThreads) void k_preference_small(LogitsArgs l, PreferenceArgs a,
+                                                                   RowStat* stat, float* logp,
+                                                                   T* dlogits, int64_t ldd) {
+  constexpr int W = kPrefThreads / 64;
+  __shared__ double lds[3][W];
+  const int64_t p = blockIdx.x;
+  const int wave = threadIdx.x / 64;
+  const Outside o = outside_rows(a.offsets, 2 * a.pairs, a.rows);
+  if (p == 0) {
+    for (int64_t row = wave; row < o.begin; row += W) {
+      wave_logp<T>(l, row, logp, stat);
+      if (dlogits) wave_grad<T>(l, row, RowStat{0.0f, 0.0f}, 0.0f, dlogits, ldd);
+    }
+  }
+  if (p == gridDim.x - 1) {
+    for (int64_t row = o.end + wave; row < a.rows; row += W) {
+      wave_logp<T>(l, row, logp, stat);
+      if (dlogits) wave_grad<T>(l, row, RowStat{0.0f, 0.0f}, 0.0f, dlogits, ldd);
+    }
+  }
+  if (a.pairs == 0) return;
+  int64_t b[2], e[2];
+  seq_rows(a.offsets, p, a.rows, b[0], e[0]);
+  seq_rows(a.offsets, p + a.pairs, a.rows, b[1], e[1]);
+  const int64_t first = e[0] - b[0], n = first + e[1] - b[1];
+  for (int64_t i = wave; i < n; i += W)
+    wave_logp<T>(l, i < first ? b[0] + i : b[1] + (i - first), logp, stat);
+  __syncthreads();
+  const PairSlope s = pair_loss(a, p, lds);
+  if (!dlogits) return;
+  for (int64_t i = wave; i < n; i += W) {
+    const int64_t row = i < first ? b[0] + i : b[1] + (i - first);
+    wave_grad<T>(l, row, stat[row], i < first ? s.c[0] : s.c[1], dlogits, ldd);
+  }
 }
 
 // One workgroup per sequence: the rows that count, and each row's sequence.
 __global__ __launch_bounds__(256) void k_policy_count(LogitsArgs l, PolicyArgs a) {
   __shared__ int lds[4];
   const int64_t s = blockIdx.x;
-  int64_t b0 = 0, e1 = 0, skip;
-  if (a.seqs > 0) {
-    seq_rows(a.offsets, 0, l.rows, b0, skip);
-    seq_rows(a.offsets, a.seqs - 1, l.rows, skip, e1);
-  }
+  const Outside o = outside_rows(a.offsets, a.seqs, l.rows);
   if (s == 0)
-    for (int64_t i = threadIdx.x; i < b0; i += 256) a.row_seq[i] = -1;
+    for (int64_t i = threadIdx.x; i < o.begin; i += 256) a.row_seq[i] = -1;
   if (s == gridDim.x - 1)
-    for (int64_t i = e1 + threadIdx.x; i < l.rows; i += 256) a.row_seq[i] = -1;
+    for (int64_t i = o.end + threadIdx.x; i < l.rows; i += 256) a.row_seq[i] = -1;
   if (a.seqs == 0) return;
   int64_t b, e;
   seq_rows(a.offsets, s, l.rows, b, e);
@@ -332,38 +478,58 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& a, int64_t row
     dkl = -em;
   }
   o.terms = {w, clipped ? held : free, kl, clipped ? 1.0f : 0.0f};
-  o.dlogp = a.weight * w * ((clipped ? 0.0f : free) + a.kl_coef * dkl);
+  o.dlogp = a.weight * w * ((clipped ? 0.0f : free) + (a.kl_coef > 0.0f ? a.kl_coef * dkl : 0.0f));
   return o;
 }
 
-// Weight of a row of sequence s; `total` counts the rows of all sequences.
-__device__ __forceinline__ float policy_weight(const PolicyArgs& a, int s, float total) {
-  if (s < 0) return 0.0f;
-  return a.reduction == QLORA_POLICY_TOKEN_MEAN ? 1.0f / total
-                                                : 1.0f / ((float)a.seqs * (float)a.count[s]);
-}
-
-// Sum of the sequences' counts for the mean over tokens, by one wavefront
-// (every lane gets it).
-__device__ __forceinline__ float policy_total(const PolicyArgs& a) {
-  if (a.reduction != QLORA_POLICY_TOKEN_MEAN) return 0.0f;
-  int n = 0;
-  for (int64_t i = threadIdx.x & 63; i < a.seqs; i += 64) n += a.count[i];
-  return (float)wave_sum(n);
-}
-
-// A row's gradient where no logit is read: zeros, or NaN for a bad target.
-template <typename T, int THREADS>
-__device__ __forceinline__ void fill_row(T* out, int vocab, float value) {
-  constexpr int N = kVec<T>;
-  float f[N];
+// The sequence that a row counts in (-1: in none) and its weight, by a full
+// wavefront: from k_policy_count's results, or where that did not run (row_seq
+// NULL) from the offsets and targets themselves.
+struct Place {
+  int seq;
+  float w;
+};
+__device__ __forceinline__ Place policy_place(const LogitsArgs& l, const PolicyArgs& a,
+                                              int64_t row) {
+  const int lane = threadIdx.x & 63;
+  const bool token_mean = a.reduction == QLORA_POLICY_TOKEN_MEAN;
+  int seq, n = 0;
+  if (a.row_seq) {
+    seq = a.row_seq[row];
+    if (seq < 0) return {-1, 0.0f};
+    if (token_mean) {
+      for (int64_t i = lane; i < a.seqs; i += 64) n += a.count[i];
+      n = wave_sum(n);
+    } else {
+      n = a.count[seq];
+    }
+  } else {
+    if (l.targets[row] == l.ignore) return {-1, 0.0f};
+    int at = 0;   // offsets at or before the row
+    for (int64_t j = 0; j <= a.seqs; j += 64) {
+      const bool before = j + lane <= a.seqs && a.offsets[j + lane] <= row;
+      at += __popcll(__ballot(before));
+    }
+    seq = at - 1;
+    if (seq < 0 || seq >= a.seqs) return {-1, 0.0f};
+    int64_t b, e;
+    seq_rows(a.offsets, seq, l.rows, b, e);
+    if (row < b || row >= e) return {-1, 0.0f};
+    if (token_mean) {
+      const Outside o = outside_rows(a.offsets, a.seqs, l.rows);
+      b = o.begin;
+      e = o.end;
+    }
+    for (int64_t i = b + lane; i < e; i += 64 * 8) {
+      int64_t t[8];   // loaded together
 #pragma unroll
-  for (int j = 0; j < N; ++j) f[j] = value;
-  const u32x4 v = pack<T>(f);
-  const int nvec = vocab / N;
-  for (int i = threadIdx.x; i < nvec; i += THREADS) store_vec_once(out + (int64_t)i * N, v);
-  const int i = nvec * N + (int)threadIdx.x;
-  if (i < vocab) from_f32(value, out[i]);
+      for (int u = 0; u < 8; ++u) t[u] = i + 64 * u < e ? l.targets[i + 64 * u] : l.ignore;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) n += t[u] != l.ignore ? 1 : 0;
+    }
+    n = wave_sum(n);
+  }
+  return {seq, token_mean ? 1.0f / (float)n : 1.0f / ((float)a.seqs * (float)n)};
 }
 
 // Loss and gradient of one row in one pass: the row's logits stay in
@@ -378,19 +544,18 @@ __global__ __launch_bounds__(THREADS, MIN_WAVES) void k_policy(LogitsArgs l, Pol
   const int64_t row = blockIdx.x;
   const int vocab = (int)l.vocab, nvec = vocab / N;
   const int64_t t = l.targets[row];
-  const int seq = a.row_seq[row];
   T* out = dlogits ? dlogits + row * ldd : nullptr;
   const bool lead = threadIdx.x < 64;
   if (t == l.ignore || t < 0 || t >= l.vocab) {
     const float lp = t == l.ignore ? 0.0f : __builtin_nanf("");
     if (lead) {
-      const float total = policy_total(a);
+      const Place at = policy_place(l, a, row);
       if (threadIdx.x == 0) {
         a.logp[row] = lp;
-        a.terms[row] = policy_row(a, row, seq, policy_weight(a, seq, total), lp).terms;
+        a.terms[row] = policy_row(a, row, at.seq, at.w, lp).terms;
       }
     }
-    if (out) fill_row<T, THREADS>(out, vocab, seq < 0 ? 0.0f : lp);
+    if (out) fill_row<T, THREADS>(out, vocab, lp, threadIdx.x);
     return;
   }
   const T* x = static_cast<const T*>(l.logits) + row * l.ld;
@@ -404,6 +569,8 @@ __global__ __launch_bounds__(THREADS, MIN_WAVES) void k_policy(LogitsArgs l, Pol
   }
   const int last = nvec * N + (int)threadIdx.x;   // the last, partial vector
   float el = last < vocab ? to_f32(x[last]) : -kInf;
+  Place at{-1, 0.0f};
+  if (lead) at = policy_place(l, a, row);   // while the logits arrive
   float e[E], m = el;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -422,10 +589,9 @@ __global__ __launch_bounds__(THREADS, MIN_WAVES) void k_policy(LogitsArgs l, Pol
   }
   s = block_sum<THREADS>(s, lds_s);
   if (lead) {
-    const float total = policy_total(a);
     if (threadIdx.x == 0) {
       const float lp = (xt - m) * l.scale - logf(s);
-      const PolicyRow o = policy_row(a, row, seq, policy_weight(a, seq, total), lp);
+      const PolicyRow o = policy_row(a, row, at.seq, at.w, lp);
       a.logp[row] = lp;
       a.terms[row] = o.terms;
       lds_g = o.dlogp * l.scale;
@@ -435,7 +601,7 @@ __global__ __launch_bounds__(THREADS, MIN_WAVES) void k_policy(LogitsArgs l, Pol
   __syncthreads();
   const float g = lds_g, c = -g / s;
   if (g == 0.0f) {
-    fill_row<T, THREADS>(out, vocab, 0.0f);
+    fill_row<T, THREADS>(out, vocab, 0.0f, threadIdx.x);
     return;
   }
 #pragma unroll
@@ -458,63 +624,43 @@ __global__ __launch_bounds__(THREADS, MIN_WAVES) void k_policy(LogitsArgs l, Pol
 template <typename T, int THREADS>
 __global__ __launch_bounds__(THREADS) void k_policy_long(LogitsArgs l, PolicyArgs a, T* dlogits,
                                                          int64_t ldd) {
-  constexpr int N = kVec<T>, kU = 2;
   __shared__ MaxSum lds[THREADS / 64];
   __shared__ float lds_g;
   const int64_t row = blockIdx.x;
-  const int vocab = (int)l.vocab, nvec = vocab / N;
+  const int vocab = (int)l.vocab;
   const int64_t t = l.targets[row];
-  const int seq = a.row_seq[row];
   T* out = dlogits ? dlogits + row * ldd : nullptr;
   const bool lead = threadIdx.x < 64;
   const bool skip = t == l.ignore || t < 0 || t >= l.vocab;
   const T* x = static_cast<const T*>(l.logits) + row * l.ld;
   const float k = l.scale * kLog2e;
   MaxSum v{0.0f, 1.0f};
-  if (!skip) v = block_join<THREADS>(stream_row<T, THREADS>(x, vocab, k), k, lds);
+  if (!skip) v = block_join<THREADS>(stream_row<T, THREADS>(x, vocab, k, threadIdx.x), k, lds);
   const float m = shift(v.m), ls = logf(v.s);
   if (lead) {
-    const float total = policy_total(a);
+    const Place at = policy_place(l, a, row);
     if (threadIdx.x == 0) {
       const float lp = t == l.ignore ? 0.0f
                        : skip        ? __builtin_nanf("")
                                      : (to_f32(x[t]) - m) * l.scale - ls;
-      const PolicyRow o = policy_row(a, row, seq, policy_weight(a, seq, total), lp);
+      const PolicyRow o = policy_row(a, row, at.seq, at.w, lp);
       a.logp[row] = lp;
       a.terms[row] = o.terms;
-      lds_g = skip ? (seq < 0 ? 0.0f : lp) : o.dlogp * l.scale;
+      lds_g = skip ? lp : o.dlogp * l.scale;
     }
   }
   if (!out) return;
   __syncthreads();
   const float g = lds_g;
   if (skip || g == 0.0f) {
-    fill_row<T, THREADS>(out, vocab, g);
+    fill_row<T, THREADS>(out, vocab, g, threadIdx.x);
     return;
   }
   const RowGrad q{g, m, ls * kLog2e, k, (int)t};
-  for (int v0 = threadIdx.x; v0 < nvec; v0 += THREADS * kU) {
-    u32x4 d[kU];
-#pragma unroll
-    for (int i = 0; i < kU; ++i)
-      if (v0 + i * THREADS < nvec) d[i] = load_vec(x + (int64_t)(v0 + i * THREADS) * N);
-#pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      if (v0 + i * THREADS >= nvec) continue;
-      float f[N];
-      unpack<T>(d[i], f);
-      grad_terms<N>(q, (v0 + i * THREADS) * N, f);
-      store_vec_once(out + (int64_t)(v0 + i * THREADS) * N, pack<T>(f));
-    }
-  }
-  const int i = nvec * N + (int)threadIdx.x;
-  if (i < vocab) {
-    float f = to_f32(x[i]);
-    grad_terms<1>(q, i, &f);
-    from_f32(f, out[i]);
-  }
+  grad_row<T, THREADS>(x, out, vocab, q, threadIdx.x);
 }
 
+// Loss and averages from all rows' terms, by one workgroup.
 __global__ __launch_bounds__(1024) void k_policy_stats(PolicyArgs a, int64_t rows) {
   __shared__ double lds[3][16];
   double p = 0.0, k = 0.0, c = 0.0;
@@ -577,10 +723,31 @@ hipError_t launch_dlogits(const LogitsArgs& l, const RowStat* stat, const float*
   return hipGetLastError();
 }
 
-hipError_t launch_preference(const PreferenceArgs& a, hipStream_t st) {
-  const unsigned grid = (unsigned)std::max<int64_t>(a.pairs, 1);
-  hipLaunchKernelGGL(k_preference, dim3(grid), dim3(kPrefThreads), 0, st, a);
-  return hipGetLastError();
+// Pairs of at most about 64 rows and 2^17 logits (on average) are done sooner
+// by a workgroup each in one launch than by three launches: 14.8 against 20.5
+// us a call at 8 x 500 to 32 x 500 logits a pair, 18.2 against 20.4 at
+// 32 x 4000, but 26.8 against 20.6 at 128 x 500.
+static bool small_pairs(const LogitsArgs& l, int64_t pairs) {
+  return l.rows <= 64 * pairs && l.rows * l.vocab <= (pairs << 17);
+}
+
+hipError_t launch_preference(const LogitsArgs& l, const PreferenceArgs& a, RowStat* stat,
+                             float* logp, void* dlogits, int64_t ldd, hipStream_t st) {
+  const dim3 grid((unsigned)std::max<int64_t>(a.pairs, 1));
+  if (small_pairs(l, a.pairs)) {
+    if (l.type == QLORA_BF16)
+      hipLaunchKernelGGL(k_preference_small<uint16_t>, grid, dim3(kPrefThreads), 0, st, l, a, stat,
+                         logp, static_cast<uint16_t*>(dlogits), ldd);
+    else
+      hipLaunchKernelGGL(k_preference_small<float>, grid, dim3(kPrefThreads), 0, st, l, a, stat,
+                         logp, static_cast<float*>(dlogits), ldd);
+    return hipGetLastError();
+  }
+  hipError_t e = launch_logp(l, logp, nullptr, stat, st);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_preference, grid, dim3(kPrefThreads), 0, st, a);
+  if (!dlogits) return hipGetLastError();
+  return launch_dlogits(l, stat, nullptr, a.dlogp, dlogits, ldd, st);
 }
 
 // E logits a thread and THREADS a row, the smallest that hold the row.
@@ -604,16 +771,20 @@ static void policy_by_width(const LogitsArgs& l, const PolicyArgs& a, T* dlogits
     hipLaunchKernelGGL((k_policy_long<T, 1024>), grid, dim3(1024), 0, st, l, a, dlogits, ldd);
 }
 
-hipError_t launch_policy(const LogitsArgs& l, const PolicyArgs& a, void* dlogits, int64_t ldd,
+hipError_t launch_policy(const LogitsArgs& l, const PolicyArgs& args, void* dlogits, int64_t ldd,
                          hipStream_t st) {
+  PolicyArgs a = args;
+  const bool bf16 = l.type == QLORA_BF16;
   if (l.rows > 0) {
-    const unsigned seqs = (unsigned)std::max<int64_t>(a.seqs, 1);
-    hipLaunchKernelGGL(k_policy_count, dim3(seqs), dim3(256), 0, st, l, a);
-    if (l.type == QLORA_BF16) {
-      policy_by_width(l, a, static_cast<uint16_t*>(dlogits), ldd, st);
-    } else {
-      policy_by_width(l, a, static_cast<float*>(dlogits), ldd, st);
-    }
+    // in a batch of few rows a row's workgroup finds its sequence and weight
+    // by itself: one launch less (20.5 to 17.3 us a call at 23 rows, no
+    // difference any more at 1586)
+    if (l.rows <= 1024 && a.seqs < 1024) a.row_seq = nullptr;
+    if (a.row_seq)
+      hipLaunchKernelGGL(k_policy_count, dim3((unsigned)std::max<int64_t>(a.seqs, 1)), dim3(256), 0,
+                         st, l, a);
+    if (bf16) policy_by_width(l, a, static_cast<uint16_t*>(dlogits), ldd, st);
+    else policy_by_width(l, a, static_cast<float*>(dlogits), ldd, st);
   }
   hipLaunchKernelGGL(k_policy_stats, dim3(1), dim3(1024), 0, st, a, l.rows);
   return hipGetLastError();

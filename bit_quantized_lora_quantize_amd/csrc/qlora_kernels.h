@@ -537,7 +537,10 @@ struct PreferenceArgs {
   float* loss;             // [pairs]
   float* dlogp;            // [rows], or NULL for the loss alone
 };
-hipError_t launch_preference(const PreferenceArgs& a, hipStream_t st);
+// a.logp is logp; dlogits NULL: the loss alone (a.dlogp is then not used).
+// rows >= 0; without rows only the losses are written.
+hipError_t launch_preference(const LogitsArgs& l, const PreferenceArgs& a, RowStat* stat,
+                             float* logp, void* dlogits, int64_t ldd, hipStream_t st);
 
 struct PolicyArgs {
   const int64_t* offsets;  // [seqs + 1]
