@@ -8,16 +8,27 @@
 // with mean = 0 (and no sum(u) term) for the RMS norm.
 //
 // Every kernel is bound by memory.  A row is held in the registers of the
-// ROW threads that own it, E values each, so every array is read once; the
-// variance is summed from the centred values, which costs no second read.
-// ROW and E are the smallest that hold the row (by_width); wider rows take
-// the looping kernels below, which read them again from the caches.
+// threads that own it, so every array is read once; the variance is summed
+// from the centred values, which costs no second read.  A row takes as many
+// wavefronts as it fills (at 8 or 16 values a thread, 32 in the widest
+// forward), a workgroup as many rows as fit it, and the grid is persistent: a
+// thread keeps its columns' weights, loads its part of the next row before it
+// works on the present one, and in the backward sums its columns' weight
+// gradients in registers.  Wider rows take the looping kernels below, which
+// read them again from the caches.
 #include "qlora_kernels.h"
 #include "row_ops.h"
 
 namespace qlora {
 
 namespace {
+
+constexpr int kFinishCols = 16;
+// Arrays of this size and more go past the caches' retention: the two to four
+// of a call would drive each other out of the 256 MB of the last level anyway.
+// Backward of 16384 x 8192 BF16: 199 us kept, 187 us past; smaller outputs stay
+// for the layer that reads them next.
+constexpr int64_t kOnceBytes = int64_t(128) << 20;
 
 __device__ __forceinline__ float load_w(const void* w, int w_type, int64_t i) {
   return w_type == QLORA_F32 ? static_cast<const float*>(w)[i]
@@ -39,46 +50,59 @@ __device__ __forceinline__ void load_w_vec(const void* w, int w_type, int64_t i,
   }
 }
 
-// The part of a row that one of its ROW threads holds: V vectors, ROW apart,
-// and at most one element of the last, partial vector (`rest`, -1 without).
-template <typename T, int ROW, int E>
-struct Part {
-  static constexpr int N = kVec<T>, V = E / N;
-  int lane, nvec, rest;
-  __device__ __forceinline__ Part(int thread, int d) {
-    lane = thread;
-    nvec = d / N;
-    const int i = nvec * N + thread;
-    rest = i < d ? i : -1;
-  }
-  __device__ __forceinline__ bool has(int q) const { return lane + q * ROW < nvec; }
-  __device__ __forceinline__ int64_t at(int q) const { return (int64_t)(lane + q * ROW) * N; }
-};
-
-template <bool ONCE, typename T, int ROW, int E>
-__device__ __forceinline__ void load_part(const Part<T, ROW, E>& p, const T* x, u32x4* v, T& rest) {
-#pragma unroll
-  for (int q = 0; q < Part<T, ROW, E>::V; ++q) {
-    v[q] = u32x4{0, 0, 0, 0};
-    if (p.has(q)) v[q] = ONCE ? load_vec_once(x + p.at(q)) : load_vec(x + p.at(q));
-  }
-  rest = T(0);
-  if (p.rest >= 0) rest = x[p.rest];
+template <bool ONCE, typename T>
+__device__ __forceinline__ u32x4 get_vec(const T* p) {
+  if constexpr (ONCE) return load_vec_once(p);
+  else return load_vec(p);
 }
-
 template <bool ONCE, typename T>
 __device__ __forceinline__ void put_vec(T* p, u32x4 v) {
   if constexpr (ONCE) store_vec_once(p, v);
   else store_vec(p, v);
 }
 
-// The weights of a thread's part (0 past the row's end).
-template <typename T, int ROW, int E>
-__device__ __forceinline__ void weight_part(const Part<T, ROW, E>& p, const void* w, int w_type,
-                                            float* f, float& rest) {
-  constexpr int N = Part<T, ROW, E>::N;
+// The part of a row that one of its `threads` threads holds: V vectors,
+// `threads` apart, and at most one element of the last, partial vector
+// (`rest`, -1 without).
+template <typename T, int V>
+struct Part {
+  static constexpr int N = kVec<T>, E = V * N;
+  int lane, threads, nvec, rest;
+  __device__ __forceinline__ Part(int thread, int threads_, int d) {
+    lane = thread;
+    threads = threads_;
+    nvec = d / N;
+    const int i = nvec * N + thread;
+    rest = i < d ? i : -1;
+  }
+  __device__ __forceinline__ bool has(int q) const { return lane + q * threads < nvec; }
+  __device__ __forceinline__ int at(int q) const { return (lane + q * threads) * N; }
+};
+
+// A part's values of one array (0 past the row's end).
+template <typename T, int V>
+struct Held {
+  u32x4 v[V];
+  T rest;
+};
+template <bool ONCE, typename T, int V>
+__device__ __forceinline__ void load_part(const Part<T, V>& p, const T* x, Held<T, V>& h) {
 #pragma unroll
-  for (int q = 0; q < Part<T, ROW, E>::V; ++q) {
+  for (int q = 0; q < V; ++q) {
+    h.v[q] = u32x4{0, 0, 0, 0};
+    if (p.has(q)) h.v[q] = get_vec<ONCE>(x + p.at(q));
+  }
+  h.rest = T(0);
+  if (p.rest >= 0) h.rest = x[p.rest];
+}
+
+// Its weights (0 past the row's end).
+template <typename T, int V>
+__device__ __forceinline__ void weight_part(const Part<T, V>& p, const void* w, int w_type,
+                                            float* f, float& rest) {
+  constexpr int N = kVec<T>;
+#pragma unroll
+  for (int q = 0; q < V; ++q) {
 #pragma unroll
     for (int j = 0; j < N; ++j) f[q * N + j] = 0.0f;
     if (p.has(q)) load_w_vec<N>(w, w_type, p.at(q), f + q * N);
@@ -86,237 +110,298 @@ __device__ __forceinline__ void weight_part(const Part<T, ROW, E>& p, const void
   rest = p.rest >= 0 ? load_w(w, w_type, p.rest) : 0.0f;
 }
 
-// Sums over the ROW threads of each row of a workgroup; the rows of a
-// workgroup go through it together.
-template <int ROW, int THREADS, int COUNT>
-__device__ __forceinline__ void row_sums(float (&v)[COUNT], float (*lds)[COUNT]) {
+// A barrier for data in LDS alone: loads from memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Sums over the `threads` threads (whole wavefronts, at most 16) of each row of
+// a workgroup; the rows of a workgroup go through it together.
+template <int COUNT>
+__device__ __forceinline__ void row_sums(float (&v)[COUNT], int threads, float (*lds)[COUNT]) {
 #pragma unroll
   for (int c = 0; c < COUNT; ++c) v[c] = wave_sum(v[c]);
-  if constexpr (ROW > 64) {
-    constexpr int W = ROW / 64;
-    const int wave = threadIdx.x / 64;
-    if ((threadIdx.x & 63) == 0) {
+  if (threads == 64) return;
+  const int wave = threadIdx.x / 64, lane = threadIdx.x & 63, W = threads / 64;
+  if (lane == 0) {
 #pragma unroll
-      for (int c = 0; c < COUNT; ++c) lds[wave][c] = v[c];
+    for (int c = 0; c < COUNT; ++c) lds[wave][c] = v[c];
+  }
+  lds_barrier();
+  const int first = wave / W * W;
+#pragma unroll
+  for (int c = 0; c < COUNT; ++c) v[c] = row16_sum(lane < W ? lds[first + lane][c] : 0.0f);
+}
+
+// A thread's place: its row group of the workgroup, the same for its
+// wavefront.
+__device__ __forceinline__ int row_group(int row_threads) {
+  return __builtin_amdgcn_readfirstlane((int)threadIdx.x / row_threads);
+}
+
+}  // namespace
+
+// blockDim.x / row_threads rows per workgroup at a time, `stride` rows from
+// one to the next.
+template <typename T, int V, bool LAYER, bool ONCE>
+__global__ __launch_bounds__(1024) void k_norm_fwd(NormFwdArgs a, int row_threads,
+                                                   int64_t stride) {
+  constexpr int N = kVec<T>, E = V * N;
+  constexpr bool AHEAD = E <= 16;              // wider: no registers for the next row
+  __shared__ float lds[2][2][16][1];
+  const int group = row_group(row_threads), groups = blockDim.x / row_threads;
+  const Part<T, V> p(threadIdx.x - group * row_threads, row_threads, (int)a.d);
+  const T *xs = static_cast<const T*>(a.x), *rs = static_cast<const T*>(a.r);
+  const float inv = 1.0f / (float)a.d;
+  int64_t row = (int64_t)blockIdx.x * groups + group;
+  // rows past the end are those of a workgroup's idle groups: they read the last
+  const auto base = [&](int64_t r) { return (r < a.rows ? r : a.rows - 1) * a.d; };
+  Held<T, V> x, r;
+  load_part<ONCE>(p, xs + base(row), x);
+  if (rs) load_part<ONCE>(p, rs + base(row), r);
+  const bool shifted = LAYER && a.beta;
+  float g[AHEAD ? E : N], b[AHEAD ? E : N], gr, br = 0.0f;
+  if constexpr (AHEAD) {
+    weight_part(p, a.gamma, a.w_type, g, gr);
+    if (shifted) weight_part(p, a.beta, a.w_type, b, br);
+  } else {
+    gr = p.rest >= 0 ? load_w(a.gamma, a.w_type, p.rest) : 0.0f;
+    if (shifted && p.rest >= 0) br = load_w(a.beta, a.w_type, p.rest);
+  }
+  for (int turn = 0;; turn ^= 1, row += stride) {
+    const bool live = row < a.rows, more = row - group + stride < a.rows;
+    Held<T, V> xn, rn;
+    if (AHEAD && more) {
+      load_part<ONCE>(p, xs + base(row + stride), xn);
+      if (rs) load_part<ONCE>(p, rs + base(row + stride), rn);
     }
-    __syncthreads();
-    const int first = wave / W * W;
+    float h[E], hr;
+    if (rs) {
+      T* out = static_cast<T*>(a.h) + base(row);
+      float f[N];
 #pragma unroll
-    for (int c = 0; c < COUNT; ++c) {
-      v[c] = 0.0f;
+      for (int q = 0; q < V; ++q) {
+        unpack<T>(x.v[q], h + q * N);
+        unpack<T>(r.v[q], f);
 #pragma unroll
-      for (int w = 0; w < W; ++w) v[c] += lds[first + w][c];
+        for (int j = 0; j < N; ++j) f[j] += h[q * N + j];
+        x.v[q] = pack<T>(f);                   // the one rounding of H
+        if (live && p.has(q)) put_vec<ONCE>(out + p.at(q), x.v[q]);
+      }
+      from_f32(to_f32(x.rest) + to_f32(r.rest), x.rest);
+      if (live && p.rest >= 0) out[p.rest] = x.rest;
+    }
+#pragma unroll
+    for (int q = 0; q < V; ++q) unpack<T>(x.v[q], h + q * N);
+    hr = to_f32(x.rest);
+    float mean = 0.0f;
+    if constexpr (LAYER) {
+      float s[1] = {hr};                       // 0 in threads without a rest
+#pragma unroll
+      for (int j = 0; j < E; ++j) s[0] += h[j];
+      row_sums(s, row_threads, lds[turn][0]);
+      mean = s[0] * inv;
+      hr -= mean;
+#pragma unroll
+      for (int j = 0; j < E; ++j) h[j] -= mean;
+    }
+    float s[1] = {p.rest >= 0 ? hr * hr : 0.0f};
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+      float t = 0.0f;
+#pragma unroll
+      for (int j = 0; j < N; ++j) t += h[q * N + j] * h[q * N + j];
+      if (p.has(q)) s[0] += t;
+    }
+    row_sums(s, row_threads, lds[turn][1]);
+    const float rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
+    if (live) {
+      T* y = static_cast<T*>(a.y) + base(row);
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        const int w = AHEAD ? q * N : 0;       // the widest rows fetch their weights here
+        if (!AHEAD && p.has(q)) {
+          load_w_vec<N>(a.gamma, a.w_type, p.at(q), g);
+          if (shifted) load_w_vec<N>(a.beta, a.w_type, p.at(q), b);
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          h[q * N + j] = h[q * N + j] * rstd * g[w + j];
+          if (shifted) h[q * N + j] += b[w + j];
+        }
+        if (p.has(q)) put_vec<ONCE>(y + p.at(q), pack<T>(h + q * N));
+      }
+      if (p.rest >= 0) from_f32(shifted ? hr * rstd * gr + br : hr * rstd * gr, y[p.rest]);
+      if (p.lane == 0) {
+        if (LAYER && a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = rstd;
+      }
+    }
+    if (!more) return;
+    if constexpr (AHEAD) {
+      x = xn;
+      r = rn;
+    } else {
+      load_part<ONCE>(p, xs + base(row + stride), x);
+      if (rs) load_part<ONCE>(p, rs + base(row + stride), r);
     }
   }
+}
+
+namespace {
+
+// What the backward reads of one row.
+template <typename T, int V>
+struct BwdRow {
+  Held<T, V> y, h, d;
+  float mean, rstd;
+};
+template <bool LAYER, bool ONCE, typename T, int V>
+__device__ __forceinline__ void load_row(const NormBwdArgs& a, const Part<T, V>& p, int64_t row,
+                                         BwdRow<T, V>& o) {
+  row = row < a.rows ? row : a.rows - 1;       // an idle group reads the last row
+  const int64_t base = row * a.d;
+  load_part<ONCE>(p, static_cast<const T*>(a.dy) + base, o.y);
+  load_part<ONCE>(p, static_cast<const T*>(a.h) + base, o.h);
+  if (a.dh) load_part<ONCE>(p, static_cast<const T*>(a.dh) + base, o.d);
+  o.mean = LAYER ? a.mean[row] : 0.0f;
+  o.rstd = a.rstd[row];
 }
 
 // The sums of a workgroup's row groups, added in order, as one row of d
 // partials: four columns a thread at a time, the groups meeting in LDS.
-template <typename T, int ROW, int E, int THREADS>
-__device__ __forceinline__ void write_partial(const Part<T, ROW, E>& p, int group, const float* v,
-                                              float rest, float* part) {
-  constexpr int G = THREADS / ROW, N = kVec<T>;
-  if constexpr (G == 1) {
+template <typename T, int V>
+__device__ __forceinline__ void write_partial(const Part<T, V>& p, int group, int groups,
+                                              const float* v, float rest, float* part,
+                                              f32x4* lds) {
+  constexpr int N = kVec<T>, E = V * N;
+  if (groups == 1) {
 #pragma unroll
     for (int c = 0; c < E / 4; ++c)
       if (p.has(4 * c / N)) store_vec(part + p.at(4 * c / N) + 4 * c % N, pack<float>(v + 4 * c));
     if (p.rest >= 0) part[p.rest] = rest;
-  } else {
-    __shared__ f32x4 sum[THREADS];
+    return;
+  }
 #pragma unroll
-    for (int c = 0; c <= E / 4; ++c) {
-      const bool last = c == E / 4;            // the partial vector's element
-      __syncthreads();
-      if (last) sum[threadIdx.x].x = rest;
-      else sum[threadIdx.x] = __builtin_bit_cast(f32x4, pack<float>(v + 4 * c));
-      __syncthreads();
-      if (group) continue;
-      f32x4 t = sum[p.lane];
-#pragma unroll
-      for (int k = 1; k < G; ++k) t += sum[k * ROW + p.lane];
-      if (last) {
-        if (p.rest >= 0) part[p.rest] = t.x;
-      } else if (p.has(4 * c / N)) {
-        store_vec(part + p.at(4 * c / N) + 4 * c % N, __builtin_bit_cast(u32x4, t));
-      }
+  for (int c = 0; c <= E / 4; ++c) {
+    const bool last = c == E / 4;              // the partial vector's element
+    lds_barrier();
+    if (last) lds[threadIdx.x].x = rest;
+    else lds[threadIdx.x] = __builtin_bit_cast(f32x4, pack<float>(v + 4 * c));
+    lds_barrier();
+    if (group) continue;
+    f32x4 t = lds[p.lane];
+    for (int k = 1; k < groups; ++k) t += lds[k * p.threads + p.lane];
+    if (last) {
+      if (p.rest >= 0) part[p.rest] = t.x;
+    } else if (p.has(4 * c / N)) {
+      store_vec(part + p.at(4 * c / N) + 4 * c % N, __builtin_bit_cast(u32x4, t));
     }
   }
 }
-
-constexpr int kBwdThreads = 1024;
-constexpr int kFinishCols = 16;
-// Arrays of this size and more go past the caches' retention: the two to four
-// of a call would drive each other out of the 256 MB of the last level anyway.
-// Backward of 16384 x 8192 BF16: 199 us kept, 187 us past; smaller outputs stay
-// for the layer that reads them next.
-constexpr int64_t kOnceBytes = int64_t(128) << 20;
 
 }  // namespace
 
-// THREADS / ROW rows per workgroup, each by ROW of its threads.
-template <typename T, int ROW, int E, int THREADS, bool ONCE>
-__global__ __launch_bounds__(THREADS) void k_norm_fwd(NormFwdArgs a) {
-  __shared__ float lds[2][THREADS / 64][1];
-  const int64_t row = (int64_t)blockIdx.x * (THREADS / ROW) + threadIdx.x / ROW;
-  const bool live = row < a.rows;
-  const int64_t base = (live ? row : a.rows - 1) * a.d;
-  const Part<T, ROW, E> p(threadIdx.x % ROW, (int)a.d);
-  constexpr int N = Part<T, ROW, E>::N, V = Part<T, ROW, E>::V;
-  u32x4 v[V];
-  T rest;
-  load_part<ONCE>(p, static_cast<const T*>(a.x) + base, v, rest);
-  float h[E], hr;
-  if (a.r) {
-    u32x4 w[V];
-    T rr;
-    load_part<ONCE>(p, static_cast<const T*>(a.r) + base, w, rr);
-    T* out = static_cast<T*>(a.h) + base;
-    float f[N];
-#pragma unroll
-    for (int q = 0; q < V; ++q) {
-      unpack<T>(v[q], h + q * N);
-      unpack<T>(w[q], f);
-#pragma unroll
-      for (int j = 0; j < N; ++j) f[j] += h[q * N + j];
-      v[q] = pack<T>(f);                       // the one rounding of H
-      if (live && p.has(q)) put_vec<ONCE>(out + p.at(q), v[q]);
-    }
-    from_f32(to_f32(rest) + to_f32(rr), rest);
-    if (live && p.rest >= 0) out[p.rest] = rest;
-  }
-  float g[E], b[E], gr, br = 0.0f;
-  weight_part(p, a.gamma, a.w_type, g, gr);
-  if (a.beta) {
-    weight_part(p, a.beta, a.w_type, b, br);
-  } else {
-#pragma unroll
-    for (int j = 0; j < E; ++j) b[j] = 0.0f;
-  }
-#pragma unroll
-  for (int q = 0; q < V; ++q) unpack<T>(v[q], h + q * N);
-  hr = to_f32(rest);
-  const float inv = 1.0f / (float)a.d;
-  float mean = 0.0f;
-  if (a.kind == QLORA_NORM_LAYER) {
-    float s[1] = {hr};                         // 0 in threads without a rest
-#pragma unroll
-    for (int j = 0; j < E; ++j) s[0] += h[j];
-    row_sums<ROW, THREADS>(s, lds[0]);
-    mean = s[0] * inv;
-    hr -= mean;
-#pragma unroll
-    for (int j = 0; j < E; ++j) h[j] -= mean;
-  }
-  float s[1] = {p.rest >= 0 ? hr * hr : 0.0f};
-#pragma unroll
-  for (int q = 0; q < V; ++q) {
-    float t = 0.0f;
-#pragma unroll
-    for (int j = 0; j < N; ++j) t += h[q * N + j] * h[q * N + j];
-    if (p.has(q)) s[0] += t;
-  }
-  row_sums<ROW, THREADS>(s, lds[1]);
-  const float rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
-  if (!live) return;
-  T* y = static_cast<T*>(a.y) + base;
-#pragma unroll
-  for (int q = 0; q < V; ++q) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int e = q * N + j;
-      h[e] = h[e] * rstd * g[e] + b[e];
-    }
-    if (p.has(q)) put_vec<ONCE>(y + p.at(q), pack<T>(h + q * N));
-  }
-  if (p.rest >= 0) from_f32(hr * rstd * gr + br, y[p.rest]);
-  if (p.lane == 0) {
-    if (a.mean && a.kind == QLORA_NORM_LAYER) a.mean[row] = mean;
-    if (a.rstd) a.rstd[row] = rstd;
-  }
-}
-
 // Input gradients, and with WEIGHTS the partial weight gradients of the rows
-// that a workgroup takes: G = THREADS / ROW at a time, each by ROW threads
-// that keep the sums of their own columns in registers; at the end the G
-// sums of a column are added in order and written as one partial.
-template <typename T, int ROW, int E, int THREADS, bool WEIGHTS, bool ONCE>
-__global__ __launch_bounds__(THREADS) void k_norm_bwd(NormBwdArgs a, int parts) {
-  constexpr int N = Part<T, ROW, E>::N, V = Part<T, ROW, E>::V, G = THREADS / ROW;
-  __shared__ float lds[2][THREADS / 64][2];
-  const Part<T, ROW, E> p(threadIdx.x % ROW, (int)a.d);
-  const int group = threadIdx.x / ROW;
-  const bool layer = a.kind == QLORA_NORM_LAYER;
+// that a workgroup takes.  gamma waits in LDS (four of a thread's columns side
+// by side, so that a wavefront reads without bank conflicts).
+template <typename T, int V, bool LAYER, bool WEIGHTS, bool ONCE>
+__global__ __launch_bounds__(1024) void k_norm_bwd(NormBwdArgs a, int row_threads,
+                                                   int64_t stride) {
+  constexpr int N = kVec<T>, E = V * N;
+  // the next row's values need registers: of 16 a thread only beside few sums
+  constexpr bool AHEAD = E <= 8 || (sizeof(T) == 2 && !(LAYER && WEIGHTS));
+  __shared__ float lds[2][16][2];
+  extern __shared__ f32x4 dyn[];               // gamma, later the groups' sums
+  const int group = row_group(row_threads), groups = blockDim.x / row_threads;
+  const Part<T, V> p(threadIdx.x - group * row_threads, row_threads, (int)a.d);
   const float inv = 1.0f / (float)a.d;
-  float g[E], gr;
-  weight_part(p, a.gamma, a.w_type, g, gr);
+  int64_t row = (int64_t)blockIdx.x * groups + group;
+  BwdRow<T, V> cur;
+  load_row<LAYER, ONCE>(a, p, row, cur);
+  float gr;
+  {
+    float g[E];
+    weight_part(p, a.gamma, a.w_type, g, gr);
+    if (group == 0) {
+#pragma unroll
+      for (int c = 0; c < E / 4; ++c)
+        dyn[c * row_threads + p.lane] = __builtin_bit_cast(f32x4, pack<float>(g + 4 * c));
+    }
+    lds_barrier();
+  }
+  const f32x4* gam = dyn + p.lane;
   float dg[E], db[E], dgr = 0.0f, dbr = 0.0f;
   if constexpr (WEIGHTS) {
 #pragma unroll
     for (int j = 0; j < E; ++j) dg[j] = db[j] = 0.0f;
   }
-  int turn = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * G; r0 < a.rows; r0 += (int64_t)parts * G, turn ^= 1) {
-    const int64_t row = r0 + group;
-    const bool live = row < a.rows;
-    const int64_t base = (live ? row : a.rows - 1) * a.d;
-    const float mean = layer ? a.mean[live ? row : a.rows - 1] : 0.0f;
-    const float rstd = a.rstd[live ? row : a.rows - 1];
-    u32x4 vy[V], vh[V], vd[V];
-    T ry, rh, rd = T(0);
-    load_part<ONCE>(p, static_cast<const T*>(a.dy) + base, vy, ry);
-    load_part<ONCE>(p, static_cast<const T*>(a.h) + base, vh, rh);
-    if (a.dh) load_part<ONCE>(p, static_cast<const T*>(a.dh) + base, vd, rd);
-    float s[2] = {0.0f, 0.0f};                 // sum(u), sum(u n)
+  for (int turn = 0;; turn ^= 1, row += stride) {
+    const bool live = row < a.rows, more = row - group + stride < a.rows;
+    BwdRow<T, V> next;
+    if (AHEAD && more) load_row<LAYER, ONCE>(a, p, row + stride, next);
+    const float mean = cur.mean, rstd = cur.rstd;
+    float s[2] = {0.0f, 0.0f};                 // sum(u n), sum(u)
     float y[N], n[N];
 #pragma unroll
     for (int q = 0; q < V; ++q) {
-      unpack<T>(vy[q], y);
-      unpack<T>(vh[q], n);
+      unpack<T>(cur.y.v[q], y);
+      unpack<T>(cur.h.v[q], n);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const int e = q * N + j;
         n[j] = (n[j] - mean) * rstd;
         if constexpr (WEIGHTS) {
           dg[e] += live ? y[j] * n[j] : 0.0f;
-          db[e] += live ? y[j] : 0.0f;
+          if constexpr (LAYER) db[e] += live ? y[j] : 0.0f;
         }
-        const float u = y[j] * g[e];           // 0 past the row's end
-        s[0] += u;
-        s[1] += u * n[j];
+        const float u = y[j] * gam[e / 4 * row_threads][e % 4];   // 0 past the row's end
+        s[0] += u * n[j];
+        if constexpr (LAYER) s[1] += u;
       }
     }
-    const float yr = to_f32(ry), nr = (to_f32(rh) - mean) * rstd, ur = yr * gr;
+    const float yr = to_f32(cur.y.rest), nr = (to_f32(cur.h.rest) - mean) * rstd, ur = yr * gr;
     if constexpr (WEIGHTS) {
       dgr += live ? yr * nr : 0.0f;
       dbr += live ? yr : 0.0f;
     }
-    s[0] += ur;
-    s[1] += ur * nr;
-    row_sums<ROW, THREADS>(s, lds[turn]);
-    const float mu = layer ? s[0] * inv : 0.0f, mn = s[1] * inv;
+    s[0] += ur * nr;
+    s[1] += ur;
+    row_sums(s, row_threads, lds[turn]);
+    const float mn = s[0] * inv, mu = LAYER ? s[1] * inv : 0.0f;
     if (live) {
-      T* dx = static_cast<T*>(a.dx) + base;
+      T* dx = static_cast<T*>(a.dx) + row * a.d;
 #pragma unroll
       for (int q = 0; q < V; ++q) {
-        unpack<T>(vy[q], y);
-        unpack<T>(vh[q], n);
+        unpack<T>(cur.y.v[q], y);
+        unpack<T>(cur.h.v[q], n);
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-          y[j] = (y[j] * g[q * N + j] - mu - (n[j] - mean) * rstd * mn) * rstd;
+        for (int j = 0; j < N; ++j) {
+          const int e = q * N + j;
+          y[j] = (y[j] * gam[e / 4 * row_threads][e % 4] - mu - (n[j] - mean) * rstd * mn) * rstd;
+        }
         if (a.dh) {
-          unpack<T>(vd[q], n);
+          unpack<T>(cur.d.v[q], n);
 #pragma unroll
           for (int j = 0; j < N; ++j) y[j] += n[j];
         }
         if (p.has(q)) put_vec<ONCE>(dx + p.at(q), pack<T>(y));
       }
-      if (p.rest >= 0) from_f32((ur - mu - nr * mn) * rstd + to_f32(rd), dx[p.rest]);
+      if (p.rest >= 0)
+        from_f32((ur - mu - nr * mn) * rstd + (a.dh ? to_f32(cur.d.rest) : 0.0f), dx[p.rest]);
     }
+    if (!more) break;
+    if constexpr (AHEAD) cur = next;
+    else load_row<LAYER, ONCE>(a, p, row + stride, cur);
   }
   if constexpr (WEIGHTS) {
     float* part = a.part + (int64_t)blockIdx.x * 2 * a.d;
-    if (a.dgamma) write_partial<T, ROW, E, THREADS>(p, group, dg, dgr, part);
-    if (a.dbeta) write_partial<T, ROW, E, THREADS>(p, group, db, dbr, part + a.d);
+    if (a.dgamma) write_partial(p, group, groups, dg, dgr, part, dyn);
+    if constexpr (LAYER) {
+      if (a.dbeta) write_partial(p, group, groups, db, dbr, part + a.d, dyn);
+    }
   }
 }
 
@@ -446,83 +531,104 @@ __global__ __launch_bounds__(256) void k_norm_wgrad_wide(NormBwdArgs a, int64_t 
 
 // ------------------------------------------------- launches
 constexpr int64_t kFwdHeld = 32768;   // widest row held in registers, forward
-constexpr int64_t kBwdHeld = 16384;   // backward: twice the arrays, and the sums
+constexpr int64_t kBwdHeld = 16384;   // backward: more arrays, and the sums
 
-// Threads that hold a row of the backward: 8 values each (16 above 8192).
-static int bwd_row_threads(int64_t d) {
-  int row = 64;
-  while (row < 1024 && (int64_t)row * 8 < d) row *= 2;
-  return row;
+namespace {
+
+// How a call takes its rows: threads a row, rows a workgroup, workgroups.
+struct Shape {
+  int row_threads, groups, grid;
+};
+// `held` values a thread, workgroups of at most `threads`, at most `waves`
+// wavefronts on each of the 256 compute units.
+Shape row_shape(int64_t rows, int64_t d, int held, int threads, int waves) {
+  Shape s;
+  s.row_threads = 64 * (int)((d + 64 * held - 1) / (64 * held));
+  s.groups = std::max(1, threads / s.row_threads);
+  const int64_t turns = (rows + s.groups - 1) / s.groups;
+  const int64_t resident = 256 * std::max(1, waves * 64 / (s.groups * s.row_threads));
+  s.grid = (int)std::min(turns, resident);
+  return s;
 }
+// With weight gradients a workgroup costs a partial, and their sums registers:
+// fewer of them.  Narrow rows meet in smaller workgroups, whose barriers wait
+// for fewer (26090 x 566 BF16: 30.0 against 32.5 us).
+Shape bwd_shape(int64_t rows, int64_t d, bool weights) {
+  return row_shape(rows, d, d <= 8192 ? 8 : 16, d <= 1024 ? 512 : 1024, weights ? 16 : 24);
+}
+
+}  // namespace
 
 int norm_parts(int64_t rows, int64_t d) {
-  if (d > kBwdHeld) return (int)std::min<int64_t>(rows, 64);
-  const int64_t g = kBwdThreads / bwd_row_threads(d);
-  const int64_t turns = (rows + g - 1) / g;   // rounds of g rows
-  // one workgroup on each of the 256 compute units at most (the
-  // registers allow no second one)
-  return (int)std::min<int64_t>(turns, 256);
+  return d <= kBwdHeld ? bwd_shape(rows, d, true).grid : (int)std::min<int64_t>(rows, 64);
 }
 
-template <typename T, int ROW, int E, int THREADS>
-static void run_fwd(const NormFwdArgs& a, hipStream_t st) {
-  constexpr int64_t g = THREADS / ROW;
-  const dim3 grid((unsigned)((a.rows + g - 1) / g));
+template <typename T, int V, bool LAYER>
+static void run_fwd(const NormFwdArgs& a, int waves, hipStream_t st) {
+  const Shape s = row_shape(a.rows, a.d, V * kVec<T>, 512, waves);
+  const dim3 grid((unsigned)s.grid), block((unsigned)(s.row_threads * s.groups));
+  const int64_t stride = (int64_t)s.grid * s.groups;
   if (a.rows * a.d * (int64_t)sizeof(T) < kOnceBytes)
-    hipLaunchKernelGGL((k_norm_fwd<T, ROW, E, THREADS, false>), grid, dim3(THREADS), 0, st, a);
-  else hipLaunchKernelGGL((k_norm_fwd<T, ROW, E, THREADS, true>), grid, dim3(THREADS), 0, st, a);
+    hipLaunchKernelGGL((k_norm_fwd<T, V, LAYER, false>), grid, block, 0, st, a, s.row_threads,
+                       stride);
+  else
+    hipLaunchKernelGGL((k_norm_fwd<T, V, LAYER, true>), grid, block, 0, st, a, s.row_threads,
+                       stride);
 }
 
-template <typename T>
+template <typename T, bool LAYER>
 static void fwd_by_width(const NormFwdArgs& a, hipStream_t st) {
-  if (a.d <= 512) run_fwd<T, 64, 8, 256>(a, st);
-  else if (a.d <= 1024) run_fwd<T, 128, 8, 256>(a, st);
-  else if (a.d <= 2048) run_fwd<T, 256, 8, 256>(a, st);
-  else if (a.d <= 4096) run_fwd<T, 512, 8, 512>(a, st);
-  else if (a.d <= 8192) run_fwd<T, 1024, 8, 1024>(a, st);
-  else if (a.d <= 16384) run_fwd<T, 1024, 16, 1024>(a, st);
-  else if (a.d <= kFwdHeld) run_fwd<T, 1024, 32, 1024>(a, st);
+  constexpr int U = 8 / kVec<T>;   // vectors of 8 values
+  // as many wavefronts as the registers allow (5123 x 7040 BF16: 28 us with
+  // 32 a compute unit, 36 with 24)
+  if (a.d <= 8192) run_fwd<T, U, LAYER>(a, sizeof(T) == 2 ? 32 : 24, st);
+  else if (a.d <= 16384) run_fwd<T, 2 * U, LAYER>(a, 16, st);
+  else if (a.d <= kFwdHeld) run_fwd<T, 4 * U, LAYER>(a, 16, st);
   else
     hipLaunchKernelGGL(k_norm_fwd_wide<T>, dim3((unsigned)a.rows), dim3(1024), 0, st, a);
 }
 
+template <typename T>
+static void fwd_by_kind(const NormFwdArgs& a, hipStream_t st) {
+  if (a.kind == QLORA_NORM_LAYER) fwd_by_width<T, true>(a, st);
+  else fwd_by_width<T, false>(a, st);
+}
+
 hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t st) {
-  if (a.type == QLORA_BF16) fwd_by_width<uint16_t>(a, st);
-  else fwd_by_width<float>(a, st);
+  if (a.type == QLORA_BF16) fwd_by_kind<uint16_t>(a, st);
+  else fwd_by_kind<float>(a, st);
   return hipGetLastError();
 }
 
-template <typename T, int ROW, int E, bool ONCE>
-static void run_bwd_as(const NormBwdArgs& a, hipStream_t st) {
-  constexpr int64_t g = kBwdThreads / ROW;
-  if (a.dgamma || a.dbeta) {
-    const int parts = norm_parts(a.rows, a.d);
-    hipLaunchKernelGGL((k_norm_bwd<T, ROW, E, kBwdThreads, true, ONCE>), dim3((unsigned)parts),
-                       dim3(kBwdThreads), 0, st, a, parts);
-  } else {
-    const int grid = (int)((a.rows + g - 1) / g);
-    hipLaunchKernelGGL((k_norm_bwd<T, ROW, E, kBwdThreads, false, ONCE>), dim3((unsigned)grid),
-                       dim3(kBwdThreads), 0, st, a, grid);
-  }
+template <typename T, int V, bool LAYER, bool ONCE>
+static void run_bwd(const NormBwdArgs& a, hipStream_t st) {
+  const bool weights = a.dgamma || a.dbeta;
+  const Shape s = bwd_shape(a.rows, a.d, weights);
+  const dim3 grid((unsigned)s.grid), block((unsigned)(s.row_threads * s.groups));
+  const int64_t stride = (int64_t)s.grid * s.groups;
+  // gamma of a row's threads; then one 16-byte piece of every thread
+  const size_t lds = 16 * std::max<size_t>(block.x, (size_t)s.row_threads * V * kVec<T> / 4);
+  if (weights)
+    hipLaunchKernelGGL((k_norm_bwd<T, V, LAYER, true, ONCE>), grid, block, lds, st, a,
+                       s.row_threads, stride);
+  else
+    hipLaunchKernelGGL((k_norm_bwd<T, V, LAYER, false, ONCE>), grid, block, lds, st, a,
+                       s.row_threads, stride);
 }
 
-template <typename T, int ROW, int E>
-static void run_bwd(const NormBwdArgs& a, hipStream_t st) {
-  if (a.rows * a.d * (int64_t)sizeof(T) < kOnceBytes) run_bwd_as<T, ROW, E, false>(a, st);
-  else run_bwd_as<T, ROW, E, true>(a, st);
+template <typename T, int V, bool LAYER>
+static void bwd_by_size(const NormBwdArgs& a, hipStream_t st) {
+  if (a.rows * a.d * (int64_t)sizeof(T) < kOnceBytes) run_bwd<T, V, LAYER, false>(a, st);
+  else run_bwd<T, V, LAYER, true>(a, st);
 }
 
 template <typename T>
 static void bwd_by_width(const NormBwdArgs& a, hipStream_t st) {
-  switch (bwd_row_threads(a.d)) {
-    case 64: return run_bwd<T, 64, 8>(a, st);
-    case 128: return run_bwd<T, 128, 8>(a, st);
-    case 256: return run_bwd<T, 256, 8>(a, st);
-    case 512: return run_bwd<T, 512, 8>(a, st);
-    default: break;
-  }
-  if (a.d <= 8192) return run_bwd<T, 1024, 8>(a, st);
-  if (a.d <= kBwdHeld) return run_bwd<T, 1024, 16>(a, st);
+  constexpr int U = 8 / kVec<T>;
+  const bool layer = a.kind == QLORA_NORM_LAYER;
+  if (a.d <= 8192) return layer ? bwd_by_size<T, U, true>(a, st) : bwd_by_size<T, U, false>(a, st);
+  if (a.d <= kBwdHeld)
+    return layer ? bwd_by_size<T, 2 * U, true>(a, st) : bwd_by_size<T, 2 * U, false>(a, st);
   if (a.dgamma || a.dbeta) {   // before dX, which may overwrite dY
     const int parts = norm_parts(a.rows, a.d);
     hipLaunchKernelGGL(k_norm_wgrad_wide<T>,
@@ -539,7 +645,8 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t st) {
   }
   if (a.dgamma || a.dbeta) {
     const int parts = a.rows > 0 ? norm_parts(a.rows, a.d) : 0;
-    const dim3 grid((unsigned)((a.d + kFinishCols - 1) / kFinishCols), a.dgamma && a.dbeta ? 2 : 1);
+    const dim3 grid((unsigned)((a.d + kFinishCols - 1) / kFinishCols),
+                    a.dgamma && a.dbeta ? 2 : 1);
     hipLaunchKernelGGL(k_norm_wgrad_finish, grid, dim3(1024), 0, st, a.part, parts, a.d, a.dgamma,
                        a.dbeta);
   }

@@ -114,6 +114,14 @@ __device__ __forceinline__ float wave_sum(float v) {
   v += lane_move<kRowBcast31, 0xC>(0.0f, v);
   return last_lane(v);
 }
+// Sum over the first 16 lanes; every lane gets it.
+__device__ __forceinline__ float row16_sum(float v) {
+  v += lane_move<kRowShr1, 0xF>(0.0f, v);
+  v += lane_move<kRowShr2, 0xF>(0.0f, v);
+  v += lane_move<kRowShr4, 0xF>(0.0f, v);
+  v += lane_move<kRowShr8, 0xF>(0.0f, v);
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 15));
+}
 __device__ __forceinline__ float wave_max(float v) {
   const float none = -__builtin_huge_valf();
   v = fmaxf(v, lane_move<kRowShr1, 0xF>(none, v));
