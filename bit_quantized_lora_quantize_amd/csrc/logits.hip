@@ -271,12 +271,14 @@ __device__ __forceinline__ PairSlope pair_loss(const PreferenceArgs& a, int64_t 
     lds[2][wave] = vn;
   }
   __syncthreads();
-  double s[2] = {0.0, 0.0}, g[2] = {0.0, 0.0}, n[2] = {0.0, 0.0};
+  // every wavefront adds the W partial sums of each sequence
+  double s[2], g[2], n[2];
+  const int at = threadIdx.x & 63;
 #pragma unroll
-  for (int w = 0; w < 2 * W; ++w) {
-    s[w / W] += lds[0][w];
-    g[w / W] += lds[1][w];
-    n[w / W] += lds[2][w];
+  for (int i = 0; i < 2; ++i) {
+    s[i] = row16_sum(at < W ? lds[0][i * W + at] : 0.0);
+    g[i] = row16_sum(at < W ? lds[1][i * W + at] : 0.0);
+    n[i] = row16_sum(at < W ? lds[2][i * W + at] : 0.0);
   }
   if (a.length_normalize) {
 #pragma unroll
@@ -671,9 +673,20 @@ __global__ __launch_bounds__(1024) void k_policy_stats(PolicyArgs a, int64_t row
     k += (double)t.x * (double)t.z;
     c += (double)t.x * (double)t.w;
   }
-  p = block_sum<1024>(p, lds[0]);
-  k = block_sum<1024>(k, lds[1]);
-  c = block_sum<1024>(c, lds[2]);
+  p = wave_sum(p);
+  k = wave_sum(k);
+  c = wave_sum(c);
+  const int wave = threadIdx.x / 64, lane = threadIdx.x & 63;
+  if (lane == 0) {
+    lds[0][wave] = p;
+    lds[1][wave] = k;
+    lds[2][wave] = c;
+  }
+  __syncthreads();
+  if (wave) return;
+  p = row16_sum(lane < 16 ? lds[0][lane] : 0.0);
+  k = row16_sum(lane < 16 ? lds[1][lane] : 0.0);
+  c = row16_sum(lane < 16 ? lds[2][lane] : 0.0);
   if (threadIdx.x == 0) {
     a.stats[0] = (float)(a.kl_coef == 0.0f ? p : p + (double)a.kl_coef * k);
     a.stats[1] = (float)p;

@@ -92,35 +92,53 @@ __device__ __forceinline__ u32x4 vec_neg_inf() {
 // primitives): lane i takes lane i - 1, 2, 4 or 8 of its row of 16, then rows
 // 1 and 3 take lane 15 of the row before them and rows 2 and 3 lane 31.  Lanes
 // without a source take `none`.  After the six steps lane 63 has combined all.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float lane_move(float none, float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(none), __float_as_int(v), CTRL,
-                                                    ROWS, 0xF, false));
-}
 constexpr int kRowShr1 = 0x111, kRowShr2 = 0x112, kRowShr4 = 0x114, kRowShr8 = 0x118;
 constexpr int kRowBcast15 = 0x142, kRowBcast31 = 0x143;
 
-__device__ __forceinline__ float last_lane(float v) {
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+template <int CTRL, int ROWS, typename V>
+__device__ __forceinline__ V lane_move(V none, V v) {
+  constexpr int W = sizeof(V) / 4;
+  struct Words {
+    int w[W];
+  };
+  const Words n = __builtin_bit_cast(Words, none);
+  Words x = __builtin_bit_cast(Words, v);
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+    x.w[i] = __builtin_amdgcn_update_dpp(n.w[i], x.w[i], CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(V, x);
+}
+template <typename V>
+__device__ __forceinline__ V from_lane(V v, int lane) {
+  constexpr int W = sizeof(V) / 4;
+  struct Words {
+    int w[W];
+  };
+  Words x = __builtin_bit_cast(Words, v);
+#pragma unroll
+  for (int i = 0; i < W; ++i) x.w[i] = __builtin_amdgcn_readlane(x.w[i], lane);
+  return __builtin_bit_cast(V, x);
 }
 
 // Sum over a wavefront, all of whose lanes are active; every lane gets it.
-__device__ __forceinline__ float wave_sum(float v) {
-  v += lane_move<kRowShr1, 0xF>(0.0f, v);
-  v += lane_move<kRowShr2, 0xF>(0.0f, v);
-  v += lane_move<kRowShr4, 0xF>(0.0f, v);
-  v += lane_move<kRowShr8, 0xF>(0.0f, v);
-  v += lane_move<kRowBcast15, 0xA>(0.0f, v);
-  v += lane_move<kRowBcast31, 0xC>(0.0f, v);
-  return last_lane(v);
+template <typename V>
+__device__ __forceinline__ V wave_sum(V v) {
+  v += lane_move<kRowShr1, 0xF>(V(0), v);
+  v += lane_move<kRowShr2, 0xF>(V(0), v);
+  v += lane_move<kRowShr4, 0xF>(V(0), v);
+  v += lane_move<kRowShr8, 0xF>(V(0), v);
+  v += lane_move<kRowBcast15, 0xA>(V(0), v);
+  v += lane_move<kRowBcast31, 0xC>(V(0), v);
+  return from_lane(v, 63);
 }
 // Sum over the first 16 lanes; every lane gets it.
-__device__ __forceinline__ float row16_sum(float v) {
-  v += lane_move<kRowShr1, 0xF>(0.0f, v);
-  v += lane_move<kRowShr2, 0xF>(0.0f, v);
-  v += lane_move<kRowShr4, 0xF>(0.0f, v);
-  v += lane_move<kRowShr8, 0xF>(0.0f, v);
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 15));
+template <typename V>
+__device__ __forceinline__ V row16_sum(V v) {
+  v += lane_move<kRowShr1, 0xF>(V(0), v);
+  v += lane_move<kRowShr2, 0xF>(V(0), v);
+  v += lane_move<kRowShr4, 0xF>(V(0), v);
+  v += lane_move<kRowShr8, 0xF>(V(0), v);
+  return from_lane(v, 15);
 }
 __device__ __forceinline__ float wave_max(float v) {
   const float none = -__builtin_huge_valf();
@@ -130,14 +148,7 @@ __device__ __forceinline__ float wave_max(float v) {
   v = fmaxf(v, lane_move<kRowShr8, 0xF>(none, v));
   v = fmaxf(v, lane_move<kRowBcast15, 0xA>(none, v));
   v = fmaxf(v, lane_move<kRowBcast31, 0xC>(none, v));
-  return last_lane(v);
-}
-// Other types.
-template <typename V>
-__device__ __forceinline__ V wave_sum(V v) {
-#pragma unroll
-  for (int half = 32; half >= 1; half >>= 1) v += __shfl_xor(v, half, 64);
-  return v;
+  return from_lane(v, 63);
 }
 
 // Sum over a workgroup of THREADS; every thread gets it.  `lds` holds one
