@@ -12,7 +12,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _lib
-from ._lib import _check, _need
+from ._lib import _check
 
 QLORA_BF16, QLORA_F32 = 0, 1
 QLORA_NORM_LAYER, QLORA_NORM_RMS = 0, 1
@@ -61,9 +61,17 @@ def declare(L: ctypes.CDLL) -> None:
                                     _I64, _P, sz, _P]
 
 
+# A call on a few rows is bound by host time: the helpers below stay cheap.
+
 def _raw_stream(device) -> int:
     """The current stream's handle, without building a Stream object."""
     return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _need(t: torch.Tensor, dtype, shape, name):
+    """_lib._need, with the passing case first."""
+    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda):
+        _lib._need(t, dtype, shape, name)
 
 
 def _addr(t: Optional[torch.Tensor]):
@@ -75,6 +83,14 @@ def _out(t, shape, dtype, device, name):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
     _need(t, dtype, shape, name)
+    return t
+
+
+def _out_like(t, X, name):
+    """The same for an output of X's type and shape."""
+    if t is None:
+        return torch.empty_like(X)
+    _need(t, X.dtype, X.shape, name)
     return t
 
 
@@ -119,14 +135,15 @@ def qlora_norm_fwd(X: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Te
     given; H may be X or the residual.  save_stats=False leaves out what only
     the backward needs."""
     ty = _matrix_type(X, "X")
-    M, d = X.shape
+    shape = X.shape
+    M, d = shape
     dev = X.device
-    _need(X, X.dtype, (M, d), "X")
+    _need(X, X.dtype, shape, "X")
     wt = _weight_type(gamma, beta, d)
     if residual is not None:
-        _need(residual, X.dtype, (M, d), "residual")
-        H = _out(H, (M, d), X.dtype, dev, "H")
-    Y = _out(Y, (M, d), X.dtype, dev, "Y")
+        _need(residual, X.dtype, shape, "residual")
+        H = _out_like(H, X, "H")
+    Y = _out_like(Y, X, "Y")
     mean = rstd = None
     if save_stats:
         rstd = torch.empty(M, dtype=torch.float32, device=dev)
@@ -154,10 +171,11 @@ def qlora_norm_bwd(dY: torch.Tensor, H: torch.Tensor, gamma: torch.Tensor,
     """Backward of qlora_norm_fwd for its H, mean and rstd; dH is the gradient
     that reaches H past the norm.  dX may be dY or dH."""
     ty = _matrix_type(H, "H")
-    M, d = H.shape
+    shape = H.shape
+    M, d = shape
     dev = H.device
-    _need(H, H.dtype, (M, d), "H")
-    _need(dY, H.dtype, (M, d), "dY")
+    _need(H, H.dtype, shape, "H")
+    _need(dY, H.dtype, shape, "dY")
     wt = _weight_type(gamma, None, d)
     _need(rstd, torch.float32, (M,), "rstd")
     if kind == QLORA_NORM_LAYER:
@@ -165,8 +183,8 @@ def qlora_norm_bwd(dY: torch.Tensor, H: torch.Tensor, gamma: torch.Tensor,
             raise ValueError("mean: the layer norm's backward needs it")
         _need(mean, torch.float32, (M,), "mean")
     if dH is not None:
-        _need(dH, H.dtype, (M, d), "dH")
-    dX = _out(dX, (M, d), H.dtype, dev, "dX")
+        _need(dH, H.dtype, shape, "dH")
+    dX = _out_like(dX, H, "dX")
     ws = None
     if need_dgamma or need_dbeta:
         dgamma = _out(dgamma, (d,), torch.float32, dev, "dgamma") if need_dgamma else None

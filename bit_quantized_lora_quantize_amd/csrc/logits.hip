@@ -534,15 +534,28 @@ __device__ __forceinline__ Place policy_place(const LogitsArgs& l, const PolicyA
   return {seq, token_mean ? 1.0f / (float)n : 1.0f / ((float)a.seqs * (float)n)};
 }
 
+// N terms of a row to its gradient: -g p = c term, and g more at the target.
+template <int N>
+__device__ __forceinline__ void scale_terms(float c, float g, int t, int first, float* f) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) f[j] *= c;
+  if ((uint32_t)(t - first) < (uint32_t)N) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[j] += first + j == t ? g : 0.0f;
+  }
+}
+
 // Loss and gradient of one row in one pass: the row's logits stay in
 // registers (E of them a thread, as FP32 terms once the maximum is known),
-// so they are read once and their exponentials taken once.  dlogits NULL:
-// the loss alone, with the same bits.
-template <typename T, int THREADS, int E, int MIN_WAVES>
+// so they are read once and their exponentials taken once.  A longer row
+// leaves L more vectors a thread in LDS, as they came; their exponentials are
+// taken twice.  dlogits NULL: the loss alone, with the same bits.
+template <typename T, int THREADS, int E, int L, int MIN_WAVES>
 __global__ __launch_bounds__(THREADS, MIN_WAVES) void k_policy(LogitsArgs l, PolicyArgs a,
                                                                T* dlogits, int64_t ldd) {
   constexpr int N = kVec<T>, V = E / N;
   __shared__ float lds_m[THREADS / 64], lds_s[THREADS / 64], lds_g;
+  extern __shared__ u32x4 far[];                  // [L][THREADS]: each thread its own
   const int64_t row = blockIdx.x;
   const int vocab = (int)l.vocab, nvec = vocab / N;
   const int64_t t = l.targets[row];
@@ -571,9 +584,27 @@ __global__ __launch_bounds__(THREADS, MIN_WAVES) void k_policy(LogitsArgs l, Pol
   }
   const int last = nvec * N + (int)threadIdx.x;   // the last, partial vector
   float el = last < vocab ? to_f32(x[last]) : -kInf;
-  Place at{-1, 0.0f};
-  if (lead) at = policy_place(l, a, row);   // while the logits arrive
   float e[E], m = el;
+  if constexpr (L > 0) {
+    u32x4 r[L];
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      const int v = (V + i) * THREADS + (int)threadIdx.x;
+      r[i] = vec_neg_inf<T>();
+      if (v < nvec) r[i] = load_vec(x + (int64_t)v * N);
+    }
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      if ((V + i) * THREADS >= nvec) break;       // none of the workgroup's
+      far[i * THREADS + threadIdx.x] = r[i];
+      float f[N];
+      unpack<T>(r[i], f);
+#pragma unroll
+      for (int j = 0; j < N; ++j) m = fmaxf(m, f[j]);
+    }
+  }
+  Place at{-1, 0.0f};
+  if (lead) at = policy_place(l, a, row);         // while the logits arrive
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     unpack<T>(d[i], e + i * N);
@@ -588,6 +619,14 @@ __global__ __launch_bounds__(THREADS, MIN_WAVES) void k_policy(LogitsArgs l, Pol
     unpack<T>(d[i], e + i * N);
 #pragma unroll
     for (int j = 0; j < N; ++j) s += e[i * N + j] = term(e[i * N + j], m, k);
+  }
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    if ((V + i) * THREADS >= nvec) break;
+    float f[N];
+    unpack<T>(far[i * THREADS + threadIdx.x], f);
+#pragma unroll
+    for (int j = 0; j < N; ++j) s += term(f[j], m, k);
   }
   s = block_sum<THREADS>(s, lds_s);
   if (lead) {
@@ -609,13 +648,18 @@ __global__ __launch_bounds__(THREADS, MIN_WAVES) void k_policy(LogitsArgs l, Pol
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int v = i * THREADS + (int)threadIdx.x;
-    float* f = e + i * N;
+    scale_terms<N>(c, g, (int)t, v * N, e + i * N);
+    if (v < nvec) store_vec_once(out + (int64_t)v * N, pack<T>(e + i * N));
+  }
 #pragma unroll
-    for (int j = 0; j < N; ++j) f[j] *= c;
-    if ((uint32_t)((int)t - v * N) < (uint32_t)N) {
+  for (int i = 0; i < L; ++i) {
+    const int v = (V + i) * THREADS + (int)threadIdx.x;
+    if ((V + i) * THREADS >= nvec) break;
+    float f[N];
+    unpack<T>(far[i * THREADS + threadIdx.x], f);
 #pragma unroll
-      for (int j = 0; j < N; ++j) f[j] += v * N + j == (int)t ? g : 0.0f;
-    }
+    for (int j = 0; j < N; ++j) f[j] = term(f[j], m, k);
+    scale_terms<N>(c, g, (int)t, v * N, f);
     if (v < nvec) store_vec_once(out + (int64_t)v * N, pack<T>(f));
   }
   if (last < vocab) from_f32(el * c + (last == (int)t ? g : 0.0f), out[last]);
@@ -763,25 +807,28 @@ hipError_t launch_preference(const LogitsArgs& l, const PreferenceArgs& a, RowSt
   return launch_dlogits(l, stat, nullptr, a.dlogp, dlogits, ldd, st);
 }
 
-// E logits a thread and THREADS a row, the smallest that hold the row.
+template <typename T, int THREADS, int E, int L, int MIN_WAVES>
+static void policy_held(const LogitsArgs& l, const PolicyArgs& a, T* dlogits, int64_t ldd,
+                        hipStream_t st) {
+  hipLaunchKernelGGL((k_policy<T, THREADS, E, L, MIN_WAVES>), dim3((unsigned)l.rows),
+                     dim3(THREADS), (size_t)L * THREADS * 16, st, l, a, dlogits, ldd);
+}
+
+// The fewest threads, and logits a thread, that hold the row.
 template <typename T>
 static void policy_by_width(const LogitsArgs& l, const PolicyArgs& a, T* dlogits, int64_t ldd,
                             hipStream_t st) {
-  const dim3 grid((unsigned)l.rows);
-  if (l.vocab <= 512)
-    hipLaunchKernelGGL((k_policy<T, 64, 8, 8>), grid, dim3(64), 0, st, l, a, dlogits, ldd);
-  else if (l.vocab <= 2048)
-    hipLaunchKernelGGL((k_policy<T, 64, 32, 6>), grid, dim3(64), 0, st, l, a, dlogits, ldd);
-  else if (l.vocab <= 8192)
-    hipLaunchKernelGGL((k_policy<T, 256, 32, 8>), grid, dim3(256), 0, st, l, a, dlogits, ldd);
-  else if (l.vocab <= 16384)
-    hipLaunchKernelGGL((k_policy<T, 512, 32, 8>), grid, dim3(512), 0, st, l, a, dlogits, ldd);
-  else if (l.vocab <= 32768)
-    hipLaunchKernelGGL((k_policy<T, 1024, 32, 8>), grid, dim3(1024), 0, st, l, a, dlogits, ldd);
-  else if (l.vocab <= 65536)
-    hipLaunchKernelGGL((k_policy<T, 1024, 64, 4>), grid, dim3(1024), 0, st, l, a, dlogits, ldd);
+  constexpr int kFar = 65536 + 8 * 1024 * kVec<T>;   // with 128 KB of LDS
+  if (l.vocab <= 512) policy_held<T, 64, 8, 0, 8>(l, a, dlogits, ldd, st);
+  else if (l.vocab <= 2048) policy_held<T, 64, 32, 0, 6>(l, a, dlogits, ldd, st);
+  else if (l.vocab <= 8192) policy_held<T, 256, 32, 0, 8>(l, a, dlogits, ldd, st);
+  else if (l.vocab <= 16384) policy_held<T, 512, 32, 0, 8>(l, a, dlogits, ldd, st);
+  else if (l.vocab <= 32768) policy_held<T, 1024, 32, 0, 8>(l, a, dlogits, ldd, st);
+  else if (l.vocab <= 65536) policy_held<T, 1024, 64, 0, 4>(l, a, dlogits, ldd, st);
+  else if (l.vocab <= kFar) policy_held<T, 1024, 64, 8, 4>(l, a, dlogits, ldd, st);
   else
-    hipLaunchKernelGGL((k_policy_long<T, 1024>), grid, dim3(1024), 0, st, l, a, dlogits, ldd);
+    hipLaunchKernelGGL((k_policy_long<T, 1024>), dim3((unsigned)l.rows), dim3(1024), 0, st, l, a,
+                       dlogits, ldd);
 }
 
 hipError_t launch_policy(const LogitsArgs& l, const PolicyArgs& args, void* dlogits, int64_t ldd,
