@@ -55,15 +55,15 @@ __device__ __forceinline__ MaxSum block_join(MaxSum v, float k, MaxSum* lds) {
 template <typename T, int THREADS>
 __device__ __forceinline__ MaxSum stream_row(const T* x, int vocab, float k, int lane) {
   constexpr int N = kVec<T>, kU = 32 / N;
-  const int nvec = vocab / N;
+  const RowCut<T> cut(x, vocab, lane);
   MaxSum r{-kInf, 0.0f};
-  for (int v0 = lane; v0 < nvec; v0 += THREADS * kU) {
+  for (int v0 = lane; v0 < cut.nvec; v0 += THREADS * kU) {
     u32x4 d[kU];
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       const int v = v0 + i * THREADS;
       d[i] = vec_neg_inf<T>();
-      if (v < nvec) d[i] = load_vec(x + (int64_t)v * N);
+      if (v < cut.nvec) d[i] = load_vec(x + cut.at(v));
     }
     float f[N], m = r.m;
 #pragma unroll
@@ -82,9 +82,8 @@ __device__ __forceinline__ MaxSum stream_row(const T* x, int vocab, float k, int
     }
     r = {m, s};
   }
-  const int i = nvec * N + lane;   // the last, partial vector
-  if (i < vocab) {
-    const float f = to_f32(x[i]), m = fmaxf(r.m, f), z = shift(m);
+  if (cut.edge >= 0) {
+    const float f = to_f32(x[cut.edge]), m = fmaxf(r.m, f), z = shift(m);
     r = {m, r.s * term(r.m, z, k) + term(f, z, k)};
   }
   return r;
@@ -150,10 +149,9 @@ __device__ __forceinline__ void fill_row(T* out, int vocab, float value, int lan
 #pragma unroll
   for (int j = 0; j < N; ++j) f[j] = value;
   const u32x4 v = pack<T>(f);
-  const int nvec = vocab / N;
-  for (int i = lane; i < nvec; i += THREADS) store_vec_once(out + (int64_t)i * N, v);
-  const int i = nvec * N + lane;
-  if (i < vocab) from_f32(value, out[i]);
+  const RowCut<T> cut(out, vocab, lane);
+  for (int i = lane; i < cut.nvec; i += THREADS) store_vec_once(out + cut.at(i), v);
+  if (cut.edge >= 0) from_f32(value, out[cut.edge]);
 }
 
 // A row's gradient by THREADS threads, from its logits read again.
@@ -161,26 +159,26 @@ template <typename T, int THREADS>
 __device__ __forceinline__ void grad_row(const T* x, T* out, int vocab, const RowGrad& q,
                                          int lane) {
   constexpr int N = kVec<T>, kU = 2;
-  const int nvec = vocab / N;
-  for (int v0 = lane; v0 < nvec; v0 += THREADS * kU) {
+  const RowCut<T> cut(x, vocab, lane);
+  for (int v0 = lane; v0 < cut.nvec; v0 += THREADS * kU) {
     u32x4 d[kU];
 #pragma unroll
     for (int i = 0; i < kU; ++i)
-      if (v0 + i * THREADS < nvec) d[i] = load_vec(x + (int64_t)(v0 + i * THREADS) * N);
+      if (v0 + i * THREADS < cut.nvec) d[i] = load_vec(x + cut.at(v0 + i * THREADS));
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
-      if (v0 + i * THREADS >= nvec) continue;
+      if (v0 + i * THREADS >= cut.nvec) continue;
+      const int first = cut.at(v0 + i * THREADS);
       float f[N];
       unpack<T>(d[i], f);
-      grad_terms<N>(q, (v0 + i * THREADS) * N, f);
-      store_vec_once(out + (int64_t)(v0 + i * THREADS) * N, pack<T>(f));
+      grad_terms<N>(q, first, f);
+      store_vec_once(out + first, pack<T>(f));
     }
   }
-  const int i = nvec * N + lane;
-  if (i < vocab) {
-    float f = to_f32(x[i]);
-    grad_terms<1>(q, i, &f);
-    from_f32(f, out[i]);
+  if (cut.edge >= 0) {
+    float f = to_f32(x[cut.edge]);
+    grad_terms<1>(q, cut.edge, &f);
+    from_f32(f, out[cut.edge]);
   }
 }
 
@@ -200,7 +198,10 @@ __global__ __launch_bounds__(256) void k_dlogits(LogitsArgs l, const RowStat* st
   const uint32_t r = blockIdx.x / chunks;
   const int64_t row = last - r;
   const int v = (int)((blockIdx.x - r * chunks) * 256 + threadIdx.x);
-  const int vocab = (int)l.vocab, nvec = vocab / N, rest = vocab - nvec * N;
+  const T* x = static_cast<const T*>(l.logits) + row * l.ld;
+  // the threads past the vectors take the single elements
+  const int vocab = (int)l.vocab, nvec = RowCut<T>(x, vocab, 0).nvec;
+  const RowCut<T> cut(x, vocab, v - nvec);
   const int64_t t = l.targets[row];
   RowGrad q;
   q.k = l.scale * kLog2e;
@@ -222,22 +223,20 @@ __global__ __launch_bounds__(256) void k_dlogits(LogitsArgs l, const RowStat* st
     float f[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) f[j] = to_f32(e);
-    if (v < nvec) store_vec_once(out + (int64_t)v * N, pack<T>(f));
-    else if (v - nvec < rest) out[(int64_t)nvec * N + (v - nvec)] = e;
+    if (v < nvec) store_vec_once(out + cut.at(v), pack<T>(f));
+    else if (cut.edge >= 0) out[cut.edge] = e;
     return;
   }
   q.t = (int)t;
-  const T* x = static_cast<const T*>(l.logits) + row * l.ld;
   if (v < nvec) {
     float f[N];
-    unpack<T>(load_vec_once(x + (int64_t)v * N), f);
-    grad_terms<N>(q, v * N, f);
-    store_vec_once(out + (int64_t)v * N, pack<T>(f));
-  } else if (v - nvec < rest) {          // the last, partial vector: a thread per element
-    const int i = nvec * N + (v - nvec);
-    float f = to_f32(x[i]);
-    grad_terms<1>(q, i, &f);
-    from_f32(f, out[i]);
+    unpack<T>(load_vec_once(x + cut.at(v)), f);
+    grad_terms<N>(q, cut.at(v), f);
+    store_vec_once(out + cut.at(v), pack<T>(f));
+  } else if (cut.edge >= 0) {
+    float f = to_f32(x[cut.edge]);
+    grad_terms<1>(q, cut.edge, &f);
+    from_f32(f, out[cut.edge]);
   }
 }
 
@@ -557,7 +556,7 @@ __global__ __launch_bounds__(THREADS, MIN_WAVES) void k_policy(LogitsArgs l, Pol
   __shared__ float lds_m[THREADS / 64], lds_s[THREADS / 64], lds_g;
   extern __shared__ u32x4 far[];                  // [L][THREADS]: each thread its own
   const int64_t row = blockIdx.x;
-  const int vocab = (int)l.vocab, nvec = vocab / N;
+  const int vocab = (int)l.vocab;
   const int64_t t = l.targets[row];
   T* out = dlogits ? dlogits + row * ldd : nullptr;
   const bool lead = threadIdx.x < 64;
@@ -574,16 +573,17 @@ __global__ __launch_bounds__(THREADS, MIN_WAVES) void k_policy(LogitsArgs l, Pol
     return;
   }
   const T* x = static_cast<const T*>(l.logits) + row * l.ld;
+  const RowCut<T> cut(x, vocab, threadIdx.x);
+  const int nvec = cut.nvec;
   const float xt = to_f32(x[t]);
   u32x4 d[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int v = i * THREADS + (int)threadIdx.x;
     d[i] = vec_neg_inf<T>();
-    if (v < nvec) d[i] = load_vec(x + (int64_t)v * N);
+    if (v < nvec) d[i] = load_vec(x + cut.at(v));
   }
-  const int last = nvec * N + (int)threadIdx.x;   // the last, partial vector
-  float el = last < vocab ? to_f32(x[last]) : -kInf;
+  float el = cut.edge >= 0 ? to_f32(x[cut.edge]) : -kInf;
   float e[E], m = el;
   if constexpr (L > 0) {
     u32x4 r[L];
@@ -591,7 +591,7 @@ __global__ __launch_bounds__(THREADS, MIN_WAVES) void k_policy(LogitsArgs l, Pol
     for (int i = 0; i < L; ++i) {
       const int v = (V + i) * THREADS + (int)threadIdx.x;
       r[i] = vec_neg_inf<T>();
-      if (v < nvec) r[i] = load_vec(x + (int64_t)v * N);
+      if (v < nvec) r[i] = load_vec(x + cut.at(v));
     }
 #pragma unroll
     for (int i = 0; i < L; ++i) {
@@ -648,8 +648,8 @@ __global__ __launch_bounds__(THREADS, MIN_WAVES) void k_policy(LogitsArgs l, Pol
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int v = i * THREADS + (int)threadIdx.x;
-    scale_terms<N>(c, g, (int)t, v * N, e + i * N);
-    if (v < nvec) store_vec_once(out + (int64_t)v * N, pack<T>(e + i * N));
+    scale_terms<N>(c, g, (int)t, cut.at(v), e + i * N);
+    if (v < nvec) store_vec_once(out + cut.at(v), pack<T>(e + i * N));
   }
 #pragma unroll
   for (int i = 0; i < L; ++i) {
@@ -659,10 +659,10 @@ __global__ __launch_bounds__(THREADS, MIN_WAVES) void k_policy(LogitsArgs l, Pol
     unpack<T>(far[i * THREADS + threadIdx.x], f);
 #pragma unroll
     for (int j = 0; j < N; ++j) f[j] = term(f[j], m, k);
-    scale_terms<N>(c, g, (int)t, v * N, f);
-    if (v < nvec) store_vec_once(out + (int64_t)v * N, pack<T>(f));
+    scale_terms<N>(c, g, (int)t, cut.at(v), f);
+    if (v < nvec) store_vec_once(out + cut.at(v), pack<T>(f));
   }
-  if (last < vocab) from_f32(el * c + (last == (int)t ? g : 0.0f), out[last]);
+  if (cut.edge >= 0) from_f32(el * c + (cut.edge == (int)t ? g : 0.0f), out[cut.edge]);
 }
 
 // The same where a row does not fit the registers: it is read a second time,
@@ -761,7 +761,10 @@ hipError_t launch_logp(const LogitsArgs& l, float* logp, float* lse, RowStat* st
 template <typename T>
 static void dlogits_rows(const LogitsArgs& l, const RowStat* stat, const float* lse,
                          const float* dlogp, T* dlogits, int64_t ldd, hipStream_t st) {
-  const int64_t units = l.vocab / kVec<T> + l.vocab % kVec<T>;
+  // vectors and single elements of a row; one more of these where whole
+  // vectors start at its second element
+  const int64_t rest = l.vocab % kVec<T>;
+  const int64_t units = l.vocab / kVec<T> + (rest ? rest : sizeof(T) == 2 ? kVec<T> - 1 : 0);
   const int64_t chunks = (units + 255) / 256;
   // a launch's threads are counted in 32 bits: at most 2^22 workgroups each
   const int64_t per = std::max<int64_t>(1, (int64_t(1) << 22) / chunks);

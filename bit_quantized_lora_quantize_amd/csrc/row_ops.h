@@ -1,11 +1,12 @@
 // row_ops.h -- element access and reductions shared by the kernels that work
 // on rows (norm.hip, logits.hip).
 //
-// Rows are taken in 16-byte vectors from their first element on, wherever it
-// lies: a row of odd length starts anywhere, and one wavefront's access still
-// covers 1 KB without gaps.  Measured on 65536-element BF16 rows, a copy runs at
-// 5.9-6.2 TB/s at any alignment; reading alone loses 17 % where the elements
-// are not 4-byte aligned (5.8 to 4.8 TB/s).
+// Rows are taken in 16-byte vectors that need not be aligned: a row of odd
+// length starts anywhere, and one wavefront's access still covers 1 KB without
+// gaps.  Measured on 65536-element BF16 rows, a read and a copy run as fast at
+// 4-byte alignment as at 16-byte; off it, a read loses 17 % (5.8 to 4.8 TB/s).
+// Rows of logits therefore start their vectors at the first 4-byte boundary
+// (RowCut).
 #pragma once
 
 #include "qlora.h"
@@ -80,6 +81,22 @@ __device__ __forceinline__ u32x4 pack(const float* f) {
   }
   return v;
 }
+
+// A row of `size` elements as `nvec` vectors from element `head` on and single
+// elements for the first lanes: `edge` is the calling lane's, -1 without.
+template <typename T>
+struct RowCut {
+  int head, nvec, edge;
+  __device__ __forceinline__ RowCut(const T* p, int size, int lane) {
+    head = sizeof(T) == 2 ? (int)(reinterpret_cast<uintptr_t>(p) >> 1 & 1) : 0;
+    const int body = size - head;
+    nvec = body / kVec<T>;
+    const int tail = body - nvec * kVec<T>;
+    edge = lane < tail ? size - tail + lane : (lane == tail && head ? 0 : -1);
+  }
+  // The first element of vector v.
+  __device__ __forceinline__ int at(int v) const { return head + v * kVec<T>; }
+};
 
 // A vector of -inf.
 template <typename T>
