@@ -817,18 +817,26 @@ static void policy_held(const LogitsArgs& l, const PolicyArgs& a, T* dlogits, in
                      dim3(THREADS), (size_t)L * THREADS * 16, st, l, a, dlogits, ldd);
 }
 
-// The fewest threads, and logits a thread, that hold the row.
+// The fewest threads, and logits a thread, that hold the row; steps that
+// leave fewer of them idle were kept where they measured faster (us at 2^30
+// bytes or less of logits): 128 threads at 3200 BF16 98 against 124, at 4000
+// FP32 110 against 103; 768 at 20000 BF16 124 against 140; 48 logits at 36000
+// BF16 242 against 260.
 template <typename T>
 static void policy_by_width(const LogitsArgs& l, const PolicyArgs& a, T* dlogits, int64_t ldd,
                             hipStream_t st) {
   constexpr int kFar = 65536 + 8 * 1024 * kVec<T>;   // with 128 KB of LDS
-  if (l.vocab <= 512) policy_held<T, 64, 8, 0, 8>(l, a, dlogits, ldd, st);
-  else if (l.vocab <= 2048) policy_held<T, 64, 32, 0, 6>(l, a, dlogits, ldd, st);
-  else if (l.vocab <= 8192) policy_held<T, 256, 32, 0, 8>(l, a, dlogits, ldd, st);
-  else if (l.vocab <= 16384) policy_held<T, 512, 32, 0, 8>(l, a, dlogits, ldd, st);
-  else if (l.vocab <= 32768) policy_held<T, 1024, 32, 0, 8>(l, a, dlogits, ldd, st);
-  else if (l.vocab <= 65536) policy_held<T, 1024, 64, 0, 4>(l, a, dlogits, ldd, st);
-  else if (l.vocab <= kFar) policy_held<T, 1024, 64, 8, 4>(l, a, dlogits, ldd, st);
+  const int64_t v = l.vocab;
+  if (v <= 512) policy_held<T, 64, 8, 0, 8>(l, a, dlogits, ldd, st);
+  else if (v <= 2048) policy_held<T, 64, 32, 0, 6>(l, a, dlogits, ldd, st);
+  else if (v <= 4096 && sizeof(T) == 2) policy_held<T, 128, 32, 0, 8>(l, a, dlogits, ldd, st);
+  else if (v <= 8192) policy_held<T, 256, 32, 0, 8>(l, a, dlogits, ldd, st);
+  else if (v <= 16384) policy_held<T, 512, 32, 0, 8>(l, a, dlogits, ldd, st);
+  else if (v <= 24576) policy_held<T, 768, 32, 0, 6>(l, a, dlogits, ldd, st);
+  else if (v <= 32768) policy_held<T, 1024, 32, 0, 8>(l, a, dlogits, ldd, st);
+  else if (v <= 49152) policy_held<T, 1024, 48, 0, 4>(l, a, dlogits, ldd, st);
+  else if (v <= 65536) policy_held<T, 1024, 64, 0, 4>(l, a, dlogits, ldd, st);
+  else if (v <= kFar) policy_held<T, 1024, 64, 8, 4>(l, a, dlogits, ldd, st);
   else
     hipLaunchKernelGGL((k_policy_long<T, 1024>), dim3((unsigned)l.rows), dim3(1024), 0, st, l, a,
                        dlogits, ldd);
