@@ -630,7 +630,7 @@ size_t qlora_preference_workspace_bytes(int64_t rows);
  * dlogits is the gradient of weight * loss; where the clipped branch is the
  * larger one the policy term has no gradient, at equality the unclipped
  * branch's counts.  The gradient comes from the same pass over the logits
- * as the loss: they are read once where a row fits a workgroup's registers.
+ * as the loss: rows of up to 131072 BF16 or 98304 FP32 logits are read once.
  *   offsets     int64 [sequences + 1] as in qlora_preference_loss
  *   advantages  FP32 [rows] with per_token, else FP32 [sequences]
  *   old_logp, ref_logp  FP32 [rows] or NULL (ref_logp NULL needs kl_coef 0,

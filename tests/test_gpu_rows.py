@@ -151,3 +151,26 @@ def test_preference_over_many_pairs(pairs, longest, dtype):
     assert ref.max_err(o.loss, loss.detach()) <= 5e-5 * max(1.0, float(loss.detach().max()))
     tol = 5e-5 + (ref.BF16_TOL if dtype == torch.bfloat16 else 0.0)
     assert_close("dlogits", ref.f64(o.dlogits), x.grad, tol, tol)
+
+
+@pytest.mark.parametrize("rows", [7, 1500])
+def test_policy_without_sequences_needs_no_offsets(rows):
+    """No sequences and no offsets array: no row counts, whichever way a row's
+    place is found."""
+    import ctypes
+
+    from bit_quantized_lora_quantize_amd import _train
+    z, t, _, _ = _batch(1, [rows], 50, torch.float32, 0)
+    td = t.to(DEV)
+    l = _train._Logits(z.data_ptr(), td.data_ptr(), rows, 50, 50, IGNORE, q.QLORA_F32, 1.0)
+    par = _train._Policy(q.QLORA_POLICY_TOKEN_MEAN, 0, 0.2, 0.2, 0.0, 1.0)
+    logp, stats = torch.empty(rows, device=DEV), torch.ones(4, device=DEV)
+    d, n = torch.ones_like(z), q.qlora_policy_workspace_bytes(rows, 0)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    st = q.lib().qlora_policy_loss(ctypes.byref(l), None, 0, None, None, None, ctypes.byref(par),
+                                   logp.data_ptr(), stats.data_ptr(), d.data_ptr(), 50,
+                                   ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    assert (stats == 0).all() and (d == 0).all()
+    assert torch.equal(logp, q.qlora_token_logp(z, td)[0]) or \
+        ref.max_err(logp, q.qlora_token_logp(z, td)[0]) <= 5e-6
