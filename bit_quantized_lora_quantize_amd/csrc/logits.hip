@@ -778,10 +778,11 @@ hipError_t launch_logp(const LogitsArgs& l, float* logp, float* lse, RowStat* st
 template <typename T>
 static void dlogits_rows(const LogitsArgs& l, const RowStat* stat, const float* lse,
                          const float* dlogp, T* dlogits, int64_t ldd, hipStream_t st) {
-  // vectors and single elements of a row; one more of these where whole
-  // vectors start at its second element
+  // vectors and single elements of a row (RowCut), at most: whole vectors that
+  // start at the second element leave more of these
   const int64_t rest = l.vocab % kVec<T>;
-  const int64_t units = l.vocab / kVec<T> + (rest ? rest : sizeof(T) == 2 ? kVec<T> - 1 : 0);
+  const bool shifted = sizeof(T) == 2 && ((reinterpret_cast<uintptr_t>(l.logits) >> 1 | l.ld) & 1);
+  const int64_t units = l.vocab / kVec<T> + (rest || !shifted ? rest : kVec<T> - 1);
   const int64_t chunks = (units + 255) / 256;
   // a launch's threads are counted in 32 bits: at most 2^22 workgroups each
   const int64_t per = std::max<int64_t>(1, (int64_t(1) << 22) / chunks);
