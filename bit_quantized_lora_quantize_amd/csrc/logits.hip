@@ -106,7 +106,7 @@ __device__ __forceinline__ void seq_rows(const int64_t* offsets, int64_t s, int6
 
 // One workgroup per row, in one pass.  Long rows take 1024 threads: their
 // loads of a whole round are in flight at once, and two workgroups a compute
-// unit cover each other's reductions (8349 x 131072 BF16, a quarter ignored:
+// unit cover each other's reductions (8348 x 131072 BF16, a quarter ignored:
 // 263 us, 6.2 TB/s; with 512 and 256 threads the whole loss takes 1 and 2 %
 // longer).  FP32 maxima and sums.
 template <typename T, int THREADS>
@@ -193,7 +193,7 @@ __device__ __forceinline__ void grad_row(const T* x, T* out, int vocab, const Ro
 }
 
 // One vector of one row per thread, `chunks` workgroups a row: many small
-// workgroups stream best (608 us for 8349 x 131072 BF16, 6.3 TB/s).  Rounded
+// workgroups stream best (608 us for 8348 x 131072 BF16, 6.3 TB/s).  Rounded
 // once, to the logits' type.
 //
 // A forward pass has just read the same logits, and the last-level cache (256
@@ -201,7 +201,7 @@ __device__ __forceinline__ void grad_row(const T* x, T* out, int vocab, const Ro
 // neither the gradient's stores nor this second and last read stay in the
 // caches, where they would drive out logits yet to be read.  Against plain
 // accesses: 129 to 97 us at 2048 x 32000 FP32 with a quarter of the rows
-// ignored, 943 to 880 us at 8349 x 131072 BF16 (893 us first row to last).
+// ignored, 943 to 880 us at 8348 x 131072 BF16 (893 us first row to last).
 template <typename T>
 __global__ __launch_bounds__(256) void k_dlogits(LogitsArgs l, const RowStat* stat,
                                                  const float* lse, const float* dlogp, T* dlogits,
