@@ -209,10 +209,10 @@ def _logits(logits, targets, ignore_index, scale):
     vocabulary); their elements are contiguous."""
     ty = _matrix_type(logits, "logits")
     rows, vocab = logits.shape
-    ld = logits.stride(0)
+    ld, inner = logits.stride()
     if rows <= 1:
         ld = max(ld, vocab)
-    if not logits.is_cuda or (vocab > 1 and logits.stride(1) != 1) or ld < vocab:
+    if not logits.is_cuda or (vocab > 1 and inner != 1) or ld < vocab:
         raise ValueError(f"logits: expected rows of contiguous elements on the GPU, got strides "
                          f"{logits.stride()} on {logits.device}")
     _need(targets, torch.int64, (rows,), "targets")
@@ -233,6 +233,13 @@ def _dlogits(dlogits, logits, l):
                          f"elements in a row, got {dlogits.dtype} {tuple(dlogits.shape)} with "
                          f"strides {dlogits.stride()}")
     return dlogits, ldd
+
+
+def _with_workspace(nbytes: int, device, *counts: int):
+    """A workspace and FP32 outputs of `counts` values, in one allocation (a
+    small batch's call spends a good part of its time on allocations)."""
+    n = (nbytes + 63) // 64 * 16
+    return torch.empty(n + sum(counts), dtype=torch.float32, device=device).split((n, *counts))
 
 
 def qlora_token_logp(logits: torch.Tensor, targets: torch.Tensor,
@@ -297,20 +304,18 @@ def qlora_preference_loss(logits: torch.Tensor, targets: torch.Tensor, offsets: 
         _need(ref_logp, torch.float32, (l.rows,), "ref_logp")
     par = _Preference(kind, 1 if length_normalize else 0, beta, label_smoothing, margin,
                       1.0 / max(1, pairs) if weight is None else weight)
-    logp = torch.empty(l.rows, dtype=torch.float32, device=dev)
-    seq_logp = torch.empty(2 * pairs, dtype=torch.float32, device=dev)
-    loss = torch.empty(pairs, dtype=torch.float32, device=dev)
+    nbytes = qlora_preference_workspace_bytes(l.rows) if workspace is None else 0
+    ws, logp, seq_logp, loss = _with_workspace(nbytes, dev, l.rows, 2 * pairs, pairs)
+    if workspace is not None:
+        ws, nbytes = workspace, workspace.numel()
     ldd = 0
     if need_grad:
         dlogits, ldd = _dlogits(dlogits, logits, l)
     else:
         dlogits = None
-    ws = workspace
-    if ws is None:
-        ws = _lib._workspace(qlora_preference_workspace_bytes(l.rows), dev)
     _check(_lib.lib().qlora_preference_loss(l, offsets.data_ptr(), pairs, _addr(ref_logp), par,
                                             logp.data_ptr(), seq_logp.data_ptr(), loss.data_ptr(),
-                                            _addr(dlogits), ldd, ws.data_ptr(), ws.numel(),
+                                            _addr(dlogits), ldd, ws.data_ptr(), nbytes,
                                             _raw_stream(dev)), "qlora_preference_loss")
     return PreferenceOut(loss, seq_logp, logp, dlogits)
 
@@ -349,18 +354,17 @@ def qlora_policy_loss(logits: torch.Tensor, targets: torch.Tensor, offsets: torc
     if ref_logp is not None:
         _need(ref_logp, torch.float32, (l.rows,), "ref_logp")
     par = _Policy(reduction, 1 if per_token else 0, clip_low, clip_high, kl_coef, weight)
-    logp = torch.empty(l.rows, dtype=torch.float32, device=dev)
-    stats = torch.empty(4, dtype=torch.float32, device=dev)
+    nbytes = qlora_policy_workspace_bytes(l.rows, seqs) if workspace is None else 0
+    ws, logp, stats = _with_workspace(nbytes, dev, l.rows, 4)
+    if workspace is not None:
+        ws, nbytes = workspace, workspace.numel()
     ldd = 0
     if need_grad:
         dlogits, ldd = _dlogits(dlogits, logits, l)
     else:
         dlogits = None
-    ws = workspace
-    if ws is None:
-        ws = _lib._workspace(qlora_policy_workspace_bytes(l.rows, seqs), dev)
     _check(_lib.lib().qlora_policy_loss(l, offsets.data_ptr(), seqs, advantages.data_ptr(),
                                         _addr(old_logp), _addr(ref_logp), par, logp.data_ptr(),
                                         stats.data_ptr(), _addr(dlogits), ldd, ws.data_ptr(),
-                                        ws.numel(), _raw_stream(dev)), "qlora_policy_loss")
+                                        nbytes, _raw_stream(dev)), "qlora_policy_loss")
     return PolicyOut(stats, logp, dlogits)
