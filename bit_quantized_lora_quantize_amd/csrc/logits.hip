@@ -192,6 +192,48 @@ __device__ __forceinline__ void grad_row(const T* x, T* out, int vocab, const Ro
   }
 }
 
+// One vector of a row, or one of its single elements (v past the vectors).
+template <typename T>
+struct GradAt {
+  const T* x;
+  int v, nvec;
+  RowCut<T> cut;
+  __device__ __forceinline__ GradAt(const LogitsArgs& l, int64_t row, int v_)
+      : x(static_cast<const T*>(l.logits) + row * l.ld),
+        v(v_),
+        nvec(RowCut<T>(x, (int)l.vocab, 0).nvec),
+        cut(x, (int)l.vocab, v_ - nvec) {}
+};
+// Its gradient, by one thread: q of its row but for the target t.
+template <typename T>
+__device__ __forceinline__ void grad_vec(const LogitsArgs& l, const GradAt<T>& at, int64_t t,
+                                         RowGrad q, T* out) {
+  constexpr int N = kVec<T>;
+  const RowCut<T>& cut = at.cut;
+  const bool none = t == l.ignore || q.g == 0.0f;
+  if (none || t < 0 || t >= l.vocab) {   // zeros, or NaN for a bad target
+    T e;
+    from_f32(none ? 0.0f : __builtin_nanf(""), e);
+    float f[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[j] = to_f32(e);
+    if (at.v < at.nvec) store_vec_once(out + cut.at(at.v), pack<T>(f));
+    else if (cut.edge >= 0) out[cut.edge] = e;
+    return;
+  }
+  q.t = (int)t;
+  if (at.v < at.nvec) {
+    float f[N];
+    unpack<T>(load_vec_once(at.x + cut.at(at.v)), f);
+    grad_terms<N>(q, cut.at(at.v), f);
+    store_vec_once(out + cut.at(at.v), pack<T>(f));
+  } else if (cut.edge >= 0) {
+    float f = to_f32(at.x[cut.edge]);
+    grad_terms<1>(q, cut.edge, &f);
+    from_f32(f, out[cut.edge]);
+  }
+}
+
 // One vector of one row per thread, `chunks` workgroups a row: many small
 // workgroups stream best (608 us for 8348 x 131072 BF16, 6.3 TB/s).  Rounded
 // once, to the logits' type.
@@ -206,14 +248,9 @@ template <typename T>
 __global__ __launch_bounds__(256) void k_dlogits(LogitsArgs l, const RowStat* stat,
                                                  const float* lse, const float* dlogp, T* dlogits,
                                                  int64_t ldd, int64_t last, uint32_t chunks) {
-  constexpr int N = kVec<T>;
   const uint32_t r = blockIdx.x / chunks;
   const int64_t row = last - r;
-  const int v = (int)((blockIdx.x - r * chunks) * 256 + threadIdx.x);
-  const T* x = static_cast<const T*>(l.logits) + row * l.ld;
-  // the threads past the vectors take the single elements
-  const int vocab = (int)l.vocab, nvec = RowCut<T>(x, vocab, 0).nvec;
-  const RowCut<T> cut(x, vocab, v - nvec);
+  const GradAt<T> at(l, row, (int)((blockIdx.x - r * chunks) * 256 + threadIdx.x));
   const int64_t t = l.targets[row];
   RowGrad q;
   q.k = l.scale * kLog2e;
@@ -227,40 +264,20 @@ __global__ __launch_bounds__(256) void k_dlogits(LogitsArgs l, const RowStat* st
     q.m = e / l.scale;
     q.c = (e - q.m * l.scale) * kLog2e;
   }
-  T* out = dlogits + row * ldd;
-  const bool none = t == l.ignore || q.g == 0.0f;
-  if (none || t < 0 || t >= l.vocab) {   // zeros, or NaN for a bad target
-    T e;
-    from_f32(none ? 0.0f : __builtin_nanf(""), e);
-    float f[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) f[j] = to_f32(e);
-    if (v < nvec) store_vec_once(out + cut.at(v), pack<T>(f));
-    else if (cut.edge >= 0) out[cut.edge] = e;
-    return;
-  }
-  q.t = (int)t;
-  if (v < nvec) {
-    float f[N];
-    unpack<T>(load_vec_once(x + cut.at(v)), f);
-    grad_terms<N>(q, cut.at(v), f);
-    store_vec_once(out + cut.at(v), pack<T>(f));
-  } else if (cut.edge >= 0) {
-    float f = to_f32(x[cut.edge]);
-    grad_terms<1>(q, cut.edge, &f);
-    from_f32(f, out[cut.edge]);
-  }
+  grad_vec(l, at, t, q, dlogits + row * ldd);
 }
 
 // Sums, loss and slope of one pair, half of a workgroup per sequence: the
-// sequences' sums in FP64.  Returns the gradient of a log-probability of each
-// of the two sequences, to every thread.
-struct PairSlope {
-  float c[2];
+// sequences' sums in FP64.  To every thread: the gradient of a log-probability
+// of each of the two sequences, the loss, and the sequences' log-probabilities.
+struct PairLoss {
+  float c[2], loss;
+  double s[2];
 };
-__device__ __forceinline__ PairSlope pair_loss(const PreferenceArgs& a, int64_t p,
-                                               double (*lds)[kPrefThreads / 64]) {
-  constexpr int kSide = kPrefThreads / 2, W = kSide / 64;
+template <int THREADS>
+__device__ __forceinline__ PairLoss pair_loss(const PreferenceArgs& a, int64_t p,
+                                              double (*lds)[THREADS / 64]) {
+  constexpr int kSide = THREADS / 2, W = kSide / 64;
   const int side = threadIdx.x / kSide;
   int64_t b, e;
   seq_rows(a.offsets, p + side * a.pairs, a.rows, b, e);
@@ -317,17 +334,19 @@ __device__ __forceinline__ PairSlope pair_loss(const PreferenceArgs& a, int64_t 
     loss = off * off;
     slope = 2.0f * off;
   }
-  if (threadIdx.x == 0) {
-    a.loss[p] = loss;
-    a.seq_logp[p] = (float)s[0];
-    a.seq_logp[p + a.pairs] = (float)s[1];
-  }
-  PairSlope r{{slope * a.weight, -slope * a.weight}};
+  PairLoss r{{slope * a.weight, -slope * a.weight}, loss, {s[0], s[1]}};
   if (a.length_normalize) {
     r.c[0] /= (float)n[0];
     r.c[1] /= (float)n[1];
   }
   return r;
+}
+
+// A pair's outputs, by one thread.
+__device__ __forceinline__ void write_pair(const PreferenceArgs& a, int64_t p, const PairLoss& r) {
+  a.loss[p] = r.loss;
+  a.seq_logp[p] = (float)r.s[0];
+  a.seq_logp[p + a.pairs] = (float)r.s[1];
 }
 
 // The rows before and after all sequences, [0, begin) and [end, rows).
@@ -360,7 +379,8 @@ __global__ __launch_bounds__(kPrefThreads) void k_preference(PreferenceArgs a) {
       for (int64_t i = o.end + threadIdx.x; i < a.rows; i += kPrefThreads) a.dlogp[i] = 0.0f;
   }
   if (a.pairs == 0) return;
-  const PairSlope s = pair_loss(a, p, lds);
+  const PairLoss s = pair_loss<kPrefThreads>(a, p, lds);
+  if (threadIdx.x == 0) write_pair(a, p, s);
   if (!a.dlogp) return;
   constexpr int kSide = kPrefThreads / 2;
   const int side = threadIdx.x / kSide;
@@ -368,6 +388,52 @@ __global__ __launch_bounds__(kPrefThreads) void k_preference(PreferenceArgs a) {
   seq_rows(a.offsets, p + side * a.pairs, a.rows, b, e);
   const float c = side ? s.c[1] : s.c[0];
   for (int64_t i = b + threadIdx.x % kSide; i < e; i += kSide) a.dlogp[i] = c;
+}
+
+// The sequence that a row lies in, -1 for none, by a full wavefront.
+__device__ __forceinline__ int sequence_of(const int64_t* offsets, int64_t seqs, int64_t rows,
+                                           int64_t row) {
+  if (seqs == 0) return -1;   // no offsets to read
+  const int lane = threadIdx.x & 63;
+  int at = 0;                 // offsets at or before the row
+  for (int64_t j = 0; j <= seqs; j += 64) {
+    const bool before = j + lane <= seqs && offsets[j + lane] <= row;
+    at += __popcll(__ballot(before));
+  }
+  if (at < 1 || at > seqs) return -1;
+  int64_t b, e;
+  seq_rows(offsets, at - 1, rows, b, e);
+  return row >= b && row < e ? at - 1 : -1;
+}
+
+// Losses and gradients of a batch of few rows in one launch, once its
+// log-probabilities are there: the first workgroups write a pair's loss each,
+// every other one finds its row's pair, sums it again and takes one vector of
+// the row per thread.
+template <typename T>
+__global__ __launch_bounds__(256) void k_pairs_dlogits(LogitsArgs l, PreferenceArgs a,
+                                                       const RowStat* stat, T* dlogits,
+                                                       int64_t ldd, uint32_t chunks) {
+  __shared__ double lds[3][4];
+  if ((int64_t)blockIdx.x < a.pairs) {
+    const PairLoss r = pair_loss<256>(a, blockIdx.x, lds);
+    if (threadIdx.x == 0) write_pair(a, blockIdx.x, r);
+    return;
+  }
+  const uint32_t i = blockIdx.x - (uint32_t)a.pairs;
+  const int64_t row = i / chunks;
+  const GradAt<T> at(l, row, (int)((i - (uint32_t)row * chunks) * 256 + threadIdx.x));
+  const int64_t t = l.targets[row];
+  const RowStat s = stat[row];
+  RowGrad q{0.0f, s.max, s.logsum * kLog2e, l.scale * kLog2e, 0};
+  if (t != l.ignore) {
+    const int seq = sequence_of(a.offsets, 2 * a.pairs, a.rows, row);
+    if (seq >= 0) {
+      const PairLoss r = pair_loss<256>(a, seq < a.pairs ? seq : seq - a.pairs, lds);
+      q.g = (seq < a.pairs ? r.c[0] : r.c[1]) * l.scale;
+    }
+  }
+  grad_vec(l, at, t, q, dlogits + row * ldd);
 }
 
 // Log-probability of one row by one wavefront.
@@ -439,7 +505,8 @@ __global__ __launch_bounds__(kPrefThreads) void k_preference_small(LogitsArgs l,
   for (int64_t i = wave; i < n; i += W)
     wave_logp<T>(l, i < first ? b[0] + i : b[1] + (i - first), logp, stat);
   __syncthreads();
-  const PairSlope s = pair_loss(a, p, lds);
+  const PairLoss s = pair_loss<kPrefThreads>(a, p, lds);
+  if (threadIdx.x == 0) write_pair(a, p, s);
   if (!dlogits) return;
   for (int64_t i = wave; i < n; i += W) {
     const int64_t row = i < first ? b[0] + i : b[1] + (i - first);
@@ -518,17 +585,11 @@ __device__ __forceinline__ Place policy_place(const LogitsArgs& l, const PolicyA
       n = a.count[seq];
     }
   } else {
-    if (a.seqs == 0 || l.targets[row] == l.ignore) return {-1, 0.0f};   // no offsets to read
-    int at = 0;   // offsets at or before the row
-    for (int64_t j = 0; j <= a.seqs; j += 64) {
-      const bool before = j + lane <= a.seqs && a.offsets[j + lane] <= row;
-      at += __popcll(__ballot(before));
-    }
-    seq = at - 1;
-    if (seq < 0 || seq >= a.seqs) return {-1, 0.0f};
+    if (l.targets[row] == l.ignore) return {-1, 0.0f};
+    seq = sequence_of(a.offsets, a.seqs, l.rows, row);
+    if (seq < 0) return {-1, 0.0f};
     int64_t b, e;
     seq_rows(a.offsets, seq, l.rows, b, e);
-    if (row < b || row >= e) return {-1, 0.0f};
     if (token_mean) {
       const Outside o = outside_rows(a.offsets, a.seqs, l.rows);
       b = o.begin;
@@ -775,15 +836,21 @@ hipError_t launch_logp(const LogitsArgs& l, float* logp, float* lse, RowStat* st
   return hipGetLastError();
 }
 
+// Workgroups of 256 threads that hold a row's vectors and single elements
+// (RowCut), at most: whole vectors that start at the second element leave more
+// of these.
 template <typename T>
-static void dlogits_rows(const LogitsArgs& l, const RowStat* stat, const float* lse,
-                         const float* dlogp, T* dlogits, int64_t ldd, hipStream_t st) {
-  // vectors and single elements of a row (RowCut), at most: whole vectors that
-  // start at the second element leave more of these
+static int64_t grad_chunks(const LogitsArgs& l) {
   const int64_t rest = l.vocab % kVec<T>;
   const bool shifted = sizeof(T) == 2 && ((reinterpret_cast<uintptr_t>(l.logits) >> 1 | l.ld) & 1);
   const int64_t units = l.vocab / kVec<T> + (rest || !shifted ? rest : kVec<T> - 1);
-  const int64_t chunks = (units + 255) / 256;
+  return (units + 255) / 256;
+}
+
+template <typename T>
+static void dlogits_rows(const LogitsArgs& l, const RowStat* stat, const float* lse,
+                         const float* dlogp, T* dlogits, int64_t ldd, hipStream_t st) {
+  const int64_t chunks = grad_chunks<T>(l);
   // a launch's threads are counted in 32 bits: at most 2^22 workgroups each
   const int64_t per = std::max<int64_t>(1, (int64_t(1) << 22) / chunks);
   for (int64_t end = l.rows; end > 0; end -= per) {
@@ -801,33 +868,48 @@ hipError_t launch_dlogits(const LogitsArgs& l, const RowStat* stat, const float*
   return hipGetLastError();
 }
 
-// Pairs of at most about 64 rows and 2^17 logits (on average) are done sooner
-// by a workgroup each in one launch than by three launches: 14.8 against 20.5
-// us a call at 8 x 500 to 32 x 500 logits a pair, 18.2 against 20.4 at
-// 32 x 4000, but 26.8 against 20.6 at 128 x 500.  The lengths are not known
-// here; a batch of 2^20 logits at most bounds what one pair can hold.
+// A call on few rows is bound by its launches.  Pairs of at most about 32 rows
+// and 2^16 logits (on average) take one: a workgroup each, 13 us a call against
+// 16 with two at 30 x 1000.  The lengths are not known here; a batch of 2^20
+// logits at most bounds what one pair can hold.
 static bool small_pairs(const LogitsArgs& l, int64_t pairs) {
-  return l.rows <= 64 * pairs &&
-         l.rows * l.vocab <= std::min<int64_t>(pairs << 17, int64_t(1) << 20);
+  return l.rows <= 32 * pairs &&
+         l.rows * l.vocab <= std::min<int64_t>(pairs << 16, int64_t(1) << 20);
+}
+// Batches of up to kFewRows rows and kFewBlocks workgroups of gradients take
+// two, every workgroup summing its row's pair again: 16 us a call against 18.8
+// with three (512 rows x 4000); at 8192 workgroups 26.8 against 23.7.
+constexpr int64_t kFewRows = 2048, kFewBlocks = 4096;
+
+template <typename T>
+static hipError_t preference_as(const LogitsArgs& l, const PreferenceArgs& a, RowStat* stat,
+                                float* logp, T* dlogits, int64_t ldd, hipStream_t st) {
+  const dim3 grid((unsigned)std::max<int64_t>(a.pairs, 1));
+  if (small_pairs(l, a.pairs)) {
+    hipLaunchKernelGGL(k_preference_small<T>, grid, dim3(kPrefThreads), 0, st, l, a, stat, logp,
+                       dlogits, ldd);
+    return hipGetLastError();
+  }
+  const hipError_t e = launch_logp(l, logp, nullptr, stat, st);
+  if (e != hipSuccess) return e;
+  const int64_t chunks = grad_chunks<T>(l);
+  if (l.rows <= kFewRows && l.rows * chunks <= kFewBlocks && a.pairs <= kFewRows) {
+    const int64_t blocks = a.pairs + (dlogits ? l.rows * chunks : 0);
+    if (blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL(k_pairs_dlogits<T>, dim3((unsigned)blocks), dim3(256), 0, st, l, a, stat,
+                       dlogits, ldd, (uint32_t)chunks);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(k_preference, grid, dim3(kPrefThreads), 0, st, a);
+  if (!dlogits) return hipGetLastError();
+  return launch_dlogits(l, stat, nullptr, a.dlogp, dlogits, ldd, st);
 }
 
 hipError_t launch_preference(const LogitsArgs& l, const PreferenceArgs& a, RowStat* stat,
                              float* logp, void* dlogits, int64_t ldd, hipStream_t st) {
-  const dim3 grid((unsigned)std::max<int64_t>(a.pairs, 1));
-  if (small_pairs(l, a.pairs)) {
-    if (l.type == QLORA_BF16)
-      hipLaunchKernelGGL(k_preference_small<uint16_t>, grid, dim3(kPrefThreads), 0, st, l, a, stat,
-                         logp, static_cast<uint16_t*>(dlogits), ldd);
-    else
-      hipLaunchKernelGGL(k_preference_small<float>, grid, dim3(kPrefThreads), 0, st, l, a, stat,
-                         logp, static_cast<float*>(dlogits), ldd);
-    return hipGetLastError();
-  }
-  hipError_t e = launch_logp(l, logp, nullptr, stat, st);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_preference, grid, dim3(kPrefThreads), 0, st, a);
-  if (!dlogits) return hipGetLastError();
-  return launch_dlogits(l, stat, nullptr, a.dlogp, dlogits, ldd, st);
+  if (l.type == QLORA_BF16)
+    return preference_as(l, a, stat, logp, static_cast<uint16_t*>(dlogits), ldd, st);
+  return preference_as(l, a, stat, logp, static_cast<float*>(dlogits), ldd, st);
 }
 
 template <typename T, int THREADS, int E, int L, int MIN_WAVES>
