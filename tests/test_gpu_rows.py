@@ -174,3 +174,42 @@ def test_policy_without_sequences_needs_no_offsets(rows):
     assert (stats == 0).all() and (d == 0).all()
     assert torch.equal(logp, q.qlora_token_logp(z, td)[0]) or \
         ref.max_err(logp, q.qlora_token_logp(z, td)[0]) <= 5e-6
+
+
+def test_captured_calls_replay_like_eager_ones():
+    """A graph of the norms and losses, replayed several times over new inputs
+    with eager work between, gives the eager calls' bits every time."""
+    rows, width, vocab = 600, 1032, 2051
+    X, R = _draw(21, (rows, width), torch.bfloat16), _draw(22, (rows, width), torch.bfloat16)
+    gamma = _draw(23, (width,), torch.float32, 0.2, 1.0)
+    z, t, _, g = _batch(24, [200, 100, 180, 120], vocab, torch.bfloat16, 1)
+    z = z.contiguous()
+    td, off = t.to(DEV), torch.tensor([0, 200, 300, 480, 600], device=DEV)
+    adv = torch.randn(4, generator=g).to(DEV)
+    old = torch.full((rows,), -3.0, device=DEV)
+
+    def calls():
+        n = q.qlora_norm_fwd(X, gamma, kind=q.QLORA_NORM_RMS, residual=R)
+        b = q.qlora_norm_bwd(n.Y, n.H, gamma, None, n.rstd, kind=q.QLORA_NORM_RMS)
+        p = q.qlora_preference_loss(z, td, off, ref_logp=old)
+        c = q.qlora_policy_loss(z, td, off, adv, old_logp=old, ref_logp=old, kl_coef=0.1)
+        return [n.Y, n.H, b.dX, b.dgamma, p.loss, p.logp, p.dlogits, c.stats, c.dlogits]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls()                                  # the library is loaded before the capture
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = calls()
+    for turn in range(4):
+        X.copy_(_draw(30 + turn, (rows, width), torch.bfloat16))
+        z.copy_(_draw(40 + turn, (rows, vocab), torch.bfloat16, 2.0))
+        old.fill_(-7.0 - turn)
+        want = [w.clone() for w in calls()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for h, w in zip(held, want):
+            assert torch.equal(h, w), turn
