@@ -282,12 +282,28 @@ __device__ __forceinline__ PairLoss pair_loss(const PreferenceArgs& a, int64_t p
   int64_t b, e;
   seq_rows(a.offsets, p + side * a.pairs, a.rows, b, e);
   double vs = 0.0, vg = 0.0, vn = 0.0;
-  for (int64_t i = b + threadIdx.x % kSide; i < e; i += kSide) {
-    const float lp = a.logp[i], rf = a.ref ? a.ref[i] : 0.0f;
-    if (a.targets[i] == a.ignore) continue;
-    vs += (double)lp;
-    vg += (double)lp - (double)rf;
-    vn += 1.0;
+  constexpr int U = 4;   // rows a thread loads together
+  for (int64_t i0 = b + threadIdx.x % kSide; i0 < e; i0 += kSide * U) {
+    float lp[U], rf[U];
+    int64_t t[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = i0 + u * kSide;
+      lp[u] = rf[u] = 0.0f;
+      t[u] = a.ignore;
+      if (i < e) {
+        lp[u] = a.logp[i];
+        t[u] = a.targets[i];
+        if (a.ref) rf[u] = a.ref[i];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (t[u] == a.ignore) continue;
+      vs += (double)lp[u];
+      vg += (double)lp[u] - (double)rf[u];
+      vn += 1.0;
+    }
   }
   vs = wave_sum(vs);
   vg = wave_sum(vg);
