@@ -169,7 +169,8 @@ def qlora_norm_bwd(dY: torch.Tensor, H: torch.Tensor, gamma: torch.Tensor,
                    dbeta: Optional[torch.Tensor] = None,
                    workspace: Optional[torch.Tensor] = None) -> NormGrads:
     """Backward of qlora_norm_fwd for its H, mean and rstd; dH is the gradient
-    that reaches H past the norm.  dX may be dY or dH."""
+    that reaches H past the norm.  dX may be dY or dH.  need_dbeta is for the
+    layer norm alone."""
     ty = _matrix_type(H, "H")
     shape = H.shape
     M, d = shape

@@ -125,6 +125,7 @@ int qlora_norm_bwd(int kind, int type, const void* dY, const void* H, const void
   if ((kind != QLORA_NORM_LAYER && kind != QLORA_NORM_RMS) || !type_ok(type) || !type_ok(w_type))
     return QLORA_ERR_SHAPE;
   if (M < 0 || M > kMaxTokens || d < 1 || d > kMaxLinearDim) return QLORA_ERR_SHAPE;
+  if (kind == QLORA_NORM_RMS && dbeta) return QLORA_ERR_SHAPE;
   const bool weights = dgamma || dbeta;
   if (M == 0 && !weights) return QLORA_OK;
   if (M > 0 && (!dY || !H || !gamma || !rstd || !dX || (kind == QLORA_NORM_LAYER && !mean)))

@@ -513,8 +513,9 @@ int qlora_norm_fwd(int kind, int type, const void *X, const void *R, int64_t M,
  *   dH      [M, d] of `type` or NULL
  *   mean    FP32 [M] (LAYER), rstd FP32 [M]: from the forward
  *   dX      [M, d] output of `type` (may be dY or dH)
- *   dgamma  FP32 [d] or NULL, dbeta FP32 [d] or NULL: overwritten (M = 0
- *           writes zeros).  With both NULL (frozen norm) no workspace is used.
+ *   dgamma  FP32 [d] or NULL, dbeta FP32 [d] or NULL (RMS: NULL, else
+ *           QLORA_ERR_SHAPE): overwritten (M = 0 writes zeros).  With both
+ *           NULL (frozen norm) no workspace is used.
  * workspace (16B) >= qlora_norm_workspace_bytes(M, d) when dgamma or dbeta
  * is given.  Sums over rows are taken in a fixed order: deterministic.
  */

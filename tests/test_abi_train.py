@@ -184,3 +184,10 @@ def test_binding_refuses_tensors_it_cannot_describe(L):
                 lambda: q.qlora_policy_loss(x, t, off, torch.ones(2))):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_rms_norm_backward_has_no_beta(L):
+    """An RMS norm takes no beta, so its gradient is refused as the forward refuses beta."""
+    assert _bwd(L, kind=1, mean=None) == ESHAPE
+    assert _bwd(L, kind=1, mean=None, dgamma=None) == ESHAPE
+    assert _bwd(L, kind=1, mean=None, dY=None, dbeta=None) == ENULL
