@@ -655,15 +655,19 @@ __global__ __launch_bounds__(THREADS, MIN_WAVES) void k_policy(LogitsArgs l, Pol
   T* out = dlogits ? dlogits + row * ldd : nullptr;
   const bool lead = threadIdx.x < 64;
   if (t == l.ignore || t < 0 || t >= l.vocab) {
-    const float lp = t == l.ignore ? 0.0f : __builtin_nanf("");
+    const bool bad = t != l.ignore;
+    const float lp = bad ? __builtin_nanf("") : 0.0f;
     if (lead) {
       const Place at = policy_place(l, a, row);
       if (threadIdx.x == 0) {
         a.logp[row] = lp;
         a.terms[row] = policy_row(a, row, at.seq, at.w, lp).terms;
+        lds_g = at.seq < 0 ? 0.0f : lp;
       }
     }
-    if (out) fill_row<T, THREADS>(out, vocab, lp, threadIdx.x);
+    if (!out) return;
+    if (bad) __syncthreads();                     // NaN only in a sequence
+    fill_row<T, THREADS>(out, vocab, bad ? lds_g : 0.0f, threadIdx.x);
     return;
   }
   const T* x = static_cast<const T*>(l.logits) + row * l.ld;
@@ -786,7 +790,7 @@ __global__ __launch_bounds__(THREADS) void k_policy_long(LogitsArgs l, PolicyArg
       const PolicyRow o = policy_row(a, row, at.seq, at.w, lp);
       a.logp[row] = lp;
       a.terms[row] = o.terms;
-      lds_g = skip ? lp : o.dlogp * l.scale;
+      lds_g = !skip ? o.dlogp * l.scale : at.seq < 0 ? 0.0f : lp;
     }
   }
   if (!out) return;

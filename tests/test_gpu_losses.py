@@ -384,3 +384,30 @@ def test_losses_on_another_stream():
     st.synchronize()
     assert torch.equal(a.dlogits, c.dlogits) and torch.equal(b.dlogits, d.dlogits)
     assert torch.equal(a.loss, c.loss) and torch.equal(b.stats, d.stats)
+
+
+@pytest.mark.parametrize("rows,vocab", [(12, 700), (12, 4099), (1100, 700), (300, 9000),
+                                        (2100, 900), (12, 70001), (6, 100003)])
+def test_bad_targets_outside_the_sequences_have_no_gradient(rows, vocab):
+    """A row that no sequence holds gets a zero gradient, whatever its target;
+    in a sequence a bad target gives NaN."""
+    z, t = _logits(31, rows, vocab, torch.float32)
+    t[[0, -1]] = torch.tensor([vocab, -7])
+    t = t.to(DEV)
+    off = torch.tensor([1, rows // 2, rows - 1], device=DEV)
+    adv = torch.ones(2, device=DEV)
+    for run in (lambda: q.qlora_preference_loss(z, t, off),
+                lambda: q.qlora_policy_loss(z, t, off, adv),
+                lambda: q.qlora_policy_loss(z, t, off, adv, reduction=q.QLORA_POLICY_SEQUENCE_MEAN)):
+        o = run()
+        assert (o.dlogits[[0, -1]] == 0).all()
+        assert torch.isfinite(o.dlogits).all() and (o.dlogits[1:-1] != 0).any(1).all()
+        assert torch.isnan(o.logp[[0, -1]]).all() and torch.isfinite(o.logp[1:-1]).all()
+        assert torch.isfinite(o[0]).all()
+    t[1] = vocab
+    o = q.qlora_policy_loss(z, t, off, adv)
+    assert torch.isnan(o.dlogits[1]).all() and (o.dlogits[0] == 0).all()
+    assert torch.isfinite(o.stats[0])          # on-policy: the ratio is 1 whatever the row
+    o = q.qlora_policy_loss(z, t, off, adv, old_logp=torch.zeros(rows, device=DEV))
+    assert torch.isnan(o.dlogits[1]).all() and (o.dlogits[0] == 0).all()
+    assert torch.isnan(o.stats[0])
