@@ -75,6 +75,7 @@ PreferencePlan plan_preference(int64_t rows, void* ws) {
 
 struct PolicyPlan {
   int32_t* count;
+  int32_t* total;
   int32_t* row_seq;
   float4* terms;
   size_t bytes;
@@ -83,6 +84,7 @@ PolicyPlan plan_policy(int64_t rows, int64_t seqs, void* ws) {
   PolicyPlan p{};
   Carver c(ws);
   p.count = c.take<int32_t>(seqs);
+  p.total = c.take<int32_t>(1);
   p.row_seq = c.take<int32_t>(rows);
   p.terms = c.take<float4>(rows);
   p.bytes = c.off + 256;
@@ -256,7 +258,8 @@ int qlora_policy_loss(const qlora_logits_t* l, const int64_t* offsets, int64_t s
   const PolicyArgs a{offsets,        advantages,     old_logp,       ref_logp,
                      sequences,      par->reduction, par->per_token, par->clip_low,
                      par->clip_high, par->kl_coef,   par->weight,    logp,
-                     stats,          p.count,        p.row_seq,      p.terms};
+                     stats,          p.count,        p.total,        p.row_seq,
+                     p.terms};
   return hip_status(launch_policy(logits_args(l), a, dlogits, ldd,
                                   static_cast<hipStream_t>(stream)));
 }

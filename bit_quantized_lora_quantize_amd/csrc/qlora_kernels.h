@@ -553,6 +553,7 @@ struct PolicyArgs {
   float* logp;
   float* stats;            // [4]
   int32_t* count;          // [seqs] rows of each sequence that count
+  int32_t* total;          // [1] their sum
   int32_t* row_seq;        // [rows] sequence of each row, -1 without one
   float4* terms;           // [rows] w, policy, kl, clipped
 };

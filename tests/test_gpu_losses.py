@@ -411,3 +411,33 @@ def test_bad_targets_outside_the_sequences_have_no_gradient(rows, vocab):
     o = q.qlora_policy_loss(z, t, off, adv, old_logp=torch.zeros(rows, device=DEV))
     assert torch.isnan(o.dlogits[1]).all() and (o.dlogits[0] == 0).all()
     assert torch.isnan(o.stats[0])
+
+
+@pytest.mark.parametrize("seqs", [255, 256, 257, 700, 1500])
+def test_policy_loss_over_many_sequences(seqs):
+    """Both reductions against the per-sequence counts, where the rows' own
+    workgroups sum them and where they are summed once."""
+    rows, vocab = 1400, 300
+    z, t = _logits(41, rows, vocab, torch.float32)
+    t = _drop(t, 0.3, 5)
+    g = torch.Generator().manual_seed(6)
+    off = torch.sort(torch.randint(0, rows + 1, (seqs + 1,), generator=g)).values
+    adv = torch.randn(seqs, generator=g)
+    lp = torch.log_softmax(ref.f64(z), -1)
+    seq = torch.full((rows,), -1)
+    for s in range(seqs):
+        seq[off[s]:off[s + 1]] = s
+    counts = (t != IGNORE) & (seq >= 0)
+    n = torch.bincount(seq[counts], minlength=seqs)
+    for red in (q.QLORA_POLICY_TOKEN_MEAN, q.QLORA_POLICY_SEQUENCE_MEAN):
+        w = torch.zeros(rows, dtype=torch.float64)
+        w[counts] = (1.0 / int(counts.sum()) if red == q.QLORA_POLICY_TOKEN_MEAN
+                     else 1.0 / (seqs * n[seq[counts]].double()))
+        c = torch.zeros(rows, dtype=torch.float64)
+        c[counts] = -w[counts] * adv.double()[seq[counts]]
+        hot = torch.zeros(rows, vocab, dtype=torch.float64)
+        hot[counts, t[counts]] = 1.0
+        want = c[:, None] * (hot - lp.exp())
+        o = q.qlora_policy_loss(z, t.to(DEV), off.to(DEV), adv.to(DEV), reduction=red)
+        _close_grad(f"dlogits {seqs}", o.dlogits, want)
+        assert abs(o.stats[0].item() - float(c.sum())) <= 1e-6 * float(c.abs().sum())
