@@ -905,10 +905,12 @@ static bool small_pairs(const LogitsArgs& l, int64_t pairs) {
   return l.rows <= 32 * pairs &&
          l.rows * l.vocab <= std::min<int64_t>(pairs << 16, int64_t(1) << 20);
 }
-// Batches of up to kFewRows rows and kFewBlocks workgroups of gradients take
-// two, every workgroup summing its row's pair again: 16 us a call against 18.8
-// with three (512 rows x 4000); at 8192 workgroups 26.8 against 23.7.
-constexpr int64_t kFewRows = 2048, kFewBlocks = 4096;
+// Batches of up to kFewBlocks workgroups of gradients take two, every workgroup
+// summing its row's pair again: 14.5 us a call against 17.1 with three (128 x
+// 32000 or 2048 x 2000 BF16, 2048 workgroups); at 3072 17 us both, at 4096 19
+// to 24 against 17 to 19.  Finding a row's pair takes longer among more (256:
+// 16.1 us, 1024: no gain).
+constexpr int64_t kFewBlocks = 2048, kFewPairs = 256;
 
 template <typename T>
 static hipError_t preference_as(const LogitsArgs& l, const PreferenceArgs& a, RowStat* stat,
@@ -922,7 +924,7 @@ static hipError_t preference_as(const LogitsArgs& l, const PreferenceArgs& a, Ro
   const hipError_t e = launch_logp(l, logp, nullptr, stat, st);
   if (e != hipSuccess) return e;
   const int64_t chunks = grad_chunks<T>(l);
-  if (l.rows <= kFewRows && l.rows * chunks <= kFewBlocks && a.pairs <= kFewRows) {
+  if (l.rows * chunks <= kFewBlocks && a.pairs <= kFewPairs) {
     const int64_t blocks = a.pairs + (dlogits ? l.rows * chunks : 0);
     if (blocks == 0) return hipSuccess;
     hipLaunchKernelGGL(k_pairs_dlogits<T>, dim3((unsigned)blocks), dim3(256), 0, st, l, a, stat,
