@@ -78,6 +78,14 @@ def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _room(ws: torch.Tensor) -> int:
+    """The bytes of a caller's workspace, of whatever type."""
+    if not (ws.is_cuda and ws.is_contiguous()):
+        raise ValueError(f"workspace: expected a contiguous tensor on the GPU, got strides "
+                         f"{ws.stride()} on {ws.device}")
+    return ws.numel() * ws.element_size()
+
+
 def _out(t, shape, dtype, device, name):
     """The caller's output after a check, or a new one."""
     if t is None:
@@ -186,19 +194,21 @@ def qlora_norm_bwd(dY: torch.Tensor, H: torch.Tensor, gamma: torch.Tensor,
     if dH is not None:
         _need(dH, H.dtype, shape, "dH")
     dX = _out_like(dX, H, "dX")
-    ws = None
+    ws, nbytes = None, 0
     if need_dgamma or need_dbeta:
         dgamma = _out(dgamma, (d,), torch.float32, dev, "dgamma") if need_dgamma else None
         dbeta = _out(dbeta, (d,), torch.float32, dev, "dbeta") if need_dbeta else None
-        ws = workspace
-        if ws is None:
-            ws = _lib._workspace(qlora_norm_workspace_bytes(M, d), dev)
+        if workspace is None:
+            nbytes = qlora_norm_workspace_bytes(M, d)
+            ws = _lib._workspace(nbytes, dev)
+        else:
+            ws, nbytes = workspace, _room(workspace)
     else:
         dgamma = dbeta = None
     _check(_lib.lib().qlora_norm_bwd(kind, ty, dY.data_ptr(), H.data_ptr(), _addr(dH), M, d, wt,
                                      gamma.data_ptr(), _addr(mean), rstd.data_ptr(),
                                      dX.data_ptr(), _addr(dgamma), _addr(dbeta), _addr(ws),
-                                     0 if ws is None else ws.numel(), _raw_stream(dev)),
+                                     nbytes, _raw_stream(dev)),
            "qlora_norm_bwd")
     return NormGrads(dX, dgamma, dbeta)
 
@@ -308,7 +318,7 @@ def qlora_preference_loss(logits: torch.Tensor, targets: torch.Tensor, offsets: 
     nbytes = qlora_preference_workspace_bytes(l.rows) if workspace is None else 0
     ws, logp, seq_logp, loss = _with_workspace(nbytes, dev, l.rows, 2 * pairs, pairs)
     if workspace is not None:
-        ws, nbytes = workspace, workspace.numel()
+        ws, nbytes = workspace, _room(workspace)
     ldd = 0
     if need_grad:
         dlogits, ldd = _dlogits(dlogits, logits, l)
@@ -358,7 +368,7 @@ def qlora_policy_loss(logits: torch.Tensor, targets: torch.Tensor, offsets: torc
     nbytes = qlora_policy_workspace_bytes(l.rows, seqs) if workspace is None else 0
     ws, logp, stats = _with_workspace(nbytes, dev, l.rows, 4)
     if workspace is not None:
-        ws, nbytes = workspace, workspace.numel()
+        ws, nbytes = workspace, _room(workspace)
     ldd = 0
     if need_grad:
         dlogits, ldd = _dlogits(dlogits, logits, l)

@@ -66,3 +66,34 @@ def test_step_gradient_against_differences(example):
             p.param.add_(g, alpha=-sign * step)
     slope = (found[0] - found[1]) / (2 * step)
     assert abs(slope - norm2) <= 0.05 * norm2, (slope, norm2)
+
+
+def test_caller_workspaces():
+    """A caller's workspace of any type gives the results of one's own; one on
+    the host, strided or too small is refused."""
+    dev = torch.device("cuda:0")
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(70, 600, generator=g).to(dev)
+    t = torch.randint(0, 600, (70,), generator=g).to(dev)
+    off, adv = torch.tensor([0, 40, 70], device=dev), torch.ones(2, device=dev)
+    gamma = torch.ones(600, device=dev)
+    n = q.qlora_norm_fwd(x, gamma)
+    calls = [
+        (q.qlora_norm_workspace_bytes(70, 600),
+         lambda w: q.qlora_norm_bwd(x, n.H, gamma, n.mean, n.rstd, need_dbeta=True, workspace=w)),
+        (q.qlora_preference_workspace_bytes(70),
+         lambda w: q.qlora_preference_loss(x, t, off, workspace=w)),
+        (q.qlora_policy_workspace_bytes(70, 2),
+         lambda w: q.qlora_policy_loss(x, t, off, adv, workspace=w))]
+    for need, call in calls:
+        want = call(None)
+        for ws in (torch.empty(need, dtype=torch.uint8, device=dev),
+                   torch.empty((need + 3) // 4, dtype=torch.float32, device=dev)):
+            got = call(ws)
+            assert all(a is None and b is None or torch.equal(a, b) for a, b in zip(got, want))
+        for ws in (torch.empty(need, dtype=torch.uint8),
+                   torch.empty(2 * need, dtype=torch.uint8, device=dev)[::2]):
+            with pytest.raises(ValueError):
+                call(ws)
+        with pytest.raises(q.QloraError):
+            call(torch.empty(need - 1, dtype=torch.uint8, device=dev))
