@@ -262,7 +262,7 @@ __global__ __launch_bounds__(256) void k_dlogits(LogitsArgs l, const RowStat* st
   } else {
     const float e = lse[row];
     q.m = e / l.scale;
-    q.c = (e - q.m * l.scale) * kLog2e;
+    q.c = __builtin_fmaf(-q.m, l.scale, e) * kLog2e;   // what the quotient's rounding left
   }
   grad_vec(l, at, t, q, dlogits + row * ldd);
 }
