@@ -234,6 +234,24 @@ __device__ __forceinline__ void grad_vec(const LogitsArgs& l, const GradAt<T>& a
   }
 }
 
+// A row's gradient by one workgroup of 256 that takes its maximum and sum again.
+template <typename T>
+__device__ __forceinline__ void regrad_row(const LogitsArgs& l, int64_t row, float g, int t,
+                                           T* out) {
+  __shared__ MaxSum lds[4];
+  const T* x = static_cast<const T*>(l.logits) + row * l.ld;
+  const float k = l.scale * kLog2e;
+  const MaxSum v = block_join<256>(stream_row<T, 256>(x, (int)l.vocab, k, threadIdx.x), k, lds);
+  const RowGrad q{g, shift(v.m), logf(v.s) * kLog2e, k, t};
+  grad_row<T, 256>(x, out, (int)l.vocab, q, threadIdx.x);
+}
+
+// From this size on an FP32 lse is off by more than 2^-18, and so is every p it
+// gives; a row all at its type's lowest value would get p = 1 for every token.
+// The backward then takes the row's sum again: 117 us against 84 where all rows
+// of 2048 x 32000 FP32 need it, 1205 against 705 at 8348 x 131072 BF16.
+constexpr float kLseHeld = 128.0f;
+
 // One vector of one row per thread, `chunks` workgroups a row: many small
 // workgroups stream best (608 us for 8348 x 131072 BF16, 6.3 TB/s).  Rounded
 // once, to the logits' type.
@@ -244,7 +262,10 @@ __device__ __forceinline__ void grad_vec(const LogitsArgs& l, const GradAt<T>& a
 // caches, where they would drive out logits yet to be read.  Against plain
 // accesses: 129 to 97 us at 2048 x 32000 FP32 with a quarter of the rows
 // ignored, 943 to 880 us at 8348 x 131072 BF16 (893 us first row to last).
-template <typename T>
+//
+// HELD: the softmax comes from stat, else from lse; compiled apart, since with the
+// sum taken again in one kernel the first took 2 % longer.
+template <typename T, bool HELD>
 __global__ __launch_bounds__(256) void k_dlogits(LogitsArgs l, const RowStat* stat,
                                                  const float* lse, const float* dlogp, T* dlogits,
                                                  int64_t ldd, int64_t last, uint32_t chunks) {
@@ -255,13 +276,22 @@ __global__ __launch_bounds__(256) void k_dlogits(LogitsArgs l, const RowStat* st
   RowGrad q;
   q.k = l.scale * kLog2e;
   q.g = dlogp[row] * l.scale;
-  if (stat) {
-    const RowStat s = stat[row];
+  if constexpr (HELD) {
+    RowStat s = stat[row];
+    // waited for with the target and the slope: loaded past their test, 922 us for 879
+    asm volatile("" : "+s"(s.max), "+s"(s.logsum));
     q.m = s.max;
     q.c = s.logsum * kLog2e;
   } else {
     const float e = lse[row];
     q.m = e / l.scale;
+    if (!(fabsf(e) < kLseHeld && fabsf(q.m) < kInf) && t != l.ignore && q.g != 0.0f && t >= 0 &&
+        t < l.vocab) {
+      // the same for the whole row: one of its workgroups takes it all, another
+      // one each row (workgroup i runs on die i mod 8)
+      if (blockIdx.x - r * chunks == r % chunks) regrad_row(l, row, q.g, (int)t, dlogits + row * ldd);
+      return;
+    }
     q.c = __builtin_fmaf(-q.m, l.scale, e) * kLog2e;   // what the quotient's rounding left
   }
   grad_vec(l, at, t, q, dlogits + row * ldd);
@@ -884,8 +914,13 @@ static void dlogits_rows(const LogitsArgs& l, const RowStat* stat, const float* 
   const int64_t per = std::max<int64_t>(1, (int64_t(1) << 22) / chunks);
   for (int64_t end = l.rows; end > 0; end -= per) {
     const int64_t rows = std::min(per, end);
-    hipLaunchKernelGGL(k_dlogits<T>, dim3((unsigned)(rows * chunks)), dim3(256), 0, st, l, stat,
-                       lse, dlogp, dlogits, ldd, end - 1, (uint32_t)chunks);
+    const dim3 grid((unsigned)(rows * chunks));
+    if (stat)
+      hipLaunchKernelGGL((k_dlogits<T, true>), grid, dim3(256), 0, st, l, stat, lse, dlogp, dlogits,
+                         ldd, end - 1, (uint32_t)chunks);
+    else
+      hipLaunchKernelGGL((k_dlogits<T, false>), grid, dim3(256), 0, st, l, stat, lse, dlogp, dlogits,
+                         ldd, end - 1, (uint32_t)chunks);
   }
 }
 

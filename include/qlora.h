@@ -563,8 +563,10 @@ int qlora_token_logp(const qlora_logits_t *l, float *logp, float *lse,
  *     dlogits[i][j] = scale * dlogp[i] * ((j == target_i) - p_ij),
  *     p_ij = exp(scale * l_ij - lse_i).
  * Rows that do not count and rows with dlogp = 0 are written as zeros without
- * being read.  p carries the rounding of the FP32 lse.
- *   lse, dlogp  FP32 [rows]; dlogits [rows, ldd] output of l->type,
+ * being read.  p carries the rounding of the FP32 lse, 2^-18 at most: a row
+ * whose lse is 128 or more in size (or no number) has its sum taken again.
+ *   lse         FP32 [rows]: qlora_token_logp's, on the same logits and scale
+ *   dlogp       FP32 [rows]; dlogits [rows, ldd] output of l->type,
  *               ldd >= vocab; may be the logits' own buffer (ldd = ld).
  */
 int qlora_token_logp_bwd(const qlora_logits_t *l, const float *lse,

@@ -36,3 +36,67 @@ def test_backward_takes_the_lse_as_it_is():
     rel[:, 3] = 0.0
     say(f"  largest relative error {float(rel.abs().max()):.2e}")
     assert float(rel.abs().max()) <= 1.6e-6
+
+
+@pytest.mark.parametrize("vocab", [100, 4099, 32000, 131072])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("offset", [200.0, -1000.0, 30000.0, 1e30])
+def test_backward_of_rows_far_from_zero(vocab, dtype, offset):
+    """A common offset of a row's logits does not change its probabilities,
+    though the FP32 lse holds none of the logits' differences at 1e30.  Inputs
+    are rounded first; |scale (l - max)| is at most 16 nats at the offsets that
+    leave differences, so 2e-5 as for other rows; in BF16 one rounding more."""
+    rows = 5
+    say(f"far from zero: {rows}x{vocab} {dtype} offset {offset}")
+    z = (_draw(vocab, (rows, vocab)) + offset).to(dtype)
+    t = torch.arange(rows) * (vocab // rows)
+    t[4] = IGNORE
+    dl = _draw(2, (rows,))
+    buf = torch.empty(rows, vocab + 3, dtype=dtype, device=DEV)
+    v = buf[:, :vocab]
+    v.copy_(z)
+    _, lse = q.qlora_token_logp(v, t.to(DEV))
+    got = q.qlora_token_logp_bwd(v, t.to(DEV), lse, dl.to(DEV))
+    p = torch.softmax(z.double(), 1)
+    hot = torch.zeros_like(p)
+    hot[torch.arange(4), t[:4]] = 1.0
+    c = dl.double()[:, None] * (t != IGNORE)[:, None]
+    want = c * (hot - p)
+    # differences of 2^-8 of the offset, up to 128 nats at 30000 in BF16: the
+    # exponent's rounding grows with them, the element shrinks below 1e-30
+    bound = 2e-5 * c.abs() * p + 2.0 ** -23 * c.abs() * hot + 1e-30
+    if dtype == torch.bfloat16:
+        bound = bound + ref.BF16_TOL * (want.abs() + bound)
+    assert ((ref.f64(got) - want).abs() <= bound).all()
+    q.qlora_token_logp_bwd(v, t.to(DEV), lse, dl.to(DEV), dlogits=v)
+    assert torch.equal(v, got)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_backward_of_rows_at_the_lowest_value(dtype):
+    """A row that a mask of the type's lowest value empties is uniform, also in
+    the backward; beside one such row the others keep their values."""
+    rows, vocab = 4, 2051
+    z = _draw(3, (rows, vocab)).to(dtype)
+    z[2] = torch.finfo(dtype).min
+    t = torch.tensor([4, 5, 6, 7])
+    _, lse = q.qlora_token_logp(z.to(DEV), t.to(DEV))
+    got = ref.f64(q.qlora_token_logp_bwd(z.to(DEV), t.to(DEV), lse, torch.ones(rows, device=DEV)))
+    # (not from a log of the sum: that holds nothing beside -3e38 in 64 bits either)
+    want = -torch.softmax(z.double(), 1)
+    want[torch.arange(rows), t] += 1.0
+    tol = 2e-5 + (ref.BF16_TOL if dtype == torch.bfloat16 else 0.0)
+    assert ((got - want).abs() <= tol * want.abs() + 2e-7).all()
+
+
+def test_backward_at_scales_that_overflow_the_quotient():
+    """lse / scale past the FP32 range, at scales of 1e-38: p is still uniform."""
+    rows, vocab, scale = 3, 1000, 1e-38
+    z = _draw(4, (rows, vocab))
+    t = torch.tensor([0, 500, 999])
+    _, lse = q.qlora_token_logp(z.to(DEV), t.to(DEV), scale=scale)
+    got = ref.f64(q.qlora_token_logp_bwd(z.to(DEV), t.to(DEV), lse,
+                                         torch.full((rows,), 1e38, device=DEV), scale=scale))
+    hot = torch.zeros(rows, vocab, dtype=torch.float64)
+    hot[torch.arange(rows), t] = 1.0
+    assert ((got - (hot - 1.0 / vocab)).abs() <= 2e-5 / vocab + 1e-6 * hot).all()
