@@ -17,6 +17,7 @@ namespace {
 
 constexpr int64_t kMaxVocab = int64_t(1) << 24;
 constexpr int64_t kMaxSequences = int64_t(1) << 21;
+constexpr float kMaxScale = 0x1p126f;   // scale * log2(e) stays finite
 
 bool type_ok(int t) { return t == QLORA_BF16 || t == QLORA_F32; }
 
@@ -36,7 +37,7 @@ int check_logits_shape(const qlora_logits_t* l) {
   if (l->rows < 0 || l->rows > kMaxTokens || l->vocab < 1 || l->vocab > kMaxVocab ||
       l->ld < l->vocab || l->ld > (int64_t(1) << 32) || !type_ok(l->type))
     return QLORA_ERR_SHAPE;
-  if (!(l->scale > 0.0f) || !std::isfinite(l->scale)) return QLORA_ERR_SHAPE;
+  if (!(l->scale > 0.0f && l->scale <= kMaxScale)) return QLORA_ERR_SHAPE;
   return QLORA_OK;
 }
 

@@ -536,7 +536,7 @@ size_t qlora_norm_workspace_bytes(int64_t M, int64_t d);
  *   logits  [rows, ld] of `type`, ld >= vocab (columns vocab .. ld - 1 are
  *           neither read nor written).  0 <= rows <= 2^21,
  *           1 <= vocab <= 2^24.
- *   scale   finite, > 0 (1 / temperature)
+ *   scale   > 0, at most 2^126 (1 / temperature)
  */
 typedef struct {
   const void *logits;
