@@ -246,11 +246,11 @@ def _dlogits(dlogits, logits, l):
     return dlogits, ldd
 
 
-def _with_workspace(nbytes: int, device, *counts: int):
-    """A workspace and FP32 outputs of `counts` values, in one allocation (a
-    small batch's call spends a good part of its time on allocations)."""
-    n = (nbytes + 63) // 64 * 16
-    return torch.empty(n + sum(counts), dtype=torch.float32, device=device).split((n, *counts))
+def _space(workspace, need, device):
+    """(workspace, its bytes): the caller's, or a new one of `need` bytes."""
+    if workspace is None:
+        return _lib._workspace(need, device), need
+    return workspace, _room(workspace)
 
 
 def qlora_token_logp(logits: torch.Tensor, targets: torch.Tensor,
@@ -315,10 +315,11 @@ def qlora_preference_loss(logits: torch.Tensor, targets: torch.Tensor, offsets: 
         _need(ref_logp, torch.float32, (l.rows,), "ref_logp")
     par = _Preference(kind, 1 if length_normalize else 0, beta, label_smoothing, margin,
                       1.0 / max(1, pairs) if weight is None else weight)
-    nbytes = qlora_preference_workspace_bytes(l.rows) if workspace is None else 0
-    ws, logp, seq_logp, loss = _with_workspace(nbytes, dev, l.rows, 2 * pairs, pairs)
-    if workspace is not None:
-        ws, nbytes = workspace, _room(workspace)
+    need = qlora_preference_workspace_bytes(l.rows) if workspace is None else 0
+    ws, nbytes = _space(workspace, need, dev)
+    # each output has memory of its own: whoever keeps one keeps nothing beside it
+    logp = torch.empty(l.rows, dtype=torch.float32, device=dev)
+    seq_logp, loss = logp.new_empty(2 * pairs), logp.new_empty(pairs)
     ldd = 0
     if need_grad:
         dlogits, ldd = _dlogits(dlogits, logits, l)
@@ -365,10 +366,10 @@ def qlora_policy_loss(logits: torch.Tensor, targets: torch.Tensor, offsets: torc
     if ref_logp is not None:
         _need(ref_logp, torch.float32, (l.rows,), "ref_logp")
     par = _Policy(reduction, 1 if per_token else 0, clip_low, clip_high, kl_coef, weight)
-    nbytes = qlora_policy_workspace_bytes(l.rows, seqs) if workspace is None else 0
-    ws, logp, stats = _with_workspace(nbytes, dev, l.rows, 4)
-    if workspace is not None:
-        ws, nbytes = workspace, _room(workspace)
+    need = qlora_policy_workspace_bytes(l.rows, seqs) if workspace is None else 0
+    ws, nbytes = _space(workspace, need, dev)
+    logp = torch.empty(l.rows, dtype=torch.float32, device=dev)
+    stats = logp.new_empty(4)   # memory of its own: whoever keeps it keeps nothing beside it
     ldd = 0
     if need_grad:
         dlogits, ldd = _dlogits(dlogits, logits, l)

@@ -100,3 +100,20 @@ def test_backward_at_scales_that_overflow_the_quotient():
     hot = torch.zeros(rows, vocab, dtype=torch.float64)
     hot[torch.arange(rows), t] = 1.0
     assert ((got - (hot - 1.0 / vocab)).abs() <= 2e-5 / vocab + 1e-6 * hot).all()
+
+
+def _batch(rows=2000, vocab=70):
+    z, t = _draw(5, (rows, vocab)).to(DEV), torch.randint(0, vocab, (rows,), device=DEV)
+    return z, t, torch.tensor([0, rows // 2, rows], device=DEV), torch.ones(2, device=DEV)
+
+
+def test_losses_keep_nothing_alive_beside_an_output():
+    """Each output holds its own values and no more, and takes an in-place
+    operation with a tensor that needs a gradient."""
+    z, t, off, adv = _batch()
+    outs = [*q.qlora_preference_loss(z, t, off)[:3], *q.qlora_policy_loss(z, t, off, adv)[:2]]
+    for o in outs:
+        held = o.untyped_storage().nbytes()
+        assert held == o.numel() * 4
+        o.mul_(torch.ones((), device=DEV, requires_grad=True))
+        assert o.requires_grad
