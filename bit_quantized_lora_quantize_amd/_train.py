@@ -231,12 +231,16 @@ def _logits(logits, targets, ignore_index, scale):
 
 
 def _dlogits(dlogits, logits, l):
-    """The gradient's buffer (by default laid out as the logits) and its row
-    stride."""
+    """The gradient's buffer and its row stride.  By default the rows are laid
+    out as the logits' where these are padded by less than 128 elements or a
+    quarter of the vocabulary, else (logits that are a slice of a larger array)
+    without gaps."""
     if dlogits is None:
-        dlogits = torch.empty_strided((l.rows, l.vocab), (l.ld, 1), dtype=logits.dtype,
+        near = l.ld - l.vocab < 128 or 4 * l.ld <= 5 * l.vocab
+        ldd = l.ld if near else l.vocab
+        dlogits = torch.empty_strided((l.rows, l.vocab), (ldd, 1), dtype=logits.dtype,
                                       device=logits.device)
-        return dlogits, l.ld
+        return dlogits, ldd
     ldd = dlogits.stride(0) if l.rows > 1 else max(dlogits.stride(0), l.vocab)
     if (dlogits.dtype != logits.dtype or dlogits.shape != logits.shape or not dlogits.is_cuda or
             (l.vocab > 1 and dlogits.stride(1) != 1) or ldd < l.vocab):
@@ -271,7 +275,9 @@ def qlora_token_logp_bwd(logits: torch.Tensor, targets: torch.Tensor, lse: torch
                          dlogp: torch.Tensor, ignore_index: int = IGNORE_INDEX, scale: float = 1.0,
                          dlogits: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of the logits from upstream gradients of qlora_token_logp's
-    log-probabilities; dlogits may be the logits themselves."""
+    log-probabilities; dlogits may be the logits themselves.  A new one has the
+    logits' padding, unless that is 128 elements and a quarter of the vocabulary
+    or more; the losses' gradients are laid out the same."""
     l = _logits(logits, targets, ignore_index, scale)
     _need(lse, torch.float32, (l.rows,), "lse")
     _need(dlogp, torch.float32, (l.rows,), "dlogp")
@@ -286,7 +292,7 @@ class PreferenceOut(NamedTuple):
     loss: torch.Tensor                # FP32 [pairs]
     seq_logp: torch.Tensor            # FP32 [2 pairs]
     logp: torch.Tensor                # FP32 [rows]
-    dlogits: Optional[torch.Tensor]   # like the logits
+    dlogits: Optional[torch.Tensor]   # as the logits, padding included
 
 
 def qlora_preference_workspace_bytes(rows: int) -> int:
@@ -335,7 +341,7 @@ def qlora_preference_loss(logits: torch.Tensor, targets: torch.Tensor, offsets: 
 class PolicyOut(NamedTuple):
     stats: torch.Tensor               # FP32 [4]: loss, policy term, KL, clipped share
     logp: torch.Tensor                # FP32 [rows]
-    dlogits: Optional[torch.Tensor]   # like the logits
+    dlogits: Optional[torch.Tensor]   # as the logits, padding included
 
 
 def qlora_policy_workspace_bytes(rows: int, sequences: int) -> int:

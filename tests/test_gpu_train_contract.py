@@ -117,3 +117,25 @@ def test_losses_keep_nothing_alive_beside_an_output():
         assert held == o.numel() * 4
         o.mul_(torch.ones((), device=DEV, requires_grad=True))
         assert o.requires_grad
+
+
+def test_gradient_buffers_take_no_large_stride():
+    """Logits that are a slice of a larger array: their gradient is dense, the
+    padding of a row's end apart."""
+    x = _draw(6, (9, 50, 700)).to(DEV)
+    z = x[:, 7, :]                                   # stride 35000
+    t = torch.arange(9, device=DEV)
+    off, adv = torch.tensor([0, 5, 9], device=DEV), torch.ones(2, device=DEV)
+    lp, lse = q.qlora_token_logp(z, t)
+    calls = [lambda v: q.qlora_token_logp_bwd(v, t, lse, lp),
+             lambda v: q.qlora_preference_loss(v, t, off).dlogits,
+             lambda v: q.qlora_policy_loss(v, t, off, adv).dlogits]
+    for call in calls:
+        d = call(z)
+        held = d.untyped_storage().nbytes()
+        assert d.stride() == (700, 1) and held == 9 * 700 * 4
+        dense = z.clone()
+        assert ref.max_err(d, call(dense)) <= 5e-6
+        padded = torch.empty(9, 704, device=DEV)[:, :700]
+        padded.copy_(z)
+        assert call(padded).stride() == (704, 1)
