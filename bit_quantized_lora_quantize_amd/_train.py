@@ -139,9 +139,9 @@ def qlora_norm_fwd(X: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Te
                    eps: float = 1e-5, kind: int = QLORA_NORM_LAYER,
                    residual: Optional[torch.Tensor] = None, H: Optional[torch.Tensor] = None,
                    Y: Optional[torch.Tensor] = None, save_stats: bool = True) -> NormOut:
-    """Norm of X, or of H = X + residual, over the last axis.  H and Y may be
-    given; H may be X or the residual.  save_stats=False leaves out what only
-    the backward needs."""
+    """Norm of X, or of H = X + residual, over the last axis.  Y may be given,
+    and with a residual H, which may be X or the residual.  save_stats=False
+    leaves out what only the backward needs."""
     ty = _matrix_type(X, "X")
     shape = X.shape
     M, d = shape
@@ -151,6 +151,8 @@ def qlora_norm_fwd(X: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Te
     if residual is not None:
         _need(residual, X.dtype, shape, "residual")
         H = _out_like(H, X, "H")
+    elif H is not None:
+        raise ValueError("H: only with a residual, without one the norm is that of X")
     Y = _out_like(Y, X, "Y")
     mean = rstd = None
     if save_stats:

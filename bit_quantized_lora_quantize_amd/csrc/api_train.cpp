@@ -104,6 +104,7 @@ int qlora_norm_fwd(int kind, int type, const void* X, const void* R, int64_t M, 
   if (M < 0 || M > kMaxTokens || d < 1 || d > kMaxLinearDim) return QLORA_ERR_SHAPE;
   if (!(eps >= 0.0f) || !std::isfinite(eps)) return QLORA_ERR_SHAPE;
   if (kind == QLORA_NORM_RMS && beta) return QLORA_ERR_SHAPE;
+  if (H && !R) return QLORA_ERR_SHAPE;   // it would stay unwritten
   if (M == 0) return QLORA_OK;
   if (!X || !gamma || !Y || (R && !H)) return QLORA_ERR_NULL;
   if (!elem_aligned(X, type) || !elem_aligned(R, type) || !elem_aligned(H, type) ||

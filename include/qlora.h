@@ -491,7 +491,8 @@ int qlora_adamw_step(int count, const qlora_adamw_param *params, float lr,
  *   gamma   [d] of `w_type`; beta [d] of `w_type` or NULL (RMS: NULL, else
  *           QLORA_ERR_SHAPE)
  *   eps     finite, >= 0
- *   H       [M, d] output, needed with R (may be X or R); NULL without
+ *   H       [M, d] output, needed with R (may be X or R); NULL without (else
+ *           QLORA_ERR_SHAPE)
  *   Y       [M, d] output (may be X when R is NULL)
  *   mean    FP32 [M] or NULL (not written for RMS); rstd FP32 [M] or NULL:
  *           saved for the backward

@@ -44,3 +44,25 @@ def test_scales_whose_base_2_form_overflows_are_refused(L, scale, status):
     want = ENULL if status == OK else status       # an empty batch still writes its averages
     assert L.qlora_policy_loss(l, None, 0, None, None, None, pol, None, None, None, 0, None, 0,
                                None) == want
+
+
+def test_a_norm_without_residual_takes_no_buffer_for_the_sum(L):
+    """H without a residual would stay unwritten: refused, not ignored."""
+    call = lambda M, R, H: L.qlora_norm_fwd(0, 1, P(0x1000), R, M, 64, 1, P(0x2000), None, 1e-5,  # noqa: E731
+                                            H, P(0x3000), None, None, None)
+    assert call(0, None, None) == OK and call(0, P(0x4000), P(0x5000)) == OK
+    assert call(0, None, P(0x5000)) == ESHAPE and call(4, None, P(0x5000)) == ESHAPE
+
+
+class _OnGpu(torch.Tensor):
+    """A host tensor that says it is on GPU 0, to reach the binding's checks."""
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+
+def test_the_binding_refuses_a_buffer_for_the_sum_without_residual(L):
+    x, g = (t.as_subclass(_OnGpu) for t in (torch.zeros(4, 64), torch.ones(64)))
+    with pytest.raises(ValueError, match="residual"):
+        q.qlora_norm_fwd(x, g, H=x)
