@@ -2,8 +2,8 @@
 (include/qlora.h): norms, token log-probabilities, the preference loss and the
 clipped policy loss.  Argument marshalling only, as in _lib.py.
 
-Outputs that are not passed in are allocated on the inputs' device; work goes
-to the current stream of that device."""
+The tensors of a call are on one GPU.  Outputs that are not passed in are
+allocated there; work goes to that GPU's current stream."""
 from __future__ import annotations
 
 import ctypes
@@ -63,42 +63,56 @@ def declare(L: ctypes.CDLL) -> None:
 
 # A call on a few rows is bound by host time: the helpers below stay cheap.
 
-def _raw_stream(device) -> int:
-    """The current stream's handle, without building a Stream object."""
-    return torch._C._cuda_getCurrentRawStream(device.index)
+_current_gpu = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream   # its handle, without a Stream object
 
 
-def _need(t: torch.Tensor, dtype, shape, name):
-    """_lib._need, with the passing case first."""
-    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda):
+def _call(name: str, at: int, *args) -> None:
+    """The entry point on the current stream of GPU `at`, which is made the
+    current GPU (the default stream's handle is 0 on every one)."""
+    f = getattr(_lib.lib(), name)
+    if _current_gpu() == at:
+        status = f(*args, _raw_stream(at))
+    else:
+        with torch.cuda.device(at):
+            status = f(*args, _raw_stream(at))
+    if status:
+        _check(status, name)
+
+
+def _need(t: torch.Tensor, dtype, shape, name, at: int):
+    """_lib._need, with the passing case first, and on GPU `at` like the call's
+    first tensor."""
+    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == at):
         _lib._need(t, dtype, shape, name)
+        raise ValueError(f"{name}: expected on GPU {at}, got {t.device}")
 
 
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _room(ws: torch.Tensor) -> int:
+def _room(ws: torch.Tensor, at: int) -> int:
     """The bytes of a caller's workspace, of whatever type."""
-    if not (ws.is_cuda and ws.is_contiguous()):
-        raise ValueError(f"workspace: expected a contiguous tensor on the GPU, got strides "
+    if not (ws.get_device() == at and ws.is_contiguous()):
+        raise ValueError(f"workspace: expected a contiguous tensor on GPU {at}, got strides "
                          f"{ws.stride()} on {ws.device}")
     return ws.numel() * ws.element_size()
 
 
-def _out(t, shape, dtype, device, name):
+def _out(t, shape, dtype, device, name, at):
     """The caller's output after a check, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _need(t, dtype, shape, name)
+    _need(t, dtype, shape, name, at)
     return t
 
 
-def _out_like(t, X, name):
+def _out_like(t, X, name, at):
     """The same for an output of X's type and shape."""
     if t is None:
         return torch.empty_like(X)
-    _need(t, X.dtype, X.shape, name)
+    _need(t, X.dtype, X.shape, name, at)
     return t
 
 
@@ -117,22 +131,23 @@ class NormGrads(NamedTuple):
     dbeta: Optional[torch.Tensor]
 
 
-def _weight_type(gamma, beta, d):
+def _weight_type(gamma, beta, d, at):
     wt = _TYPES.get(gamma.dtype)
     if wt is None:
         raise ValueError(f"gamma: expected bfloat16 or float32, got {gamma.dtype}")
-    _need(gamma, gamma.dtype, (d,), "gamma")
+    _need(gamma, gamma.dtype, (d,), "gamma", at)
     if beta is not None:
-        _need(beta, gamma.dtype, (d,), "beta")
+        _need(beta, gamma.dtype, (d,), "beta", at)
     return wt
 
 
 def _matrix_type(X, name):
-    t = _TYPES.get(X.dtype)
-    if t is None or X.dim() != 2:
-        raise ValueError(f"{name}: expected a bfloat16 or float32 matrix, got {X.dtype} "
-                         f"{tuple(X.shape)}")
-    return t
+    """The element type of the call's first tensor, and its GPU."""
+    t, at = _TYPES.get(X.dtype), X.get_device()
+    if t is None or at < 0 or X.dim() != 2:
+        raise ValueError(f"{name}: expected a bfloat16 or float32 matrix on the GPU, got {X.dtype} "
+                         f"{tuple(X.shape)} on {X.device}")
+    return t, at
 
 
 def qlora_norm_fwd(X: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tensor] = None,
@@ -142,28 +157,28 @@ def qlora_norm_fwd(X: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Te
     """Norm of X, or of H = X + residual, over the last axis.  Y may be given,
     and with a residual H, which may be X or the residual.  save_stats=False
     leaves out what only the backward needs."""
-    ty = _matrix_type(X, "X")
+    ty, at = _matrix_type(X, "X")
     shape = X.shape
     M, d = shape
     dev = X.device
-    _need(X, X.dtype, shape, "X")
-    wt = _weight_type(gamma, beta, d)
+    if not X.is_contiguous():
+        _lib._need(X, X.dtype, shape, "X")
+    wt = _weight_type(gamma, beta, d, at)
     if residual is not None:
-        _need(residual, X.dtype, shape, "residual")
-        H = _out_like(H, X, "H")
+        _need(residual, X.dtype, shape, "residual", at)
+        H = _out_like(H, X, "H", at)
     elif H is not None:
         raise ValueError("H: only with a residual, without one the norm is that of X")
-    Y = _out_like(Y, X, "Y")
+    Y = _out_like(Y, X, "Y", at)
     mean = rstd = None
     if save_stats:
         rstd = torch.empty(M, dtype=torch.float32, device=dev)
         if kind == QLORA_NORM_LAYER:
             mean = torch.empty(M, dtype=torch.float32, device=dev)
-    _check(_lib.lib().qlora_norm_fwd(kind, ty, X.data_ptr(), _addr(residual), M, d, wt,
-                                     gamma.data_ptr(), _addr(beta), eps,
-                                     H.data_ptr() if residual is not None else None, Y.data_ptr(),
-                                     _addr(mean), _addr(rstd), _raw_stream(dev)),
-           "qlora_norm_fwd")
+    _call("qlora_norm_fwd", at, kind, ty, X.data_ptr(), _addr(residual), M, d, wt,
+          gamma.data_ptr(), _addr(beta), eps,
+          H.data_ptr() if residual is not None else None, Y.data_ptr(),
+          _addr(mean), _addr(rstd))
     return NormOut(Y, H if residual is not None else X, mean, rstd)
 
 
@@ -181,58 +196,59 @@ def qlora_norm_bwd(dY: torch.Tensor, H: torch.Tensor, gamma: torch.Tensor,
     """Backward of qlora_norm_fwd for its H, mean and rstd; dH is the gradient
     that reaches H past the norm.  dX may be dY or dH.  need_dbeta is for the
     layer norm alone."""
-    ty = _matrix_type(H, "H")
+    ty, at = _matrix_type(H, "H")
     shape = H.shape
     M, d = shape
     dev = H.device
-    _need(H, H.dtype, shape, "H")
-    _need(dY, H.dtype, shape, "dY")
-    wt = _weight_type(gamma, None, d)
-    _need(rstd, torch.float32, (M,), "rstd")
+    if not H.is_contiguous():
+        _lib._need(H, H.dtype, shape, "H")
+    _need(dY, H.dtype, shape, "dY", at)
+    wt = _weight_type(gamma, None, d, at)
+    _need(rstd, torch.float32, (M,), "rstd", at)
     if kind == QLORA_NORM_LAYER:
         if mean is None:
             raise ValueError("mean: the layer norm's backward needs it")
-        _need(mean, torch.float32, (M,), "mean")
+        _need(mean, torch.float32, (M,), "mean", at)
     if dH is not None:
-        _need(dH, H.dtype, shape, "dH")
-    dX = _out_like(dX, H, "dX")
+        _need(dH, H.dtype, shape, "dH", at)
+    dX = _out_like(dX, H, "dX", at)
     ws, nbytes = None, 0
     if need_dgamma or need_dbeta:
-        dgamma = _out(dgamma, (d,), torch.float32, dev, "dgamma") if need_dgamma else None
-        dbeta = _out(dbeta, (d,), torch.float32, dev, "dbeta") if need_dbeta else None
+        dgamma = _out(dgamma, (d,), torch.float32, dev, "dgamma", at) if need_dgamma else None
+        dbeta = _out(dbeta, (d,), torch.float32, dev, "dbeta", at) if need_dbeta else None
         if workspace is None:
             nbytes = qlora_norm_workspace_bytes(M, d)
             ws = _lib._workspace(nbytes, dev)
         else:
-            ws, nbytes = workspace, _room(workspace)
+            ws, nbytes = workspace, _room(workspace, at)
     else:
         dgamma = dbeta = None
-    _check(_lib.lib().qlora_norm_bwd(kind, ty, dY.data_ptr(), H.data_ptr(), _addr(dH), M, d, wt,
-                                     gamma.data_ptr(), _addr(mean), rstd.data_ptr(),
-                                     dX.data_ptr(), _addr(dgamma), _addr(dbeta), _addr(ws),
-                                     nbytes, _raw_stream(dev)),
-           "qlora_norm_bwd")
+    _call("qlora_norm_bwd", at, kind, ty, dY.data_ptr(), H.data_ptr(), _addr(dH), M, d, wt,
+          gamma.data_ptr(), _addr(mean), rstd.data_ptr(),
+          dX.data_ptr(), _addr(dgamma), _addr(dbeta), _addr(ws),
+          nbytes)
     return NormGrads(dX, dgamma, dbeta)
 
 
 # ---------------------------------------------------------- losses on logits
 
 def _logits(logits, targets, ignore_index, scale):
-    """The C description of a logits batch.  Rows may be strided (a padded
+    """The C description of a logits batch, and its GPU.  Rows may be strided (a padded
     vocabulary); their elements are contiguous."""
-    ty = _matrix_type(logits, "logits")
+    ty, at = _matrix_type(logits, "logits")
     rows, vocab = logits.shape
     ld, inner = logits.stride()
     if rows <= 1:
         ld = max(ld, vocab)
-    if not logits.is_cuda or (vocab > 1 and inner != 1) or ld < vocab:
-        raise ValueError(f"logits: expected rows of contiguous elements on the GPU, got strides "
-                         f"{logits.stride()} on {logits.device}")
-    _need(targets, torch.int64, (rows,), "targets")
-    return _Logits(logits.data_ptr(), targets.data_ptr(), rows, vocab, ld, ignore_index, ty, scale)
+    if (vocab > 1 and inner != 1) or ld < vocab:
+        raise ValueError(f"logits: expected rows of contiguous elements, got strides "
+                         f"{logits.stride()}")
+    _need(targets, torch.int64, (rows,), "targets", at)
+    l = _Logits(logits.data_ptr(), targets.data_ptr(), rows, vocab, ld, ignore_index, ty, scale)
+    return l, at
 
 
-def _dlogits(dlogits, logits, l):
+def _dlogits(dlogits, logits, l, at):
     """The gradient's buffer and its row stride.  By default the rows are laid
     out as the logits' where these are padded by less than 128 elements or a
     quarter of the vocabulary, else (logits that are a slice of a larger array)
@@ -244,19 +260,21 @@ def _dlogits(dlogits, logits, l):
                                       device=logits.device)
         return dlogits, ldd
     ldd = dlogits.stride(0) if l.rows > 1 else max(dlogits.stride(0), l.vocab)
-    if (dlogits.dtype != logits.dtype or dlogits.shape != logits.shape or not dlogits.is_cuda or
-            (l.vocab > 1 and dlogits.stride(1) != 1) or ldd < l.vocab):
-        raise ValueError(f"dlogits: expected {logits.dtype} {tuple(logits.shape)} with contiguous "
-                         f"elements in a row, got {dlogits.dtype} {tuple(dlogits.shape)} with "
-                         f"strides {dlogits.stride()}")
+    if (dlogits.dtype != logits.dtype or dlogits.shape != logits.shape or
+            dlogits.get_device() != at or (l.vocab > 1 and dlogits.stride(1) != 1) or
+            ldd < l.vocab):
+        raise ValueError(f"dlogits: expected {logits.dtype} {tuple(logits.shape)} on GPU {at} with "
+                         f"contiguous elements in a row, got {dlogits.dtype} "
+                         f"{tuple(dlogits.shape)} on {dlogits.device} with strides "
+                         f"{dlogits.stride()}")
     return dlogits, ldd
 
 
-def _space(workspace, need, device):
+def _space(workspace, need, device, at):
     """(workspace, its bytes): the caller's, or a new one of `need` bytes."""
     if workspace is None:
         return _lib._workspace(need, device), need
-    return workspace, _room(workspace)
+    return workspace, _room(workspace, at)
 
 
 def qlora_token_logp(logits: torch.Tensor, targets: torch.Tensor,
@@ -264,12 +282,11 @@ def qlora_token_logp(logits: torch.Tensor, targets: torch.Tensor,
                      logp: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
     """(logp, lse), FP32 [rows]: log-probability of each row's target under
     softmax(scale * logits) and the log of the row's summed exponentials."""
-    l = _logits(logits, targets, ignore_index, scale)
+    l, at = _logits(logits, targets, ignore_index, scale)
     dev = logits.device
-    logp = _out(logp, (l.rows,), torch.float32, dev, "logp")
-    lse = _out(lse, (l.rows,), torch.float32, dev, "lse")
-    _check(_lib.lib().qlora_token_logp(l, logp.data_ptr(), lse.data_ptr(), _raw_stream(dev)),
-           "qlora_token_logp")
+    logp = _out(logp, (l.rows,), torch.float32, dev, "logp", at)
+    lse = _out(lse, (l.rows,), torch.float32, dev, "lse", at)
+    _call("qlora_token_logp", at, l, logp.data_ptr(), lse.data_ptr())
     return logp, lse
 
 
@@ -280,13 +297,12 @@ def qlora_token_logp_bwd(logits: torch.Tensor, targets: torch.Tensor, lse: torch
     log-probabilities; dlogits may be the logits themselves.  A new one has the
     logits' padding, unless that is 128 elements and a quarter of the vocabulary
     or more; the losses' gradients are laid out the same."""
-    l = _logits(logits, targets, ignore_index, scale)
-    _need(lse, torch.float32, (l.rows,), "lse")
-    _need(dlogp, torch.float32, (l.rows,), "dlogp")
-    dlogits, ldd = _dlogits(dlogits, logits, l)
-    _check(_lib.lib().qlora_token_logp_bwd(l, lse.data_ptr(), dlogp.data_ptr(),
-                                           dlogits.data_ptr(), ldd, _raw_stream(logits.device)),
-           "qlora_token_logp_bwd")
+    l, at = _logits(logits, targets, ignore_index, scale)
+    _need(lse, torch.float32, (l.rows,), "lse", at)
+    _need(dlogp, torch.float32, (l.rows,), "dlogp", at)
+    dlogits, ldd = _dlogits(dlogits, logits, l, at)
+    _call("qlora_token_logp_bwd", at, l, lse.data_ptr(), dlogp.data_ptr(),
+          dlogits.data_ptr(), ldd)
     return dlogits
 
 
@@ -312,31 +328,30 @@ def qlora_preference_loss(logits: torch.Tensor, targets: torch.Tensor, offsets: 
     p; offsets int64 [2 pairs + 1] are the sequences' first rows) and the
     gradient of weight * sum of the losses (weight None: 1 / pairs, the mean).
     dlogits may be the logits themselves."""
-    l = _logits(logits, targets, ignore_index, scale)
+    l, at = _logits(logits, targets, ignore_index, scale)
     dev = logits.device
     n = offsets.numel()
     if n % 2 == 0:
         raise ValueError(f"offsets: expected 2 pairs + 1 of them, got {n}")
     pairs = n // 2
-    _need(offsets, torch.int64, (n,), "offsets")
+    _need(offsets, torch.int64, (n,), "offsets", at)
     if ref_logp is not None:
-        _need(ref_logp, torch.float32, (l.rows,), "ref_logp")
+        _need(ref_logp, torch.float32, (l.rows,), "ref_logp", at)
     par = _Preference(kind, 1 if length_normalize else 0, beta, label_smoothing, margin,
                       1.0 / max(1, pairs) if weight is None else weight)
     need = qlora_preference_workspace_bytes(l.rows) if workspace is None else 0
-    ws, nbytes = _space(workspace, need, dev)
+    ws, nbytes = _space(workspace, need, dev, at)
     # each output has memory of its own: whoever keeps one keeps nothing beside it
     logp = torch.empty(l.rows, dtype=torch.float32, device=dev)
     seq_logp, loss = logp.new_empty(2 * pairs), logp.new_empty(pairs)
     ldd = 0
     if need_grad:
-        dlogits, ldd = _dlogits(dlogits, logits, l)
+        dlogits, ldd = _dlogits(dlogits, logits, l, at)
     else:
         dlogits = None
-    _check(_lib.lib().qlora_preference_loss(l, offsets.data_ptr(), pairs, _addr(ref_logp), par,
-                                            logp.data_ptr(), seq_logp.data_ptr(), loss.data_ptr(),
-                                            _addr(dlogits), ldd, ws.data_ptr(), nbytes,
-                                            _raw_stream(dev)), "qlora_preference_loss")
+    _call("qlora_preference_loss", at, l, offsets.data_ptr(), pairs, _addr(ref_logp), par,
+          logp.data_ptr(), seq_logp.data_ptr(), loss.data_ptr(),
+          _addr(dlogits), ldd, ws.data_ptr(), nbytes)
     return PreferenceOut(loss, seq_logp, logp, dlogits)
 
 
@@ -362,29 +377,29 @@ def qlora_policy_loss(logits: torch.Tensor, targets: torch.Tensor, offsets: torc
     are offsets (int64 [sequences + 1]), and the gradient of weight * loss.
     advantages: FP32 [sequences], or [rows] with per_token.  dlogits may be
     the logits themselves."""
-    l = _logits(logits, targets, ignore_index, scale)
+    l, at = _logits(logits, targets, ignore_index, scale)
     dev = logits.device
     seqs = offsets.numel() - 1
     if seqs < 0:
         raise ValueError("offsets: expected sequences + 1 of them")
-    _need(offsets, torch.int64, (seqs + 1,), "offsets")
-    _need(advantages, torch.float32, (l.rows if per_token else seqs,), "advantages")
+    _need(offsets, torch.int64, (seqs + 1,), "offsets", at)
+    _need(advantages, torch.float32, (l.rows if per_token else seqs,), "advantages", at)
     if old_logp is not None:
-        _need(old_logp, torch.float32, (l.rows,), "old_logp")
+        _need(old_logp, torch.float32, (l.rows,), "old_logp", at)
     if ref_logp is not None:
-        _need(ref_logp, torch.float32, (l.rows,), "ref_logp")
+        _need(ref_logp, torch.float32, (l.rows,), "ref_logp", at)
     par = _Policy(reduction, 1 if per_token else 0, clip_low, clip_high, kl_coef, weight)
     need = qlora_policy_workspace_bytes(l.rows, seqs) if workspace is None else 0
-    ws, nbytes = _space(workspace, need, dev)
+    ws, nbytes = _space(workspace, need, dev, at)
     logp = torch.empty(l.rows, dtype=torch.float32, device=dev)
     stats = logp.new_empty(4)   # memory of its own: whoever keeps it keeps nothing beside it
     ldd = 0
     if need_grad:
-        dlogits, ldd = _dlogits(dlogits, logits, l)
+        dlogits, ldd = _dlogits(dlogits, logits, l, at)
     else:
         dlogits = None
-    _check(_lib.lib().qlora_policy_loss(l, offsets.data_ptr(), seqs, advantages.data_ptr(),
-                                        _addr(old_logp), _addr(ref_logp), par, logp.data_ptr(),
-                                        stats.data_ptr(), _addr(dlogits), ldd, ws.data_ptr(),
-                                        nbytes, _raw_stream(dev)), "qlora_policy_loss")
+    _call("qlora_policy_loss", at, l, offsets.data_ptr(), seqs, advantages.data_ptr(),
+          _addr(old_logp), _addr(ref_logp), par, logp.data_ptr(),
+          stats.data_ptr(), _addr(dlogits), ldd, ws.data_ptr(),
+          nbytes)
     return PolicyOut(stats, logp, dlogits)

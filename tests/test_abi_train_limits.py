@@ -55,14 +55,94 @@ def test_a_norm_without_residual_takes_no_buffer_for_the_sum(L):
 
 
 class _OnGpu(torch.Tensor):
-    """A host tensor that says it is on GPU 0, to reach the binding's checks."""
+    """A host tensor that says it is on a GPU, to reach the binding's checks."""
     is_cuda = True
+    at = 0
 
     def get_device(self):
-        return 0
+        return self.at
+
+
+def _on(at, t):
+    t = t.as_subclass(_OnGpu)
+    t.at = at
+    return t
 
 
 def test_the_binding_refuses_a_buffer_for_the_sum_without_residual(L):
-    x, g = (t.as_subclass(_OnGpu) for t in (torch.zeros(4, 64), torch.ones(64)))
+    x, g = _on(0, torch.zeros(4, 64)), _on(0, torch.ones(64))
     with pytest.raises(ValueError, match="residual"):
         q.qlora_norm_fwd(x, g, H=x)
+
+
+def _calls():
+    """Every entry point with all its tensors: (function, tensors by name)."""
+    x, v, r = torch.zeros(4, 64), torch.ones(64), torch.zeros(4)
+    t, off, d = torch.zeros(4, dtype=torch.int64), torch.tensor([0, 2, 4]), torch.zeros(4, 64)
+    ws = torch.empty(1 << 16, dtype=torch.uint8)
+    return [
+        (q.qlora_norm_fwd, dict(X=x, gamma=v, beta=v.clone(), residual=x.clone(), H=d, Y=d.clone())),
+        (q.qlora_norm_bwd, dict(dY=d, H=x, gamma=v, mean=r, rstd=r.clone(), dH=x.clone(),
+                                dX=d.clone(), dgamma=v.clone(), dbeta=v.clone(), need_dbeta=True,
+                                workspace=ws)),
+        (q.qlora_token_logp, dict(logits=x, targets=t, logp=r, lse=r.clone())),
+        (q.qlora_token_logp_bwd, dict(logits=x, targets=t, lse=r, dlogp=r.clone(), dlogits=d)),
+        (q.qlora_preference_loss, dict(logits=x, targets=t, offsets=off, ref_logp=r, dlogits=d,
+                                       workspace=ws)),
+        (q.qlora_policy_loss, dict(logits=x, targets=t, offsets=off, advantages=torch.ones(2),
+                                   old_logp=r, ref_logp=r.clone(), dlogits=d, workspace=ws))]
+
+
+class _Recorder:
+    """Stands in for the library: notes the current GPU and the stream."""
+
+    def __init__(self, gpu):
+        self.seen, self.gpu = [], gpu
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.seen.append((name, self.gpu[0], args[-1]))
+            return 0
+        return call
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    from bit_quantized_lora_quantize_amd import _lib
+    gpu = [0]
+    rec = _Recorder(gpu)
+
+    class Device:
+        def __init__(self, at):
+            self.at = at
+
+        def __enter__(self):
+            self.before, gpu[0] = gpu[0], self.at
+
+        def __exit__(self, *_):
+            gpu[0] = self.before
+
+    monkeypatch.setattr(_lib, "lib", lambda: rec)
+    monkeypatch.setattr(_train, "_current_gpu", lambda: gpu[0])
+    monkeypatch.setattr(_train, "_raw_stream", lambda at: 100 + at)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    return rec
+
+
+@pytest.mark.parametrize("at", [0, 1])
+def test_work_goes_to_the_tensors_gpu(fake, at):
+    """The default stream has the same handle on every GPU: the tensors' one is
+    current during the call, and only then."""
+    for f, kw in _calls():
+        fake.seen.clear()
+        f(**{k: _on(at, v) if isinstance(v, torch.Tensor) else v for k, v in kw.items()})
+        assert fake.seen[-1] == (f.__name__, at, 100 + at) and fake.gpu == [0]
+
+
+def test_tensors_on_two_gpus_are_refused(fake):
+    for f, kw in _calls():
+        names = [k for k, v in kw.items() if isinstance(v, torch.Tensor)]
+        for odd in names:
+            with pytest.raises(ValueError):
+                f(**{k: _on(int(k == odd), v) if k in names else v for k, v in kw.items()})
+        assert not fake.seen
