@@ -995,9 +995,11 @@ static void policy_by_width(const LogitsArgs& l, const PolicyArgs& a, T* dlogits
                             hipStream_t st) {
   constexpr int kFar = 65536 + 8 * 1024 * kVec<T>;   // with 128 KB of LDS
   const int64_t v = l.vocab;
+  if constexpr (sizeof(T) == 2) {
+    if (v > 2048 && v <= 4096) return policy_held<T, 128, 32, 0, 8>(l, a, dlogits, ldd, st);
+  }
   if (v <= 512) policy_held<T, 64, 8, 0, 8>(l, a, dlogits, ldd, st);
   else if (v <= 2048) policy_held<T, 64, 32, 0, 6>(l, a, dlogits, ldd, st);
-  else if (v <= 4096 && sizeof(T) == 2) policy_held<T, 128, 32, 0, 8>(l, a, dlogits, ldd, st);
   else if (v <= 8192) policy_held<T, 256, 32, 0, 8>(l, a, dlogits, ldd, st);
   else if (v <= 16384) policy_held<T, 512, 32, 0, 8>(l, a, dlogits, ldd, st);
   else if (v <= 24576) policy_held<T, 768, 32, 0, 6>(l, a, dlogits, ldd, st);
