@@ -520,8 +520,9 @@ __device__ __forceinline__ void wave_grad(const LogitsArgs& l, int64_t row, RowS
   grad_row<T, 64>(static_cast<const T*>(l.logits) + row * l.ld, out, (int)l.vocab, q, lane);
 }
 
-// A small batch in one launch: a workgroup per pair, a wavefront per row.  The
-// rows' results pass between the wavefronts through memory, at the barriers.
+// A small batch of pairs in one launch: a workgroup per pair, a wavefront per
+// row.  The rows' results pass between the wavefronts through memory, at the
+// barriers.
 template <typename T>
 __global__ __launch_bounds__(kPrefThreads) void k_preference_small(LogitsArgs l, PreferenceArgs a,
                                                                    RowStat* stat, float* logp,
@@ -543,7 +544,6 @@ __global__ __launch_bounds__(kPrefThreads) void k_preference_small(LogitsArgs l,
       if (dlogits) wave_grad<T>(l, row, RowStat{0.0f, 0.0f}, 0.0f, dlogits, ldd);
     }
   }
-  if (a.pairs == 0) return;
   int64_t b[2], e[2];
   seq_rows(a.offsets, p, a.rows, b[0], e[0]);
   seq_rows(a.offsets, p + a.pairs, a.rows, b[1], e[1]);
@@ -932,13 +932,13 @@ hipError_t launch_dlogits(const LogitsArgs& l, const RowStat* stat, const float*
   return hipGetLastError();
 }
 
-// A call on few rows is bound by its launches.  Pairs of at most about 32 rows
-// and 2^16 logits (on average) take one: a workgroup each, 13 us a call against
-// 16 with two at 30 x 1000.  The lengths are not known here; a batch of 2^20
-// logits at most bounds what one pair can hold.
-static bool small_pairs(const LogitsArgs& l, int64_t pairs) {
-  return l.rows <= 32 * pairs &&
-         l.rows * l.vocab <= std::min<int64_t>(pairs << 16, int64_t(1) << 20);
+// A call on few rows is bound by its launches.  Batches of at most 32 rows and
+// 2^16 logits take one, a workgroup a pair: 14 us a call against 16 with two at
+// 30 x 1000, no gain any more at 60 x 1000.  The pairs' lengths are not known
+// here, so the batch is bounded: one pair may hold all of it (32 pairs of 1000 x
+// 1000 logits, all in one of them: 243 us against 17; spread evenly 14).
+static bool small_batch(const LogitsArgs& l) {
+  return l.rows <= 32 && l.rows * l.vocab <= int64_t(1) << 16;
 }
 // Batches of up to kFewBlocks workgroups of gradients take two, every workgroup
 // summing its row's pair again: 14.5 us a call against 17.1 with three (128 x
@@ -951,7 +951,7 @@ template <typename T>
 static hipError_t preference_as(const LogitsArgs& l, const PreferenceArgs& a, RowStat* stat,
                                 float* logp, T* dlogits, int64_t ldd, hipStream_t st) {
   const dim3 grid((unsigned)std::max<int64_t>(a.pairs, 1));
-  if (small_pairs(l, a.pairs)) {
+  if (a.pairs > 0 && small_batch(l)) {
     hipLaunchKernelGGL(k_preference_small<T>, grid, dim3(kPrefThreads), 0, st, l, a, stat, logp,
                        dlogits, ldd);
     return hipGetLastError();

@@ -139,3 +139,51 @@ def test_gradient_buffers_take_no_large_stride():
         padded = torch.empty(9, 704, device=DEV)[:, :700]
         padded.copy_(z)
         assert call(padded).stride() == (704, 1)
+
+
+@pytest.mark.parametrize("vocab", [300, 2048, 2100])
+@pytest.mark.parametrize("lens", [[32] + [0] * 15, [16, 16], [3, 4, 1, 8, 0, 9, 4, 3], [33, 0],
+                                  [5, 6, 7, 9, 0, 6]])
+def test_preference_of_few_rows(lens, vocab):
+    """Batches on both sides of the rule that takes them in one launch, and the
+    same pairs beside 64 rows that no sequence holds, which never do: one loss,
+    one gradient (log-probabilities summed in another order: 5e-6 each)."""
+    rows, P = sum(lens), len(lens) // 2
+    say(f"few rows: {P} pairs of {rows} x {vocab}")
+    z = _draw(11, (rows + 64, vocab), 2.0).to(DEV)
+    t = torch.randint(0, vocab, (rows + 64,), generator=torch.Generator().manual_seed(1)).to(DEV)
+    t[::7] = IGNORE
+    off = torch.tensor([0] + torch.tensor(lens).cumsum(0).tolist(), device=DEV)
+    a = q.qlora_preference_loss(z[:rows], t[:rows], off, beta=0.1)
+    b = q.qlora_preference_loss(z, t, off, beta=0.1)
+    assert ref.max_err(a.logp, b.logp[:rows]) <= 5e-6
+    assert ref.max_err(a.loss, b.loss) <= 0.1 * rows * 5e-6
+    assert ref.max_err(a.dlogits, b.dlogits[:rows]) <= 5e-5 * float(b.dlogits.abs().max())
+    assert (b.dlogits[rows:] == 0).all()
+
+
+def test_preference_with_all_rows_in_one_pair_is_not_slow():
+    """The lengths of the pairs are not known to the host: a batch whose rows all
+    lie in one pair takes no more than four times as long as an even one (it
+    took seventeen times, by one workgroup)."""
+    rows, vocab, P = 1000, 1000, 32
+    z = _draw(12, (rows, vocab)).to(torch.bfloat16).to(DEV)
+    t = torch.randint(0, vocab, (rows,), device=DEV)
+    even = torch.arange(2 * P + 1, device=DEV) * rows // (2 * P)
+    skew = torch.tensor([0, 500] + [500] * (P - 1) + [1000] * P, device=DEV)
+
+    def us(off):
+        times = []
+        for _ in range(25):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(4):
+                q.qlora_preference_loss(z, t, off)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b) * 250)
+        return sorted(times)[12]
+
+    e, s = us(even), us(skew)
+    say(f"  even {e:.1f} us, in one pair {s:.1f} us")
+    assert s <= 4 * e
