@@ -469,7 +469,10 @@ int qlora_adamw_step(int count, const qlora_adamw_param *params, float lr,
  *
  * Element types of their arrays.  Arrays of these entry points need the
  * alignment of their element type only (rows of odd length start anywhere);
- * 16-byte aligned rows are fastest, with the same results.  Infinities and
+ * 16-byte aligned rows are fastest.  The norms' results do not depend on the
+ * alignment.  Sums over a row of BF16 logits start at its first 4-byte
+ * boundary, so that log-probabilities, losses and gradients may differ in
+ * their rounding between rows at even and at odd elements.  Infinities and
  * NaN in their inputs are allowed and propagate as IEEE arithmetic has it
  * (a logit of -inf is a token that cannot be drawn).
  */
@@ -532,10 +535,11 @@ size_t qlora_norm_workspace_bytes(int64_t M, int64_t d);
  * Logits of a batch of tokens and the tokens they are judged by.  Row i's
  * distribution is softmax(scale * logits[i]); a row whose target is
  * ignore_index does not count (its log-probability is 0, its gradient row is
- * 0, its logits are not read).  Any other target outside [0, vocab) gives
- * NaN in its row (log-probability and gradient); nothing is read for it.
- *   logits  [rows, ld] of `type`, ld >= vocab (columns vocab .. ld - 1 are
- *           neither read nor written).  0 <= rows <= 2^21,
+ * 0, its logits are not read).  Any other target outside [0, vocab) gives a
+ * NaN log-probability, and nothing is read for it; what that does to the
+ * gradients is said at each entry point.
+ *   logits  [rows, ld] of `type`, vocab <= ld <= 2^32 (columns vocab .. ld - 1
+ *           are neither read nor written).  0 <= rows <= 2^21,
  *           1 <= vocab <= 2^24.
  *   scale   > 0, at most 2^126 (1 / temperature)
  */
@@ -568,7 +572,8 @@ int qlora_token_logp(const qlora_logits_t *l, float *logp, float *lse,
  * whose lse is 128 or more in size (or no number) has its sum taken again.
  *   lse         FP32 [rows]: qlora_token_logp's, on the same logits and scale
  *   dlogp       FP32 [rows]; dlogits [rows, ldd] output of l->type,
- *               ldd >= vocab; may be the logits' own buffer (ldd = ld).
+ *               vocab <= ldd <= 2^32; may be the logits' own buffer (ldd = ld).
+ * A row with a target outside the vocabulary gets NaN, with dlogp = 0 zeros.
  */
 int qlora_token_logp_bwd(const qlora_logits_t *l, const float *lse,
                          const float *dlogp, void *dlogits, int64_t ldd,
@@ -592,7 +597,10 @@ int qlora_token_logp_bwd(const qlora_logits_t *l, const float *lse,
  *   l          the logits of all sequences
  *   offsets    int64 [2 pairs + 1], nondecreasing, in [0, rows] (device
  *              memory: values outside are clamped to that range); rows that
- *              no sequence holds get zero gradients.  pairs >= 0
+ *              no sequence holds get zero gradients, also for a target outside
+ *              the vocabulary; in a sequence such a target makes its pair's
+ *              loss NaN, and the gradient of both answers' rows that count.
+ *              0 <= pairs <= 2^20
  *   ref_logp   FP32 [rows] or NULL
  *   logp       FP32 [rows] output; seq_logp FP32 [2 pairs] output (s_i);
  *   loss       FP32 [pairs] output
@@ -635,7 +643,10 @@ size_t qlora_preference_workspace_bytes(int64_t rows);
  * larger one the policy term has no gradient, at equality the unclipped
  * branch's counts.  The gradient comes from the same pass over the logits
  * as the loss: rows of up to 131072 BF16 or 98304 FP32 logits are read once.
- *   offsets     int64 [sequences + 1] as in qlora_preference_loss
+ *   offsets     int64 [sequences + 1] as in qlora_preference_loss, but that a
+ *               target outside the vocabulary makes its own row's gradient NaN
+ *               alone (and the loss where there is old_logp or a KL term).
+ *               0 <= sequences <= 2^21
  *   advantages  FP32 [rows] with per_token, else FP32 [sequences]
  *   old_logp, ref_logp  FP32 [rows] or NULL (ref_logp NULL needs kl_coef 0,
  *               else QLORA_ERR_NULL)

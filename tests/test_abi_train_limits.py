@@ -29,6 +29,28 @@ def _empty_batch(**kw):
     return _train._Logits(*a.values())
 
 
+def test_row_strides_pairs_and_sequences_at_their_limits(L):
+    l, far = _empty_batch(), 1 << 32
+    assert L.qlora_token_logp(_empty_batch(ld=far), P(0x5000), None, None) == OK
+    assert L.qlora_token_logp(_empty_batch(ld=far + 1), P(0x5000), None, None) == ESHAPE
+    par = _train._Preference(0, 0, 0.1, 0.0, 0.0, 1.0)
+    pref = lambda pairs: L.qlora_preference_loss(l, None, pairs, None, par, None, None, None, None,  # noqa: E731
+                                                 0, None, 0, None)
+    assert pref(1 << 20) == ENULL and pref((1 << 20) + 1) == ESHAPE
+    pol = _train._Policy(0, 0, 0.2, 0.2, 0.0, 1.0)
+    policy = lambda seqs: L.qlora_policy_loss(l, None, seqs, None, None, None, pol, None, None,  # noqa: E731
+                                              None, 0, None, 0, None)
+    assert policy(1 << 21) == ENULL and policy((1 << 21) + 1) == ESHAPE
+    full = _train._Logits(0x1000, 0x2000, 4, 100, 100, -100, 0, 1.0)
+    back = lambda ldd: L.qlora_token_logp_bwd(full, P(0x5000), P(0x6000), None if ldd <= far  # noqa: E731
+                                              else P(0x7000), ldd, None)
+    assert back(far) == ENULL and back(far + 1) == ESHAPE
+    assert q.qlora_policy_workspace_bytes(0, 1 << 21) > 0
+    assert q.qlora_policy_workspace_bytes(0, (1 << 21) + 1) == 0
+    assert q.qlora_preference_workspace_bytes(1 << 21) > 0
+    assert q.qlora_preference_workspace_bytes((1 << 21) + 1) == 0
+
+
 @pytest.mark.parametrize("scale,status", [(2.0 ** 126, OK), (2.0 ** 126 * 1.25, ESHAPE),
                                           (3e38, ESHAPE), (1e-38, OK), (1e-45, OK)])
 def test_scales_whose_base_2_form_overflows_are_refused(L, scale, status):

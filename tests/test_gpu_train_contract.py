@@ -187,3 +187,56 @@ def test_preference_with_all_rows_in_one_pair_is_not_slow():
     e, s = us(even), us(skew)
     say(f"  even {e:.1f} us, in one pair {s:.1f} us")
     assert s <= 4 * e
+
+
+@pytest.mark.parametrize("width", [1, 7, 72, 515, 1001, 4096, 8200, 11009, 18432, 32769, 40001])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("kind", [q.QLORA_NORM_LAYER, q.QLORA_NORM_RMS])
+def test_norms_give_the_same_bits_at_any_alignment(width, dtype, kind):
+    rows, layer = 11, kind == q.QLORA_NORM_LAYER
+
+    def at(seed, by, shape=(rows, width)):
+        src = _draw(seed, shape).to(dtype)
+        v = torch.empty(src.numel() + by, dtype=dtype, device=DEV)[by:].view(shape)
+        v.copy_(src)
+        return v
+
+    found = []
+    for by in (0, 1, 3):
+        X, R, dY, dH = (at(k, by) for k in (1, 2, 3, 4))
+        gamma, beta = at(5, by, (width,)), at(6, by, (width,)) if layer else None
+        o = q.qlora_norm_fwd(X, gamma, beta, kind=kind, residual=R, Y=at(7, by), H=at(8, by))
+        b = q.qlora_norm_bwd(dY, o.H, gamma, o.mean, o.rstd, kind=kind, dH=dH, need_dbeta=layer,
+                             dX=at(9, by))
+        found.append([o.Y, o.H, o.rstd, b.dX, b.dgamma] + ([o.mean, b.dbeta] if layer else []))
+    for other in found[1:]:
+        assert all(torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0)) for a, b in zip(found[0], other))
+
+
+def test_bad_targets_by_entry_point():
+    """A target outside the vocabulary: NaN log-probabilities everywhere; in the
+    gradient NaN in its row alone, but zeros where dlogp is 0 or no sequence
+    holds the row, and NaN in every row of its pair that counts."""
+    z, t, off, adv = _batch(40, 70)
+    t[3], t[25], t[6] = 70, -1, IGNORE
+    off = torch.tensor([0, 10, 20, 30, 36], device=DEV)         # rows 36 .. 39 in none
+    t[38] = 99
+    lp, lse = q.qlora_token_logp(z, t)
+    bad = torch.tensor([3, 25, 38], device=DEV)
+    assert torch.isnan(lp[bad]).all() and torch.isnan(lse[bad]).all()
+    up = torch.ones(40, device=DEV)
+    up[25] = 0.0
+    d = q.qlora_token_logp_bwd(z, t, lse, up)
+    assert torch.isnan(d[[3, 38]]).all() and (d[25] == 0).all() and (d[6] == 0).all()
+    assert torch.isfinite(d[[0, 24, 39]]).all()
+    o = q.qlora_preference_loss(z, t, off)                      # pairs (0, 2) and (1, 3)
+    assert torch.isnan(o.loss[0]) and torch.isfinite(o.loss[1])
+    held = torch.arange(40, device=DEV)
+    pair = ((held < 10) | (held >= 20) & (held < 30)) & (t != IGNORE)
+    assert torch.isnan(o.dlogits[pair]).all() and torch.isfinite(o.dlogits[~pair]).all()
+    assert (o.dlogits[36:] == 0).all()
+    p = q.qlora_policy_loss(z, t, off, torch.ones(4, device=DEV), old_logp=torch.zeros(40, device=DEV))
+    assert torch.isnan(p.dlogits[[3, 25]]).all() and (p.dlogits[36:] == 0).all()
+    rest = torch.ones(40, dtype=torch.bool, device=DEV)
+    rest[[3, 25]] = False
+    assert torch.isfinite(p.dlogits[rest]).all()
