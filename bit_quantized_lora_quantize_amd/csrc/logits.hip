@@ -682,6 +682,9 @@ __device__ __forceinline__ void scale_terms(float c, float g, int t, int first, 
 // 15315 x 65536 BF16: 650 us, 5.9 TB/s over one read and one write (962 us as
 // three passes); 8192 x 131072 BF16: 785 us (877 read twice).  Bound by memory;
 // with one workgroup of the widest rows a compute unit, also by its reductions.
+// The bound on registers makes the steps of 32 logits a thread spill one
+// (BF16, 1024 threads) to three (FP32, 256, 512 and 1024) of them, and the FP32
+// step with LDS three.
 template <typename T, int THREADS, int E, int L, int MIN_WAVES>
 __global__ __launch_bounds__(THREADS, MIN_WAVES) void k_policy(LogitsArgs l, PolicyArgs a,
                                                                T* dlogits, int64_t ldd) {
@@ -843,7 +846,10 @@ __global__ __launch_bounds__(THREADS) void k_policy_long(LogitsArgs l, PolicyArg
   grad_row<T, THREADS>(x, out, vocab, q, threadIdx.x);
 }
 
-// Loss and averages from all rows' terms, by one workgroup.
+// Loss and averages from all rows' terms, by one workgroup: its loads' latency
+// bounds it, 4 us at 1586 rows and 13.5 at 15315 (2 % of their call).  Many rows
+// of a small vocabulary wait for it and for k_policy_count: 131072 x 500 BF16
+// takes 142 us, 2^21 x 64 2.1 ms.
 __global__ __launch_bounds__(1024) void k_policy_stats(PolicyArgs a, int64_t rows) {
   __shared__ double lds[3][16];
   double p = 0.0, k = 0.0, c = 0.0;

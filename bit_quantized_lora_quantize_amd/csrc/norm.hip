@@ -15,7 +15,14 @@
 // thread keeps its columns' weights, loads its part of the next row before it
 // works on the present one, and in the backward sums its columns' weight
 // gradients in registers.  Wider rows take the looping kernels below, which
-// read them again from the caches.
+// read them again from the caches (backward of 4096 x 18432 BF16: 269 us, 2.3
+// TB/s; 388 with dgamma).
+//
+// Three shapes do not fit their registers and spill some: the layer norm's
+// forward of 16385 to 32768 values a row (FP32 60 a thread: 125 us at 2048 x
+// 32768, 4.3 TB/s, where the RMS norm, which spills 8, takes 102; BF16 8: 59
+// us), and the layer norm's FP32 backward of 8193 to 16384 with weight gradients
+// (15: 155 us at 4096 x 12288, 3.9 TB/s).
 #include "qlora_kernels.h"
 #include "row_ops.h"
 
@@ -26,8 +33,10 @@ namespace {
 constexpr int kFinishCols = 16;
 // Arrays of this size and more go past the caches' retention: the two to four
 // of a call would drive each other out of the 256 MB of the last level anyway.
-// Backward of 16384 x 8192 BF16: 199 us kept, 187 us past; smaller outputs stay
-// for the layer that reads them next.
+// Backward of 16384 x 8192 BF16: 199 us kept, 187 us past.  Forward with a
+// residual: 193 and 181 us at 16384 x 8192, 98 and 90 at 8192 x 8192 (228 and
+// 208 with the product that reads Y next).  Smaller outputs stay for the layer
+// that reads them next.
 constexpr int64_t kOnceBytes = int64_t(128) << 20;
 
 __device__ __forceinline__ float load_w(const void* w, int w_type, int64_t i) {
@@ -556,7 +565,10 @@ Shape row_shape(int64_t rows, int64_t d, int held, int threads, int waves) {
 }
 // With weight gradients a workgroup costs a partial, and their sums registers:
 // fewer of them.  Narrow rows meet in smaller workgroups, whose barriers wait
-// for fewer (26090 x 566 BF16: 30.0 against 32.5 us).
+// for fewer (26090 x 566 BF16: 30.0 against 32.5 us).  Without weight gradients
+// 24 wavefronts a compute unit are as fast as 16 or faster: 62.0 against 76.2 us
+// at 8192 x 5120 BF16, 22.0 against 24.9 at 26090 x 566, 96.7 both at 16384 x
+// 4096; a small batch of few turns loses (1003 x 5003 FP32 13.3 against 11.7).
 Shape bwd_shape(int64_t rows, int64_t d, bool weights) {
   return row_shape(rows, d, d <= 8192 ? 8 : 16, d <= 1024 ? 512 : 1024, weights ? 16 : 24);
 }
