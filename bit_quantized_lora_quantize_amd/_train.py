@@ -63,8 +63,9 @@ def declare(L: ctypes.CDLL) -> None:
 
 # A call on a few rows is bound by host time: the helpers below stay cheap.
 
-_current_gpu = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream   # its handle, without a Stream object
+# (None in a PyTorch without GPU support, which still imports this package)
+_current_gpu = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # a handle, no Stream object
 
 
 def _call(name: str, at: int, *args) -> None:
@@ -294,7 +295,8 @@ def qlora_token_logp_bwd(logits: torch.Tensor, targets: torch.Tensor, lse: torch
                          dlogp: torch.Tensor, ignore_index: int = IGNORE_INDEX, scale: float = 1.0,
                          dlogits: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of the logits from upstream gradients of qlora_token_logp's
-    log-probabilities; dlogits may be the logits themselves.  A new one has the
+    log-probabilities, with the lse of that call on the same logits, targets and
+    scale; dlogits may be the logits themselves.  A new one has the
     logits' padding, unless that is 128 elements and a quarter of the vocabulary
     or more; the losses' gradients are laid out the same."""
     l, at = _logits(logits, targets, ignore_index, scale)
