@@ -195,7 +195,7 @@ def prepare(case, seed):
         s["X8"] = q.Packed8(m, i, s["xcodes"], s["xscale"])
         if case["op"] == "lin":
             s["w"] = q.NF4Weight(o, i, s["codes"], s["scale_codes"], s["scale2"], s["mean"])
-            s["ws"] = torch.empty(q.qlora_workspace_bytes(q.QLORA_OP_BWD, o, i, m, r), dtype=torch.uint8, device=DEV)
+            s["ws"] = torch.empty(q.qlora_workspace_bytes(q.QLORA_OP_BWD_PACKED, o, i, m, r), dtype=torch.uint8, device=DEV)
     return s
 
 
