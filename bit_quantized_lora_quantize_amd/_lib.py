@@ -28,6 +28,7 @@ HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "qlora.h")
 
 QLORA_OP_QUANTIZE, QLORA_OP_FWD, QLORA_OP_BWD = 0, 1, 2
 QLORA_OP_FWD_DROPOUT, QLORA_OP_BWD_DROPOUT = 3, 4
+QLORA_OP_BWD_PACKED, QLORA_OP_BWD_PACKED_DROPOUT = 5, 6
 QLORA_ERR_SCRATCH = -6
 QLORA_STATIC_SCRATCH_BYTES = 32 << 20
 QLORA_MAX_GROUP = 8
@@ -130,8 +131,9 @@ def lib() -> ctypes.CDLL:
         L.qlora_linear_bwd_dropout.argtypes = [ctypes.POINTER(_Nf4), _P, _P, _I64, _P, _P, _I64,
                                                ctypes.c_float, ctypes.POINTER(_Dropout), _P, _P,
                                                _P, _P, _P, ctypes.c_size_t, _P]
-        from . import _train
+        from . import _adapters, _train
         _train.declare(L)
+        _adapters.declare(L)
         _lib = L
     return _lib
 

@@ -194,6 +194,33 @@ BwdPlan plan_bwd(int64_t d_out, int64_t d_in, int64_t M, int64_t r, void* ws) {
   return p;
 }
 
+// Backward from an input kept in 8 bits, after the region of plan_bwd: U in
+// FP32, the operands of the token contractions and their partial results.
+struct PackedPlan {
+  float* u;                     // [M][r]
+  uint16_t *t_frags, *u_frags;
+  int tps;                      // tiles a token split
+  float *da_part, *db_part;     // [splits][r][d_in], [splits][d_out][r]
+  size_t bytes;
+};
+
+PackedPlan plan_packed(size_t base_bytes, int64_t d_out, int64_t d_in, int64_t M, int64_t r,
+                       void* ws) {
+  PackedPlan p{};
+  Carver c(ws);
+  c.off = base_bytes;
+  const int64_t tiles = cdiv(M, kPlanTile);
+  p.tps = plan_split_tiles(std::max<int64_t>(M, 1));
+  const int64_t splits = cdiv(tiles, p.tps), parts = splits > 1 ? splits : 0;
+  p.u = c.take<float>(M * r);
+  p.t_frags = c.take<uint16_t>(frag_elems(tiles, r));
+  p.u_frags = c.take<uint16_t>(frag_elems(tiles, r));
+  p.da_part = c.take<float>(parts * r * d_in);
+  p.db_part = c.take<float>(parts * r * d_out);
+  p.bytes = c.off + 256;
+  return p;
+}
+
 // General block sizes: supported parameters and the workspace.
 bool blocked_ok(int64_t n, int64_t block, int64_t group) {
   const auto pow2 = [](int64_t v) { return v > 0 && (v & (v - 1)) == 0; };
@@ -581,6 +608,68 @@ int bwd_impl(const qlora_nf4_t* q, const uint16_t* XA, const uint32_t* xmask,
   return hip_status(launch_grams(gp, 2, p.ldp, M, r, st));
 }
 
+// The backward from an input kept in 8 bits, after the checks.
+int bwd_packed_impl(const qlora_nf4_t* q, const qlora_packed_t* X8, const uint16_t* dY, int64_t M,
+                    const uint16_t* A, const uint16_t* B, int64_t r, float sc,
+                    const qlora_dropout_t* drop, DropoutArgs& da, const float* T, uint16_t* dX,
+                    const BwdPlan& p, const DropPlan& dp, const PackedPlan& pp, GramArgs8& ga,
+                    hipStream_t st) {
+  int s = QLORA_OK;
+  const int64_t d_out = q->d_out, d_in = q->d_in;
+  const uint32_t *rows = nullptr, *keep = nullptr;
+  if (drop) {
+    // the forward's saved mask, or the same bits again
+    const bool saved = M > kSmallM && drop->keep_rows && drop->keep_cols;
+    // (small M: the words fit the room that plan_drop has for a masked copy)
+    uint32_t* bits = dp.xm ? reinterpret_cast<uint32_t*>(dp.xm) : dp.rbits;
+    rows = saved ? drop->keep_rows : bits;
+    keep = saved ? drop->keep_cols : dp.keep;
+    if (!saved) {
+      da.keep = dp.keep;
+      da.M = M;
+      da.d = d_in;
+      da.ldw = dp.ldw;
+      s = hip_status(launch_dropout_bits(da, bits, st));
+      if (s) return s;
+    }
+    sc /= 1.0f - drop->p;
+  }
+  // U = s dY B as in bwd_impl, in FP32 and, for the input gradient, as hi | lo
+  const bool b_as_stored = M > kSmallM && d_out % 8 == 0 && r % 8 == 0 && aligned16(B);
+  if (!b_as_stored) {
+    s = hip_status(launch_transpose_bf16(B, d_out, r, p.bt, p.ldbt, st));
+    if (s) return s;
+  }
+  RankRowsArgs ra{dY, b_as_stored ? B : p.bt, M, r, d_out, b_as_stored ? r : p.ldbt, sc, pp.u,
+                  dX ? p.u_hl : nullptr, p.rp, nullptr, nullptr, 0};
+  ra.q_kn = b_as_stored;
+  s = rank_product(ra, p.r_part, st);
+  if (s) return s;
+  if (dX) {
+    GemmArgs g{q->codes, q->scale_codes, q->scale2, q->scale_mean, dY, p.u_hl, A, dX,
+               M,        d_out,          d_in,      r,            keep, dp.ldw};
+    s = hip_status(launch_gemm_bwd(g, st));
+    if (s) return s;
+  }
+  FragArgs fa{};
+  fa.M = M;
+  fa.slots = 1;
+  fa.r = (int)r;
+  fa.T = T;
+  fa.U = pp.u;
+  fa.t_frags = pp.t_frags;
+  fa.u_frags = pp.u_frags;
+  ga.q[0].codes = X8->codes;
+  ga.q[0].scale = X8->scale;
+  ga.q[0].keep = rows;
+  ga.q[0].frags = pp.u_frags;
+  ga.q[0].part = pp.da_part;
+  ga.q[1].x = dY;
+  ga.q[1].frags = pp.t_frags;
+  ga.q[1].part = pp.db_part;
+  return hip_status(launch_gram8(fa, ga, st));
+}
+
 }  // namespace
 
 namespace qlora {
@@ -636,6 +725,11 @@ size_t qlora_workspace_bytes(int op, int64_t d_out, int64_t d_in, int64_t M, int
     return plan_drop(plan_fwd(d_out, d_in, M, r, nullptr).bytes, M, d_in, false, nullptr).bytes;
   if (op == QLORA_OP_BWD_DROPOUT)
     return plan_drop(plan_bwd(d_out, d_in, M, r, nullptr).bytes, M, d_in, true, nullptr).bytes;
+  if (op == QLORA_OP_BWD_PACKED || op == QLORA_OP_BWD_PACKED_DROPOUT) {
+    size_t base = plan_bwd(d_out, d_in, M, r, nullptr).bytes;
+    if (op == QLORA_OP_BWD_PACKED_DROPOUT) base = plan_drop(base, M, d_in, true, nullptr).bytes;
+    return plan_packed(base, d_out, d_in, M, r, nullptr).bytes;
+  }
   return 0;
 }
 
@@ -904,6 +998,46 @@ int qlora_linear_bwd_dropout(const qlora_nf4_t* q, const uint16_t* X, const uint
                     dX, dA, dB, p, st);
   return bwd_impl(q, X, dp.rbits, dp.keep, dp.ldw, dY, M, A, B, r, sc, T_saved, dX, dA, dB, p,
                   st);
+}
+
+int qlora_linear_bwd_packed(const qlora_nf4_t* q, const qlora_packed_t* X8, const uint16_t* dY,
+                            int64_t M, const uint16_t* A, const uint16_t* B, int64_t r,
+                            float lora_alpha, const qlora_dropout_t* drop, const float* T_saved,
+                            uint16_t* dX, float* dA, float* dB, void* ws, size_t ws_bytes,
+                            void* stream) {
+  DropoutArgs da{};
+  int s = drop ? dropout_params(drop, &da) : QLORA_OK;
+  if (s) return s;
+  s = check_bwd(q, dY, dY, M, A, B, r, T_saved, dX, dA, dB, ws);
+  if (s) return s;
+  if (!X8 || (M > 0 && (!X8->codes || !X8->scale || !T_saved))) return QLORA_ERR_NULL;
+  if (X8->M != M || X8->d != q->d_in) return QLORA_ERR_SHAPE;
+  if (dX && dX == dY) return QLORA_ERR_SHAPE;   // dY is read after dX is written
+  if (!aligned16(X8->codes) || (reinterpret_cast<uintptr_t>(X8->scale) & 3u))
+    return QLORA_ERR_ALIGN;
+  const int64_t d_out = q->d_out, d_in = q->d_in;
+  const BwdPlan p = plan_bwd(d_out, d_in, M, r, ws);
+  DropPlan dp{};
+  size_t base = p.bytes;
+  if (drop) {
+    dp = plan_drop(base, M, d_in, true, ws);
+    base = dp.bytes;
+  }
+  const PackedPlan pp = plan_packed(base, d_out, d_in, M, r, ws);
+  if (ws_bytes < pp.bytes) return QLORA_ERR_WORKSPACE;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  GramArgs8 ga{};
+  ga.M = M;
+  ga.slots = 1;
+  ga.r = r;
+  ga.tps = pp.tps;
+  ga.q[0].out = dA;
+  ga.q[0].d = d_in;
+  ga.q[1].out = dB;
+  ga.q[1].d = d_out;
+  if (M == 0) return hip_status(launch_gram_zero(ga, st));
+  return bwd_packed_impl(q, X8, dY, M, A, B, r, lora_alpha / (float)r, drop, da, T_saved, dX, p, dp,
+                         pp, ga, st);
 }
 
 int qlora_nf4_blocked_sizes(int64_t n, int64_t block, int64_t group, size_t* codes_bytes,

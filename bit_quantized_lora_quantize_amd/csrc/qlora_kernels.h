@@ -561,6 +561,123 @@ struct PolicyArgs {
 hipError_t launch_policy(const LogitsArgs& l, const PolicyArgs& a, void* dlogits, int64_t ldd,
                          hipStream_t st);
 
+// ------------------------------------------------- activations in 8 bits
+// codes [M][round_up(d, 64)], scale [ceil(d / 64)][M].
+hipError_t launch_pack8(int type, const void* X, int64_t M, int64_t d, uint8_t* codes,
+                        float* scale, hipStream_t st);
+hipError_t launch_unpack8(const uint8_t* codes, const float* scale, int64_t M, int64_t d, int type,
+                          void* X, hipStream_t st);
+
+// ------------------------------------------------- adapters of many requests
+// The plan of a batch: its tokens sorted by slot, those without adapter last,
+// in tiles of up to kPlanTile tokens of one slot.
+constexpr int kPlanTile = 64;
+constexpr int kPlanMaxSlots = 2048;
+constexpr int kPlanMagic = 0x51504C4E;
+// head[]: tiles of tokens with an adapter, tiles of all, splits, M, slots
+constexpr int kPlanTiles = 0, kPlanAllTiles = 1, kPlanSplits = 2, kPlanTokens = 3, kPlanSlots = 4,
+              kPlanMagicAt = 5, kPlanHead = 16;
+struct PlanView {
+  int32_t* head;   // [kPlanHead]; NULL (contractions only): one slot, every token, in order
+  int32_t* order;  // [M] token at each position
+  int32_t* begin;  // [slots + 1] first position of each slot (batches of several spans)
+  int4* tile;      // {slot (-1: none), first position, tokens, 0}
+  int4* split;     // {slot, first tile, tiles, number among its slot's splits (-1: the only one)}
+  int2* parts;     // [slots] {its splits' first partial result, its splits}
+  int32_t* hist;   // scratch of the plan's own kernels
+};
+// Tiles of a token split of the weight gradients: four splits or more from 256
+// tokens a split on, at most about 64 splits of one slot.
+inline int plan_split_tiles(int64_t M) {
+  const int64_t tiles = (M + kPlanTile - 1) / kPlanTile;
+  const int64_t four = std::min<int64_t>(16, std::max<int64_t>(4, (tiles + 3) / 4));
+  return (int)std::max<int64_t>(four, (tiles + 63) / 64);
+}
+// Bounds of what the device counts.
+inline int64_t plan_most_tiles(int64_t M, int64_t slots) {
+  return std::min<int64_t>(M, M / kPlanTile + slots + 1);
+}
+inline int64_t plan_most_splits(int64_t M, int64_t slots) {
+  return std::min<int64_t>(M, M / (int64_t(kPlanTile) * plan_split_tiles(M)) + slots);
+}
+// Splits of slots that have two or more: such a slot with n tokens has at most
+// twice n / (tokens of a split).
+inline int64_t plan_most_parts(int64_t M) {
+  return 2 * M / (int64_t(kPlanTile) * plan_split_tiles(M));
+}
+hipError_t launch_plan(const PlanView& p, const int32_t* index, int64_t M, int64_t slots,
+                       hipStream_t st);
+
+// Ranges of the long axis K that k_shrink sums apart.
+inline int shrink_splits(int64_t M, int64_t K, int64_t* kper) {
+  const int64_t tiles = std::max<int64_t>(1, (M + kPlanTile - 1) / kPlanTile);
+  int64_t s = std::min<int64_t>((512 + tiles - 1) / tiles, (K + 255) / 256);
+  s = std::max<int64_t>(1, std::min<int64_t>(s, 16));
+  *kper = ((K + s - 1) / s + 255) / 256 * 256;
+  return (int)((K + *kper - 1) / *kper);
+}
+struct ShrinkArgs {
+  PlanView plan;
+  int64_t M, slots, K, kper;
+  int r, splits;        // splits, kper: set by launch_shrink
+  bool kn;              // F as [K][r] (else [r][K])
+  const uint16_t* P;    // [M][K]
+  const uint16_t* F;    // [slots] of them
+  float* part;          // [splits][M][r], by position
+};
+hipError_t launch_shrink(const ShrinkArgs& a, hipStream_t st);
+
+struct ExpandArgs {
+  PlanView plan;
+  int64_t M, slots, K, d, cper;
+  int r, splits, chunks;   // splits, chunks, cper: set by launch_expand
+  bool rd;                 // F as [r][d] (else [d][r])
+  const float* part;       // of launch_shrink with the same K
+  const float* scale;      // [slots]
+  const uint16_t* F;       // [slots] of them
+  const uint16_t* in;      // [M][d], NULL: zeros; may be out
+  uint16_t* out;
+  float* v_out;            // [M][r] or NULL: scale * sums, by token, 0 without an adapter
+};
+hipError_t launch_expand(const ExpandArgs& a, hipStream_t st);
+
+// Blocks of 16 ranks in the operands of the contractions.
+inline int frag_blocks(int64_t r) {
+  return r <= 16 ? 1 : (r <= 32 ? 2 : (r <= 64 ? 4 : (r <= 128 ? 8 : 16)));
+}
+// Elements of one side's operands for `tiles` tiles.
+inline int64_t frag_elems(int64_t tiles, int64_t r) { return tiles * 3 * frag_blocks(r) * 1024; }
+struct FragArgs {
+  PlanView plan;
+  int64_t M, slots;
+  int r, nb;               // nb: set by launch_gram8
+  int splits;              // of U's partial sums by position; 0: U by token, scaled
+  const float* scale;      // [slots], with splits
+  const float* T;          // [M][r] by token
+  const float* U;
+  uint16_t* t_frags;
+  uint16_t* u_frags;
+};
+struct GramSide {
+  const uint16_t* x;       // BF16 [M][d], or
+  const uint8_t* codes;    // 8-bit codes [M][round_up(d, 64)] (side 0 only) with
+  const float* scale;      // their scales [ceil(d / 64)][M] and
+  const uint32_t* keep;    // keep words [M][d / 32] or NULL
+  const uint16_t* frags;   // U's or T's
+  float* out;              // [slots][r][d], side 1 [slots][d][r]
+  float* part;             // partial results, [][r][d] or [][d][r]
+  int64_t d;
+};
+struct GramArgs8 {
+  PlanView plan;
+  int64_t M, slots, r;
+  int tps;                 // without a plan: tiles a split
+  GramSide q[2];           // dA from (U, X), dB from (T, dY)
+};
+hipError_t launch_gram8(const FragArgs& f, const GramArgs8& a, hipStream_t st);
+// Zeros in both outputs.
+hipError_t launch_gram_zero(const GramArgs8& a, hipStream_t st);
+
 // ------------------------------------------------- host-side checks
 // qlora_linear_fwd's argument checks for a workspace of ws_bytes bytes (not
 // dereferenced): QLORA_ERR_WORKSPACE when the call needs more.

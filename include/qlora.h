@@ -93,6 +93,8 @@ int qlora_nf4_sizes(int64_t d_out, int64_t d_in, size_t *codes_bytes,
 #define QLORA_OP_BWD 2
 #define QLORA_OP_FWD_DROPOUT 3
 #define QLORA_OP_BWD_DROPOUT 4
+#define QLORA_OP_BWD_PACKED 5          /* qlora_linear_bwd_packed */
+#define QLORA_OP_BWD_PACKED_DROPOUT 6  /* the same with dropout   */
 
 /* Device workspace (bytes) that one call of `op` needs for these sizes
  * (M and r are ignored for QLORA_OP_QUANTIZE).  Host only.  Returns 0 for
@@ -675,6 +677,130 @@ int qlora_policy_loss(const qlora_logits_t *l, const int64_t *offsets,
                       size_t workspace_bytes, void *stream);
 /* Host only; 0 for sizes outside the documented range. */
 size_t qlora_policy_workspace_bytes(int64_t rows, int64_t sequences);
+
+/*
+ * Activations in 8 bits: what a training step keeps of a layer's input for the
+ * backward, at 1 + 1/16 bytes a value.  Blocks of 64 values of a row (the last
+ * one shorter where d % 64 != 0) share an FP32 scale:
+ *     a = max |x| over the block,  scale = RN(a / 127)
+ *     code = the integer nearest to 127 x / a, ties to even (exactly decided)
+ *     restored x = RN(RN_fp32(code * scale)), rounded to its type
+ * (the scale stops where 127 times it is FP32's largest value).  Blocks with
+ * a < 2^-119 restore as zeros.  A block that holds an infinity or a
+ * NaN restores as NaN in all its elements.  Deterministic.
+ *   codes  int8 [M, round_up(d, 64)] (16B); columns d .. are written as 0
+ *   scale  FP32 [ceil(d / 64), M]: block by block, so that the scales of
+ *          neighbouring tokens lie together
+ * 0 <= M <= 2^21, 1 <= d <= 2^21.  X [M, d] of `type` (QLORA_BF16, QLORA_F32)
+ * needs the alignment of its element type only; 16-byte aligned rows are
+ * fastest.
+ */
+typedef struct {
+  int64_t M, d;
+  uint8_t *codes;
+  float *scale;
+} qlora_packed_t;
+
+/* Byte sizes of the two buffers (host only). */
+int qlora_pack8_sizes(int64_t M, int64_t d, size_t *codes_bytes, size_t *scale_bytes);
+int qlora_pack8(int type, const void *X, const qlora_packed_t *p, void *stream);
+int qlora_unpack8(const qlora_packed_t *p, int type, void *X, void *stream);
+
+/*
+ * qlora_linear_bwd from an input kept in 8 bits: X is the BF16 matrix that
+ * qlora_unpack8 restores from X8, which is never written out.  dA and dB take
+ * U and T with 24 bits, where qlora_linear_bwd takes 16.
+ *   X8       M tokens of d_in values; T_saved is required (the forward's T).
+ *   drop     NULL, or the forward's LoRA dropout: as qlora_linear_bwd_dropout
+ *            (saved mask or regenerated; T_saved from that forward).
+ * Other arguments and limits as qlora_linear_bwd; workspace (16B) >=
+ * qlora_workspace_bytes(QLORA_OP_BWD_PACKED, ...), with drop
+ * QLORA_OP_BWD_PACKED_DROPOUT.
+ */
+int qlora_linear_bwd_packed(const qlora_nf4_t *q, const qlora_packed_t *X8,
+                            const uint16_t *dY, int64_t M, const uint16_t *A,
+                            const uint16_t *B, int64_t r, float lora_alpha,
+                            const qlora_dropout_t *drop, const float *T_saved,
+                            uint16_t *dX, float *dA, float *dB, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/*
+ * Low-rank adapters of many requests beside one shared projection: a bank of
+ * `slots` adapters of one rank (lower ranks padded with zeros), each token with
+ * the adapter of its own request or with none.
+ *   A      BF16 [slots, r, d_in]
+ *   B      BF16 [slots, d_out, r]
+ *   scale  FP32 [slots] device memory: lora_alpha / r of each
+ * 1 <= slots <= 2048, 1 <= r <= 256, 1 <= d_in, d_out <= 2^21.  Arrays of these
+ * entry points need the alignment of their element type only (the plan and the
+ * workspace: 16 bytes); 16-byte aligned rows (widths and, in B, a rank that are
+ * multiples of 8) are fastest.  Infinities and NaN of a token stay with that
+ * token in Y, T and dX and reach its own slot's dA and dB; a slot's stay with
+ * its tokens.
+ */
+typedef struct {
+  int64_t slots, r, d_in, d_out;
+  const uint16_t *A;
+  const uint16_t *B;
+  const float *scale;
+} qlora_adapters_t;
+
+/*
+ * The plan of a batch, made once for all of its projections and both
+ * directions: its tokens sorted by slot.
+ *   index  int32 [M] device memory: each token's slot; a value outside
+ *          [0, slots) means no adapter.  0 <= M <= 2^21.
+ *   plan   (16B) device memory of qlora_adapters_plan_bytes(M, slots) bytes
+ *          (host only; 0 for sizes the call would reject), an output that the
+ *          calls below read.  They write nothing where the plan they get was
+ *          made for another M or number of slots.
+ */
+size_t qlora_adapters_plan_bytes(int64_t M, int64_t slots);
+int qlora_adapters_plan(const int32_t *index, int64_t M, int64_t slots, void *plan,
+                        size_t plan_bytes, void *stream);
+
+/*
+ * Forward: for token m with the adapter a,
+ *     T[m] = scale_a X[m] A_a^T,    Y[m] = RN(Y0[m] + T[m] B_a^T),
+ * without one T[m] = 0 and Y[m] = Y0[m].  Y0 is the shared projection's output
+ * (a qlora_linear_fwd with lora_alpha = 0, or any other).  Products take BF16
+ * inputs and accumulate in FP32; T enters the second as a hi + lo BF16 pair.
+ *   X       BF16 [M, d_in] (rows of tokens without an adapter are not read)
+ *   Y0      BF16 [M, d_out] or NULL (zeros)
+ *   Y       BF16 [M, d_out] output, may be Y0
+ *   T_save  FP32 [M, r] or NULL: for the backward
+ * workspace (16B) >= qlora_adapters_workspace_bytes(0, bank, M).  Deterministic;
+ * a token's results do not depend on the other tokens' values.
+ */
+int qlora_adapters_fwd(const qlora_adapters_t *bank, const void *plan, size_t plan_bytes,
+                       const uint16_t *X, int64_t M, const uint16_t *Y0, uint16_t *Y,
+                       float *T_save, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Backward of qlora_adapters_fwd for the upstream gradient dY:
+ *     U[m] = scale_a dY[m] B_a,        dX[m] = RN(dX0[m] + U[m] A_a)
+ *     dA_a = sum of U[m]^T X[m],       dB_a = sum of dY[m]^T T[m]
+ * over the tokens m of slot a; dX[m] = dX0[m] for a token without an adapter,
+ * zeros in dA and dB for a slot without tokens.  U enters dX as a hi + lo BF16
+ * pair, U and T enter dA and dB with 24 bits.
+ *   X, X8    the forward's X: BF16 [M, d_in], or kept in 8 bits (M tokens of
+ *            d_in values, restored to BF16); exactly one, the other NULL
+ *   T        FP32 [M, r]: the forward's T_save
+ *   dY       BF16 [M, d_out]
+ *   dX0      BF16 [M, d_in] or NULL (zeros): the shared projection's gradient
+ *   dX       BF16 [M, d_in] output, may be dX0 (not X or dY); NULL to skip
+ *   dA       FP32 [slots, r, d_in], dB FP32 [slots, d_out, r]: overwritten
+ *            (M = 0 writes zeros)
+ * workspace (16B) >= qlora_adapters_workspace_bytes(1, bank, M).  Sums over
+ * tokens have a fixed order: deterministic.
+ */
+int qlora_adapters_bwd(const qlora_adapters_t *bank, const void *plan, size_t plan_bytes,
+                       const uint16_t *X, const qlora_packed_t *X8, const float *T,
+                       const uint16_t *dY, int64_t M, const uint16_t *dX0, uint16_t *dX,
+                       float *dA, float *dB, void *workspace, size_t workspace_bytes,
+                       void *stream);
+/* Host only; 0 for sizes the calls would reject. */
+size_t qlora_adapters_workspace_bytes(int backward, const qlora_adapters_t *bank, int64_t M);
 
 /* Static English text for a qlora_status value. */
 const char *qlora_status_string(int status);
