@@ -17,8 +17,21 @@
 // tokens).  Products are BF16 on the matrix cores with FP32 sums; T and U are
 // FP32 and enter them as sums of BF16 terms: two (16 bits) where the result is
 // rounded to BF16, three (24 bits, all of FP32) where it is FP32.
+#include <type_traits>
+
 #include "qlora_device.h"
 #include "qlora_kernels.h"
+#include "row_ops.h"
+
+#ifndef EXPAND_OCC
+#define EXPAND_OCC 3
+#endif
+#ifndef EXPAND_WGS
+#define EXPAND_WGS 1024
+#endif
+#ifndef EXPAND_AHEAD
+#define EXPAND_AHEAD 2
+#endif
 
 namespace qlora {
 
@@ -35,19 +48,26 @@ __device__ __forceinline__ uint2 lds_tr(const uint16_t* p) {
 
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu); }
 
-// Eight elements from column `col` on, zero at and past `end`.  VEC: `row` and
-// `end` allow whole 16-byte pieces.
-template <bool VEC>
+// Eight elements of a row from column `col` on, zero at and past `end`.  Rows
+// start at any element: the vector need not be aligned.
 __device__ __forceinline__ u32x4 load8(const uint16_t* row, int64_t col, int64_t end) {
-  if (VEC) {
-    u32x4 v = {0, 0, 0, 0};
-    if (col < end) v = *reinterpret_cast<const u32x4*>(row + col);
-    return v;
-  }
+  if (col + 8 <= end) return load_vec(row + col);
   uint32_t h[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) h[e] = col + e < end ? (uint32_t)row[col + e] : 0u;
   return u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
+}
+__device__ __forceinline__ u32x4 only_if(bool ok, u32x4 v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = ok ? v[j] : 0u;
+  return v;
+}
+
+// A barrier for data in LDS alone: loads from memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // A plan of other sizes than the call's: nothing is done for it.
@@ -173,7 +193,9 @@ __device__ void plan_lists(const PlanView& p, int M, int slots, int tps, int* cn
     }
     const int j = i - split0[lo], n = split0[lo + 1] - split0[lo];
     const int first = tile0[lo] + j * tps;
-    p.split[i] = int4{lo, first, min(tps, tile0[lo + 1] - first), n > 1 ? j : -1};
+    const int end = cnt[lo + 1];
+    p.split_first[i] = cnt[lo] + 64 * j * tps;
+    p.split[i] = int4{lo, first, min(64 * tps, end - cnt[lo] - 64 * j * tps), n > 1 ? j : -1};
   }
   if (threadIdx.x == 0) {
     p.head[kPlanTiles] = with_one;
@@ -269,350 +291,681 @@ __global__ __launch_bounds__(64) void k_plan_place(PlanView p, const int32_t* __
 // of a tile and the factor of their slot; F is stored [r][K] (A in the forward)
 // or, KN, [K][r] (B in the backward).
 //
-// Item = one tile and one of `splits` ranges of K.  The W wavefronts of a
-// workgroup take the range's steps of 32 columns in turn, each all 64 tokens and
-// all ranks: no wavefront loads what another loads, and the loop has no
-// barrier.  Their sums are added through LDS at the end, in wavefront order.
-// KN: a step's 32 rows of F go through LDS of the wavefront's own, which the
-// transposing reads turn into operands.
+// Item = one tile and one of `splits` ranges of K.  The four wavefronts of a
+// workgroup take the range's steps in turn, each all 64 tokens and all ranks:
+// no wavefront loads what another loads, and the loop has no barrier.  Their
+// sums are added through LDS at the end, in wavefront order.  KN: a step's rows
+// of F go through LDS of the wavefront's own, which the transposing reads turn
+// into operands.
 // ---------------------------------------------------------------------------
+#ifndef SHRINK_W
+#define SHRINK_W 4
+#endif
+#ifndef SHRINK_SK
+#define SHRINK_SK 2
+#endif
+#ifndef SHRINK_AHEAD
+#define SHRINK_AHEAD 0
+#endif
 template <int NB>
-constexpr int shrink_waves() { return NB <= 4 ? 8 : 4; }
+constexpr int shrink_waves() { return NB <= 4 ? SHRINK_W : 4; }
+// K slices of 32 per step
+template <int NB>
+constexpr int shrink_slices() { return NB <= 4 ? SHRINK_SK : 1; }
 template <int NB, bool KN>
 constexpr int shrink_lds() {
-  constexpr int W = shrink_waves<NB>(), CN = NB < 4 ? NB : 4;
-  constexpr int red = W * 16 * 16 * CN * 4, stage = KN ? W * 32 * (16 * NB + 8) * 2 : 0;
+  constexpr int CN = NB < 4 ? NB : 4;
+  constexpr int red = shrink_waves<NB>() * 16 * 16 * CN * 4;
+  constexpr int stage = KN ? shrink_waves<NB>() * 32 * shrink_slices<NB>() * (16 * NB + 8) * 2 : 0;
   return red > stage ? red : stage;
 }
 
-template <int NB, bool KN, bool VEC>
-__global__ __launch_bounds__(64 * shrink_waves<NB>()) void k_shrink(ShrinkArgs a) {
-  constexpr int W = shrink_waves<NB>(), CN = NB < 4 ? NB : 4;
+// V's row of a position as k_expand's operand: BF16 hi, then lo, of rp ranks.
+__device__ __forceinline__ void put_vrow(uint16_t* vrows, int64_t pos, int i, int rp, float v) {
+  float hi, lo;
+  split_bf16(v, hi, lo);
+  uint16_t* row = vrows + pos * 2 * rp;
+  row[i] = (uint16_t)(__float_as_uint(hi) >> 16);
+  row[rp + i] = bf16_bits(lo);
+}
+
+// One item with RB blocks of 16 tokens.  R8: F's rows of r are whole 16-byte
+// pieces (KN).
+template <int NB, bool KN, bool R8, int RB>
+__device__ __forceinline__ void shrink_item(const ShrinkArgs& a, const int4& td, int s, uint8_t* lds) {
+  constexpr int W = shrink_waves<NB>(), CN = NB < 4 ? NB : 4, SK = shrink_slices<NB>();
   constexpr int LF = 16 * NB + 8;                  // staged row of F, elements
-  extern __shared__ __attribute__((aligned(16))) uint8_t slds[];
-  if (!plan_fits(a.plan, a.M, a.slots)) return;
+  constexpr int STEP = 32 * SK;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
   const int64_t K = a.K;
   const int r = a.r;
-  const int items = a.plan.head[kPlanTiles] * a.splits;
-  uint16_t* stage = reinterpret_cast<uint16_t*>(slds) + w * 32 * LF;
-  float* red = reinterpret_cast<float*>(slds);
-
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int t = item / a.splits, s = item % a.splits;
-    const int4 td = a.plan.tile[t];
-    const int slot = td.x, first = td.y, count = td.z;
-    const int64_t k_begin = (int64_t)s * a.kper;
-    const int64_t k_end = k_begin + a.kper < K ? k_begin + a.kper : K;
-    const uint16_t* xp[4];   // rows past the tile's last repeat it; their sums are not stored
+  uint16_t* stage = reinterpret_cast<uint16_t*>(lds) + w * STEP * LF;
+  float* red = reinterpret_cast<float*>(lds);
+  const int slot = td.x, first = td.y, count = td.z;
+  const int64_t k_begin = (int64_t)s * a.kper;
+  const int64_t k_end = k_begin + a.kper < K ? k_begin + a.kper : K;
+  const uint16_t* F = a.F + (int64_t)slot * r * K;
+  const uint16_t* xp[RB];   // rows past the tile's last repeat it; their sums are not stored
 #pragma unroll
-    for (int rb = 0; rb < 4; ++rb) {
-      const int row = min(16 * rb + r16, count - 1);
-      xp[rb] = a.P + (int64_t)a.plan.order[first + row] * K;
+  for (int rb = 0; rb < RB; ++rb) {
+    const int row = min(16 * rb + r16, count - 1);
+    xp[rb] = a.P + (int64_t)a.plan.order[first + row] * K + 8 * g;
+  }
+
+  f32x4 acc[RB][NB];
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) acc[rb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // whole steps: loads without conditions, a step ahead (F's first: their
+  // addresses wait for nothing)
+  auto load = [&](int64_t k, u32x4 (&x)[SK][RB], u32x4 (&f)[SK * NB]) {
+#pragma unroll
+    for (int u = 0; u < SK * NB; ++u) {
+      if (KN) {
+        const int piece = lane + 64 * u, row = piece / (2 * NB), col = 8 * (piece % (2 * NB));
+        f[u] = load_vec(F + (k + row) * r + (col < r ? col : 0));
+      } else {
+        const int i = min(16 * (u / SK) + r16, r - 1);
+        f[u] = load_vec(F + i * K + k + 32 * (u % SK) + 8 * g);
+      }
     }
-    const uint16_t* F = a.F + (int64_t)slot * r * K;
-
-    f32x4 acc[4][NB];
 #pragma unroll
-    for (int rb = 0; rb < 4; ++rb)
+    for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) acc[rb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    // whole steps: loads without conditions, a step ahead
-    auto load = [&](int64_t k, u32x4 (&x)[4], u32x4 (&f)[NB]) {
+      for (int sl = 0; sl < SK; ++sl) x[sl][rb] = load_vec(xp[rb] + k + 32 * sl);
+  };
+  auto compute = [&](const u32x4 (&x)[SK][RB], const u32x4 (&f)[SK * NB]) {
+    if (KN) {
 #pragma unroll
-      for (int rb = 0; rb < 4; ++rb) x[rb] = *reinterpret_cast<const u32x4*>(xp[rb] + k + 8 * g);
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        if (KN) {
-          const int piece = lane + 64 * nb, row = piece / (2 * NB), col = 8 * (piece % (2 * NB));
-          f[nb] = *reinterpret_cast<const u32x4*>(F + (k + row) * r + (col < r ? col : 0));
-        } else {
-          const int i = min(16 * nb + r16, r - 1);
-          f[nb] = *reinterpret_cast<const u32x4*>(F + i * K + k + 8 * g);
-        }
+      for (int u = 0; u < SK * NB; ++u) {
+        const int piece = lane + 64 * u, row = piece / (2 * NB), col = 8 * (piece % (2 * NB));
+        *reinterpret_cast<u32x4*>(stage + row * LF + col) = f[u];
       }
-    };
-    auto put_stage = [&](const u32x4 (&f)[NB]) {
+    }
+#pragma unroll
+    for (int sl = 0; sl < SK; ++sl)
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const int piece = lane + 64 * nb, row = piece / (2 * NB), col = 8 * (piece % (2 * NB));
-        *reinterpret_cast<u32x4*>(stage + row * LF + col) = f[nb];
-      }
-    };
-    auto compute = [&](const u32x4 (&x)[4], const u32x4 (&f)[NB]) {
-      if (KN) put_stage(f);
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        u32x4 q = f[nb];
+        u32x4 q = f[nb * SK + sl];
         if (KN) {
-          const uint16_t* p = stage + (8 * g + (r16 >> 2)) * LF + 16 * nb + 4 * (r16 & 3);
+          const uint16_t* p = stage + (32 * sl + 8 * g + (r16 >> 2)) * LF + 16 * nb + 4 * (r16 & 3);
           const uint2 lo = lds_tr(p), hi = lds_tr(p + 4 * LF);
           q = u32x4{lo.x, lo.y, hi.x, hi.y};
         }
 #pragma unroll
-        for (int rb = 0; rb < 4; ++rb) acc[rb][nb] = mfma16(x[rb], q, acc[rb][nb]);
+        for (int rb = 0; rb < RB; ++rb) acc[rb][nb] = mfma16(x[sl][rb], q, acc[rb][nb]);
       }
-    };
-    int64_t k = k_begin + 32 * w;
-    const int64_t k_whole = k_begin + (VEC ? (k_end - k_begin) / 32 * 32 : 0);
-    if (k < k_whole) {
-      const int64_t k_last = k + (k_whole - 1 - k) / (32 * W) * (32 * W);
-      u32x4 xa[4], fa[NB], xb[4], fb[NB];
+  };
+  int64_t k = k_begin + STEP * w;
+  // (a piece of F's rows of odd r may reach into the next row, which the last
+  // row of all does not have)
+  const int64_t k_whole = k_begin + (k_end - k_begin - (KN && !R8 && k_end == K ? 1 : 0)) / STEP * STEP;
+  if (k < k_whole) {
+    const int64_t k_last = k + (k_whole - 1 - k) / (STEP * W) * (STEP * W);
+    if constexpr (SHRINK_AHEAD) {
+      u32x4 xa[SK][RB], fa[SK * NB], xb[SK][RB], fb[SK * NB];
       load(k, xa, fa);
-      for (; k <= k_last; k += 64 * W) {
-        load(min(k + 32 * W, k_last), xb, fb);
+      for (; k <= k_last; k += 2 * STEP * W) {
+        load(min(k + STEP * W, k_last), xb, fb);
+        __builtin_amdgcn_sched_barrier(0);
         compute(xa, fa);
-        load(min(k + 64 * W, k_last), xa, fa);
-        if (k + 32 * W <= k_last) compute(xb, fb);
+        load(min(k + 2 * STEP * W, k_last), xa, fa);
+        __builtin_amdgcn_sched_barrier(0);
+        if (k + STEP * W <= k_last) compute(xb, fb);
       }
-      k = k_last + 32 * W;
-    }
-    // the rest: single elements, or the pieces of a last, partial step
-    for (; k < k_end; k += 32 * W) {
-      u32x4 x[4], f[NB];
-#pragma unroll
-      for (int rb = 0; rb < 4; ++rb) x[rb] = load8<VEC>(xp[rb], k + 8 * g, k_end);
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        if (KN) {
-          const int piece = lane + 64 * nb, row = piece / (2 * NB), col = 8 * (piece % (2 * NB));
-          f[nb] = k + row < k_end ? load8<VEC>(F + (k + row) * r, col, r) : u32x4{0, 0, 0, 0};
-        } else {
-          f[nb] = load8<VEC>(F + min(16 * nb + r16, r - 1) * K, k + 8 * g, k_end);
-        }
+    } else {
+      u32x4 x[SK][RB], f[SK * NB];
+      for (; k <= k_last; k += STEP * W) {
+        load(k, x, f);
+        __builtin_amdgcn_sched_barrier(0);
+        compute(x, f);
       }
-      compute(x, f);
     }
+    k = k_last + STEP * W;
+  }
+  // the last, partial step
+  for (; k < k_end; k += STEP * W) {
+    u32x4 x[SK][RB], f[SK * NB];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+      for (int sl = 0; sl < SK; ++sl)
+        x[sl][rb] = load8(xp[rb] - 8 * g, k + 32 * sl + 8 * g, k_end);
+#pragma unroll
+    for (int u = 0; u < SK * NB; ++u) {
+      if (KN) {
+        const int piece = lane + 64 * u, row = piece / (2 * NB), col = 8 * (piece % (2 * NB));
+        f[u] = k + row < k_end ? load8(F + (k + row) * r, col, r) : u32x4{0, 0, 0, 0};
+      } else {
+        const int i = min(16 * (u / SK) + r16, r - 1);
+        f[u] = load8(F + i * K, k + 32 * (u % SK) + 8 * g, k_end);
+      }
+    }
+    compute(x, f);
+  }
 
-    // accumulator lane (r16, g): tokens 16 rb + 4 g + v, rank 16 nb + r16
-    float* part = a.part + ((int64_t)s * a.M + first) * r;
+  // accumulator lane (r16, g): tokens 16 rb + 4 g + v, rank 16 nb + r16
+  float* part = a.part + ((int64_t)s * a.M + first) * r;
+  const float sc = a.vrows ? a.scale[slot] : 0.0f;
 #pragma unroll
-    for (int rb = 0; rb < 4; ++rb) {
-      if (16 * rb >= count) break;
+  for (int rb = 0; rb < RB; ++rb) {
+    if (16 * rb >= count) break;
 #pragma unroll
-      for (int n0 = 0; n0 < NB; n0 += CN) {
-        __syncthreads();   // the stage, or the last block, is no longer read
+    for (int n0 = 0; n0 < NB; n0 += CN) {
+      lds_barrier();   // the stage, or the last block, is no longer read
 #pragma unroll
-        for (int nb = 0; nb < CN; ++nb)
+      for (int nb = 0; nb < CN; ++nb)
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            red[(w * 16 + 4 * g + v) * 16 * CN + 16 * nb + r16] = acc[rb][n0 + nb][v];
-        __syncthreads();
-        for (int e = threadIdx.x; e < 256 * CN; e += 64 * W) {
-          const int row = e / (16 * CN), i = 16 * n0 + e % (16 * CN);
-          float sum = red[e];
+        for (int v = 0; v < 4; ++v)
+          red[(w * 16 + 4 * g + v) * 16 * CN + 16 * nb + r16] = acc[rb][n0 + nb][v];
+      lds_barrier();
 #pragma unroll
-          for (int ww = 1; ww < W; ++ww) sum += red[ww * 256 * CN + e];
-          if (16 * rb + row < count && i < r) part[(int64_t)(16 * rb + row) * r + i] = sum;
+      for (int e0 = 0; e0 < 256 * CN; e0 += 64 * W) {
+        const int e = e0 + threadIdx.x;
+        if (256 * CN % (64 * W) != 0 && e >= 256 * CN) break;
+        const int row = e / (16 * CN), i = 16 * n0 + e % (16 * CN);
+        float sum = red[e];
+#pragma unroll
+        for (int ww = 1; ww < W; ++ww) sum += red[ww * 256 * CN + e];
+        if (16 * rb + row >= count) continue;
+        if (a.vrows) {
+          const int pos = first + 16 * rb + row;
+          const float v = i < r ? sum * sc : 0.0f;
+          put_vrow(a.vrows, pos, i, 32 * ((NB + 1) / 2), v);
+          if (NB == 1) put_vrow(a.vrows, pos, i + 16, 32, 0.0f);
+          if (a.v_out && i < r) a.v_out[(int64_t)a.plan.order[pos] * r + i] = v;
+        } else if (i < r) {
+          part[(16 * rb + row) * r + i] = sum;
         }
       }
     }
-    __syncthreads();
+  }
+  lds_barrier();
+}
+
+#ifndef SHRINK_OCC
+#define SHRINK_OCC 2
+#endif
+template <int NB>
+constexpr int shrink_occ() { return NB <= 4 ? SHRINK_OCC : 1; }
+template <int NB, bool KN, bool R8>
+__global__ __launch_bounds__(64 * shrink_waves<NB>(), shrink_occ<NB>()) void k_shrink(ShrinkArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t slds[];
+  // the grid has no more workgroups than the list room for items
+  int4 td = a.plan.tile[blockIdx.x / a.splits];
+  if (!plan_fits(a.plan, a.M, a.slots) || td.z <= 0) return;
+  const int items = a.plan.head[kPlanTiles] * a.splits;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int t = item / a.splits, s = item % a.splits;
+    if (item != (int)blockIdx.x) td = a.plan.tile[t];
+    // few tokens: no registers and loads for blocks of tokens that are not there
+    if (td.z <= 16) shrink_item<NB, KN, R8, 1>(a, td, s, slds);
+    else shrink_item<NB, KN, R8, 4>(a, td, s, slds);
+  }
+}
+
+// The sums of k_shrink's partial results, in order: up to Q pieces of N ranks
+// from part + at[] on, `stride` between the splits.  Few splits: every load at
+// once; many: one piece's at once.
+template <int Q, int N>
+__device__ __forceinline__ void sum_parts(const float* part, const int (&at)[Q], const bool (&on)[Q],
+                                          int splits, int64_t stride, float (&v)[Q][N]) {
+  typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
+  auto get = [&](const float* p, float* f) {
+    if constexpr (N == 4) {
+      const vec x = *reinterpret_cast<const vec*>(p);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = x[j];
+    } else {
+      f[0] = *p;
+    }
+  };
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[q][j] = 0.0f;
+  if (splits <= 4) {
+    float x[4][Q][N];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        if (s < splits && on[q]) get(part + s * stride + at[q], x[s][q]);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        if (s < splits && on[q]) {
+#pragma unroll
+          for (int j = 0; j < N; ++j) v[q][j] = s == 0 ? x[s][q][j] : v[q][j] + x[s][q][j];
+        }
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    if (!on[q]) continue;
+    float x[16][N];
+#pragma unroll
+    for (int s = 0; s < 16; ++s)
+      if (s < splits) get(part + s * stride + at[q], x[s]);
+#pragma unroll
+    for (int s = 0; s < 16; ++s)
+      if (s < splits) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[q][j] = s == 0 ? x[s][j] : v[q][j] + x[s][j];
+      }
   }
 }
 
 // ---------------------------------------------------------------------------
 // out[token][n] = RN(in[token][n] + sum_i V[token][i] F[n][i]),
-// V = scale_a * (the partial sums of k_shrink, in order), for the tokens of a
-// tile and a chunk of n.  F is stored [d][r] (B in the forward) or, RN_,
-// [r][d] (A in the backward).  The tile's V goes to LDS as BF16 hi + lo; a
-// wavefront takes 64 columns at a time, all tokens.  F is the row operand of
-// the MFMA: with its rows n = 16 (j / 4) + 4 blk + j % 4 a lane ends up with 16
-// consecutive columns of one token.
+// V of k_shrink or k_finish as BF16 hi + lo.  F is stored [d][r] (B in the
+// forward) or, RD, [r][d] (A in the backward).  Item = a few tiles of one slot
+// and 256 columns, whose part of F stays in LDS: a wavefront takes 16 tokens of a
+// tile at a time, 512 bytes of each row, and loads the next tile's while it works
+// on this one, without a barrier.  Neighbouring items are the neighbouring
+// columns of the same tokens, so that what the chip works on at a time is whole
+// rows.  F is the row operand of the MFMA: with its rows in the order of
+// unit_column a lane ends up with twice eight consecutive columns of a token; LDS
+// of the wavefront's own turns them so that its loads and stores are whole
+// 128-byte lines (64 bytes of 16 rows an instruction took 164 us for the rows of
+// 16384 x 11008 alone, lines 138).
+//
+// Items of up to 16 tokens (decoding) have nothing to reuse F for: there each
+// wavefront takes 64 columns and reads F from memory.
 // ---------------------------------------------------------------------------
-template <int KS, bool RD, bool VEC>
-__global__ __launch_bounds__(256) void k_expand(ExpandArgs a) {
-  constexpr int LT = 32 * KS + 8;                  // LDS row of V, elements
-  constexpr int LF = 72;                           // staged row of F
-  extern __shared__ __attribute__((aligned(16))) uint8_t elds[];
-  uint16_t* th = reinterpret_cast<uint16_t*>(elds);
-  uint16_t* tl = th + 64 * LT;
-  if (!plan_fits(a.plan, a.M, a.slots)) return;
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r16 = lane & 15, g = lane >> 4;
-  uint16_t* stage = tl + 64 * LT + w * 32 * LF;
-  const int r = a.r;
-  const int64_t d = a.d;
-  const bool copy = a.in != a.out;                 // tokens without an adapter are written too
-  const int items = a.plan.head[copy || a.v_out ? kPlanAllTiles : kPlanTiles] * a.chunks;
+constexpr int kExpandCols = 256;
+constexpr int kTurn = 68;   // a row of 64 sums in the wavefront's LDS, FP32
 
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int t = item / a.chunks, c = item % a.chunks;
-    const int4 td = a.plan.tile[t];
-    const int slot = td.x, first = td.y, count = td.z;
-    const int nrb = (count + 15) / 16;
-    if (slot >= 0) {
-      __syncthreads();                             // the last item's V is no longer read
-      const float sc = a.scale[slot];
-      const float* part = a.part + (int64_t)first * r;
-      for (int e = threadIdx.x; e < 16 * nrb * 32 * KS; e += 256) {
-        const int row = e / (32 * KS), i = e % (32 * KS);
-        float v = 0.0f;
-        if (row < count && i < r) {
-          const float* p = part + row * r + i;
-          v = p[0];
-          for (int s = 1; s < a.splits; ++s) v += p[(int64_t)s * a.M * r];
-          v *= sc;
-          if (a.v_out && c == 0) a.v_out[(int64_t)a.plan.order[first + row] * r + i] = v;
-        }
-        float hi, lo;
-        split_bf16(v, hi, lo);
-        th[row * LT + i] = (uint16_t)(__float_as_uint(hi) >> 16);
-        tl[row * LT + i] = bf16_bits(lo);
-      }
-      __syncthreads();
-    } else if (a.v_out && c == 0) {
-      for (int e = threadIdx.x; e < count * r; e += 256)
-        a.v_out[(int64_t)a.plan.order[first + e / r] * r + e % r] = 0.0f;
+// The column that row j of MFMA block b (0..3) stands for in a unit of 64.
+__device__ __forceinline__ int unit_column(int j, int b) {
+  return 32 * (b >> 1) + 8 * (j >> 2) + 4 * (b & 1) + (j & 3);
+}
+
+// F's part in LDS: rows n of 32 KS + 8 ranks, or RD rows i of 264 columns; zero
+// past r and past d.
+template <int KS, bool RD>
+constexpr int expand_ld() { return RD ? kExpandCols + 8 : 32 * KS + 8; }
+template <int KS, bool RD>
+constexpr int expand_lds() { return (RD ? 32 * KS : kExpandCols) * expand_ld<KS, RD>() * 2; }
+constexpr int kTurnBytes = 4 * 16 * kTurn * 4;
+
+// Block b's operand of unit u, ranks 32 ks .. +32.
+template <int KS, bool RD>
+__device__ __forceinline__ u32x4 expand_f(const uint16_t* fl, int u, int b, int ks, int lane) {
+  constexpr int L = expand_ld<KS, RD>();
+  const int r16 = lane & 15, g = lane >> 4;
+  if (RD) {
+    const uint16_t* p = fl + (32 * ks + 8 * g + (r16 >> 2)) * L + 64 * u + unit_column(4 * (r16 & 3), b);
+    const uint2 lo = lds_tr(p), hi = lds_tr(p + 4 * L);
+    return u32x4{lo.x, lo.y, hi.x, hi.y};
+  }
+  return *reinterpret_cast<const u32x4*>(fl + (64 * u + unit_column(r16, b)) * L + 32 * ks + 8 * g);
+}
+
+// Eight results: y + s.
+__device__ __forceinline__ u32x4 expand_result(u32x4 y, const f32x4& s0, const f32x4& s1) {
+  u32x4 o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const f32x4& s = j < 2 ? s0 : s1;
+    o[j] = pack_bf16x2(bf16lo_to_f32(y[j]) + s[2 * (j & 1)], bf16hi_to_f32(y[j]) + s[2 * (j & 1) + 1]);
+  }
+  return o;
+}
+__device__ __forceinline__ void store8(uint16_t* row, int64_t col, int64_t end, u32x4 o) {
+  if (col + 8 <= end) {
+    store_vec(row + col, o);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (col + e < end) row[col + e] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
+  }
+}
+
+template <int KS, bool RD, bool R8, bool DEEP>
+__device__ __forceinline__ void expand_many(const ExpandArgs& a, int slot, int first, int tokens,
+                                            int64_t c0, uint8_t* lds) {
+  constexpr int L = expand_ld<KS, RD>();
+  uint16_t* fl = reinterpret_cast<uint16_t*>(lds + kTurnBytes);
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float* turn = reinterpret_cast<float*>(lds) + w * 16 * kTurn;
+  const int r16 = lane & 15, g = lane >> 4, l8 = lane >> 3, c8 = 8 * (lane & 7);
+  const int r = a.r, tiles = (tokens + 63) / 64;
+  const int64_t d = a.d;
+  const bool whole = c0 + kExpandCols <= d;
+  const uint16_t* F = a.F + (int64_t)slot * r * d;
+
+  // Of a tile's 16 tokens: as an operand's column lane r16's, of its rows in
+  // memory the lane's two, l8 and 8 + l8 (past the last token: that one again).
+  struct Rows {
+    u32x4 y[4][2], v[KS][2];
+    int64_t at[2];
+  };
+  auto place = [&](int j, int row) { return first + min(64 * j + 16 * w + row, tokens - 1); };
+  auto token = [&](int j, int (&tok)[2]) {
+    tok[0] = a.plan.order[place(j, l8)];
+    tok[1] = a.plan.order[place(j, 8 + l8)];
+  };
+  auto load = [&](int j, const int (&tok)[2], Rows& t) {
+    const uint16_t* v = a.vrows + (int64_t)place(j, r16) * 64 * KS + 8 * g;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      t.v[ks][0] = *reinterpret_cast<const u32x4*>(v + 32 * ks);
+      t.v[ks][1] = *reinterpret_cast<const u32x4*>(v + 32 * (KS + ks));
     }
-    if (slot < 0 && !copy) continue;
-    const uint16_t* F = a.F + (slot >= 0 ? (int64_t)slot * r * d : 0);
-    int64_t tok[4];
 #pragma unroll
-    for (int rb = 0; rb < 4; ++rb) tok[rb] = a.plan.order[first + min(16 * rb + r16, count - 1)];
-    const int64_t c_begin = (int64_t)c * a.cper;
-    const int64_t c_end = c_begin + a.cper < d ? c_begin + a.cper : d;
-    for (int64_t col0 = c_begin + 64 * w; col0 < c_end; col0 += 256) {
-      const int64_t col = col0 + 16 * g;           // the lane's 16 columns
-      u32x4 y[4][2];
+    for (int h = 0; h < 2; ++h) {
+      t.at[h] = tok[h] * d + c0 + c8;
+      if (!a.in) continue;
 #pragma unroll
-      for (int rb = 0; rb < 4; ++rb) {
-        y[rb][0] = y[rb][1] = u32x4{0, 0, 0, 0};
-        if (a.in && rb < nrb) {
-          y[rb][0] = load8<VEC>(a.in + tok[rb] * d, col, d);
-          y[rb][1] = load8<VEC>(a.in + tok[rb] * d, col + 8, d);
+      for (int u = 0; u < 4; ++u)
+        t.y[u][h] = whole ? load_vec(a.in + t.at[h] + 64 * u) : load8(a.in + tok[h] * d, c0 + 64 * u + c8, d);
+    }
+  };
+  auto work = [&](int j, Rows& t) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (c0 + 64 * u >= d) break;
+      f32x4 acc[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const u32x4 f = expand_f<KS, RD>(fl, u, b, ks, lane);
+          acc[b] = mfma16(f, t.v[ks][0], acc[b]);
+          acc[b] = mfma16(f, t.v[ks][1], acc[b]);
         }
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        *reinterpret_cast<f32x4*>(turn + r16 * kTurn + unit_column(4 * g, b)) = acc[b];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float* s = turn + (8 * h + l8) * kTurn + c8;
+        const u32x4 o = expand_result(a.in ? t.y[u][h] : u32x4{0, 0, 0, 0},
+                                      *reinterpret_cast<const f32x4*>(s),
+                                      *reinterpret_cast<const f32x4*>(s + 4));
+        if (64 * j + 16 * w + 8 * h + l8 >= tokens) continue;
+        if (whole) store_vec(a.out + t.at[h] + 64 * u, o);
+        else store8(a.out + t.at[h] - c0 - c8, c0 + 64 * u + c8, d, o);
       }
-      f32x4 acc[4][4];
-#pragma unroll
-      for (int rb = 0; rb < 4; ++rb)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) acc[rb][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (slot >= 0) {
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          u32x4 f[4];
-          if (RD) {
-            // rows i of F: 64 columns through LDS
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int i = 32 * ks + (lane >> 3) + 8 * u, cc = 8 * (lane & 7);
-              u32x4 v = {0, 0, 0, 0};
-              if (i < r) v = load8<VEC>(F + (int64_t)i * d, col0 + cc, d);
-              *reinterpret_cast<u32x4*>(stage + ((lane >> 3) + 8 * u) * LF + cc) = v;
-            }
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const uint16_t* p = stage + (8 * g + (r16 >> 2)) * LF + 16 * (r16 & 3) + 4 * b;
-              const uint2 lo = lds_tr(p), hi = lds_tr(p + 4 * LF);
-              f[b] = u32x4{lo.x, lo.y, hi.x, hi.y};
-            }
-          } else {
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const int64_t n = col0 + 16 * (r16 >> 2) + 4 * b + (r16 & 3);
-              f[b] = load8<VEC>(F + (n < d ? n : d - 1) * r, 32 * ks + 8 * g, r);
-            }
-          }
-#pragma unroll
-          for (int rb = 0; rb < 4; ++rb) {
-            if (rb < nrb) {
-              const int at = (16 * rb + r16) * LT + 32 * ks + 8 * g;
-              const u32x4 vh = *reinterpret_cast<const u32x4*>(th + at);
-              const u32x4 vl = *reinterpret_cast<const u32x4*>(tl + at);
-#pragma unroll
-              for (int b = 0; b < 4; ++b) {
-                acc[rb][b] = mfma16(f[b], vh, acc[rb][b]);
-                acc[rb][b] = mfma16(f[b], vl, acc[rb][b]);
-              }
-            }
-          }
-        }
+    }
+  };
+
+  Rows ta;
+  const bool mine = 16 * w < tokens;               // a first tile of few tokens leaves wavefronts out
+  int next[2];
+  if (mine) {
+    token(0, next);
+    load(0, next, ta);                             // in flight while F is staged
+    if (DEEP) token(1, next);
+  }
+  lds_barrier();                                   // the last item's F is no longer read
+  if (RD) {
+    constexpr int P = kExpandCols / 8;
+#pragma unroll 4
+    for (int e = threadIdx.x; e < 32 * KS * P; e += 256) {
+      const int i = e / P, cc = 8 * (e % P);
+      u32x4 v = {0, 0, 0, 0};
+      if (i < r) v = whole ? load_vec(F + (int64_t)i * d + c0 + cc) : load8(F + (int64_t)i * d, c0 + cc, d);
+      *reinterpret_cast<u32x4*>(fl + i * L + cc) = v;
+    }
+  } else {
+    constexpr int P = 4 * KS;
+#pragma unroll 4
+    for (int e = threadIdx.x; e < kExpandCols * P; e += 256) {
+      const int n = e / P, i = 8 * (e % P);
+      u32x4 v = {0, 0, 0, 0};
+      if (c0 + n < d && i < r) v = R8 ? load_vec(F + (c0 + n) * r + i) : load8(F + (c0 + n) * r, i, r);
+      *reinterpret_cast<u32x4*>(fl + n * L + i) = v;
+    }
+  }
+  lds_barrier();
+  if (!mine) return;
+  if constexpr (!DEEP) {
+    work(0, ta);
+  } else {
+    Rows tb;
+    for (int j = 0; j < tiles; j += 2) {
+      if (j + 1 < tiles) {
+        load(j + 1, next, tb);
+        token(j + 2, next);
       }
-#pragma unroll
-      for (int rb = 0; rb < 4; ++rb) {
-        if (16 * rb + r16 >= count) continue;
-        uint16_t* out = a.out + tok[rb] * d;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          u32x4 o;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int b = 2 * h + j / 2, v = 2 * (j & 1);
-            o[j] = pack_bf16x2(bf16lo_to_f32(y[rb][h][j]) + acc[rb][b][v],
-                               bf16hi_to_f32(y[rb][h][j]) + acc[rb][b][v + 1]);
-          }
-          const int64_t n = col + 8 * h;
-          if (VEC) {
-            if (n < d) *reinterpret_cast<u32x4*>(out + n) = o;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (n + e < d) out[n + e] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
-          }
-        }
+      work(j, ta);
+      if (j + 1 >= tiles) break;
+      if (j + 2 < tiles) {
+        load(j + 2, next, ta);
+        token(j + 3, next);
       }
+      work(j + 1, tb);
     }
   }
 }
 
+// Up to 16 tokens: wavefront w takes columns 64 w .. of the item's.
+template <int KS, bool RD, bool R8>
+__device__ __forceinline__ void expand_few(const ExpandArgs& a, int slot, int first, int tokens,
+                                           int64_t c0, uint8_t* lds) {
+  constexpr int LF = 72;                           // staged row of F
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, g = lane >> 4;
+  const int r = a.r;
+  const int64_t d = a.d, col0 = c0 + 64 * w;
+  if (RD) lds_barrier();                           // another item's F is no longer read
+  if (col0 >= d) return;
+  const bool whole = col0 + 64 <= d;
+  uint16_t* stage = reinterpret_cast<uint16_t*>(lds) + w * 32 * LF;
+  const uint16_t* F = a.F + (int64_t)slot * r * d;
+  f32x4 acc[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  u32x4 f[KS][4];
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (RD) {
+        const int i = 32 * ks + (lane >> 3) + 8 * u;
+        const int64_t col = col0 + 8 * (lane & 7);
+        const uint16_t* row = F + (int64_t)(i < r ? i : 0) * d;
+        f[ks][u] = only_if(i < r, whole ? load_vec(row + col) : load8(row, col, d));
+      } else {
+        const int64_t n = col0 + unit_column(r16, u);
+        const uint16_t* row = F + (n < d ? n : 0) * r;
+        const int i = 32 * ks + 8 * g;
+        if (R8) f[ks][u] = only_if(n < d && i < r, load_vec(row + (i < r ? i : 0)));
+        else f[ks][u] = only_if(n < d, load8(row, i, r));
+      }
+    }
+  const int pos = first + min(r16, tokens - 1);
+  const int64_t tok = a.plan.order[pos];
+  const uint16_t* v = a.vrows + (int64_t)pos * 64 * KS + 8 * g;
+  u32x4 y[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t col = col0 + 32 * h + 8 * g;
+    y[h] = u32x4{0, 0, 0, 0};
+    if (a.in) y[h] = whole ? load_vec(a.in + tok * d + col) : load8(a.in + tok * d, col, d);
+  }
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) {
+    const u32x4 vh = *reinterpret_cast<const u32x4*>(v + 32 * ks);
+    const u32x4 vl = *reinterpret_cast<const u32x4*>(v + 32 * (KS + ks));
+    if (RD) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        *reinterpret_cast<u32x4*>(stage + ((lane >> 3) + 8 * u) * LF + 8 * (lane & 7)) = f[ks][u];
+    }
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      u32x4 q = f[ks][b];
+      if (RD) {
+        const uint16_t* p = stage + (8 * g + (r16 >> 2)) * LF + unit_column(4 * (r16 & 3), b);
+        const uint2 lo = lds_tr(p), hi = lds_tr(p + 4 * LF);
+        q = u32x4{lo.x, lo.y, hi.x, hi.y};
+      }
+      acc[b] = mfma16(q, vh, acc[b]);
+      acc[b] = mfma16(q, vl, acc[b]);
+    }
+  }
+  if (r16 >= tokens) return;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) 
+    store8(a.out + tok * d, col0 + 32 * h + 8 * g, d, expand_result(y[h], acc[2 * h], acc[2 * h + 1]));
+}
+
+// Tokens without an adapter: their rows' columns copied, T zero.
+__device__ __forceinline__ void expand_none(const ExpandArgs& a, const int4& td, int64_t c0) {
+  const int64_t n = min((int64_t)kExpandCols, a.d - c0);
+  const int vecs = (int)((n + 7) / 8);
+  if (a.in != a.out) {
+    for (int e = threadIdx.x; e < td.z * vecs; e += 256) {
+      const int64_t at = (int64_t)a.plan.order[td.y + e / vecs] * a.d + c0;
+      const int64_t col = 8 * (int64_t)(e % vecs);
+      store8(a.out + at, col, n, a.in ? load8(a.in + at, col, n) : u32x4{0, 0, 0, 0});
+    }
+  }
+  if (a.v_out && c0 == 0)
+    for (int e = threadIdx.x; e < td.z * a.r; e += 256)
+      a.v_out[(int64_t)a.plan.order[td.y + e / a.r] * a.r + e % a.r] = 0.0f;
+}
+
+// DEEP: items of several tiles, from the list of splits; else single tiles.
+template <int KS, bool RD, bool R8, bool DEEP>
+__global__ __launch_bounds__(256, KS > 4 ? 1 : (DEEP || KS > 2 ? 2 : EXPAND_OCC)) void k_expand(ExpandArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t elds[];
+  // the grid has no more workgroups than the lists room for items
+  const int g0 = min((int)blockIdx.x / a.chunks / a.subs, a.most - 1);
+  int4 rec = DEEP ? a.plan.split[g0] : a.plan.tile[g0];
+  int first = DEEP ? a.plan.split_first[g0] : rec.y;
+  if (!plan_fits(a.plan, a.M, a.slots)) return;
+  const int tiles = a.plan.head[kPlanTiles];
+  const int with_one = (DEEP ? a.plan.head[kPlanSplits] * a.subs : tiles) * a.chunks;
+  // tokens without an adapter only where something is written for them
+  const int none = a.in != a.out || a.v_out ? (a.plan.head[kPlanAllTiles] - tiles) * a.chunks : 0;
+  for (int item = blockIdx.x; item < with_one + none; item += gridDim.x) {
+    if (item >= with_one) {
+      expand_none(a, a.plan.tile[tiles + (item - with_one) / a.chunks],
+                  (int64_t)((item - with_one) % a.chunks) * kExpandCols);
+      continue;
+    }
+    const int64_t c0 = (int64_t)(item % a.chunks) * kExpandCols;
+    const int group = item / a.chunks;
+    if (item != (int)blockIdx.x) {
+      rec = DEEP ? a.plan.split[group / a.subs] : a.plan.tile[group];
+      first = DEEP ? a.plan.split_first[group / a.subs] : rec.y;
+    }
+    const int skip = DEEP ? group % a.subs * a.tpi * 64 : 0;
+    const int tokens = DEEP ? min(rec.z - skip, a.tpi * 64) : rec.z;
+    if (tokens <= 0) continue;
+    if (tokens <= 16) expand_few<KS, RD, R8>(a, rec.x, first + skip, tokens, c0, elds);
+    else expand_many<KS, RD, R8, DEEP>(a, rec.x, first + skip, tokens, c0, elds);
+  }
+}
+
 // ---------------------------------------------------------------------------
-// T and U as row operands of the contractions over tokens: per tile, BF16 term
-// (hi, mid, lo: 24 bits together), 16 ranks and 32 tokens one KB in the order
-// of an MFMA's lanes; zero past the tile's tokens and past the rank.  U comes
-// from k_shrink's partial sums by position (or a whole U by token), T by token.
+// What k_shrink's partial sums become: V = scale_a * (their sum, in order) as
+// k_expand's rows (vrows), by token (v_out), and as a row operand of the
+// contractions over tokens (u_frags); the caller's T as such an operand
+// (t_frags).  Without partial sums (splits 0) V is given by token.
+//
+// Row operands: per tile, BF16 term (hi, mid, lo: 24 bits together), 16 ranks
+// and 32 tokens one KB in the order of an MFMA's lanes; zero past the tile's
+// tokens and past the rank.
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void k_frags(FragArgs a) {
+__global__ __launch_bounds__(256) void k_finish(FinishVArgs a) {
   constexpr int L = 72;
   __shared__ __attribute__((aligned(16))) uint16_t st[3][64 * L];
   if (a.plan.head && !plan_fits(a.plan, a.M, a.slots)) return;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  const int r = a.r, nb = a.nb, groups = (nb + 3) / 4;
+  const int r = a.r, nb = a.nb, groups = (nb + 3) / 4, sides = a.t_frags ? 2 : 1;
+  const int rp = (r + 31) / 32 * 32;
+  const int rp_v = rp <= 64 ? rp : (rp <= 128 ? 128 : 256);   // k_expand's width
   const int tiles = a.plan.head ? a.plan.head[kPlanTiles] : (int)((a.M + 63) / 64);
-  for (int item = blockIdx.x; item < tiles * groups * 2; item += gridDim.x) {
-    const int src = item & 1, grp = (item >> 1) % groups, t = (item >> 1) / groups;
+  for (int item = blockIdx.x; item < tiles * groups * sides; item += gridDim.x) {
+    const bool is_t = item % sides == 1;
+    const int grp = item / sides % groups, t = item / sides / groups;
     int4 td = {0, 64 * t, (int)min((int64_t)64, a.M - 64 * (int64_t)t), 0};
     if (a.plan.head) td = a.plan.tile[t];
     const int first = td.y, count = td.z, i0 = 64 * grp;
-    const bool by_part = src == 1 && a.splits > 0;
+    const bool by_part = !is_t && a.splits > 0;
     const float sc = by_part ? a.scale[td.x] : 1.0f;
-    const float* v_in = src == 0 ? a.T : a.U;
-    __syncthreads();
-    for (int e = threadIdx.x; e < 64 * 64; e += 256) {
-      const int row = e >> 6, i = i0 + (e & 63);
-      float v = 0.0f;
-      if (row < count && i < r) {
+    const float* v_in = is_t ? a.T : a.V;
+    uint16_t* frags = is_t ? a.t_frags : a.u_frags;
+    const int64_t stride = a.M * r;
+    const int cols = min(64, max(16 * nb, a.vrows && !is_t ? rp_v : 0) - i0);
+    const int rows = frags ? 64 : (count + 15) / 16 * 16;
+    lds_barrier();
+    auto fill = [&](auto ranks) {
+      constexpr int N = decltype(ranks)::value, Q = 4, PR = 64 / N;
+#pragma unroll 1
+      for (int e0 = threadIdx.x; e0 < rows * PR; e0 += 256 * Q) {
+        float v[Q][N];
+        bool on[Q];
+        int at[Q];
+        int64_t tok[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const int e = e0 + 256 * q, row = e / PR, i = i0 + N * (e % PR);
+          on[q] = row < count && i < r;
+          at[q] = on[q] ? row * r + i : 0;
+          tok[q] = 0;
+          if (on[q] && (!by_part || a.v_out)) tok[q] = a.plan.head ? a.plan.order[first + row] : first + row;
+        }
         if (by_part) {
-          const float* p = a.U + (int64_t)(first + row) * r + i;
-          v = p[0];
-          for (int s = 1; s < a.splits; ++s) v += p[(int64_t)s * a.M * r];
-          v *= sc;
+          sum_parts<Q, N>(v_in + (int64_t)first * r, at, on, a.splits, stride, v);
         } else {
-          const int64_t tok = a.plan.head ? a.plan.order[first + row] : first + row;
-          v = v_in[tok * r + i];
+#pragma unroll
+          for (int q = 0; q < Q; ++q)
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+              v[q][j] = on[q] ? v_in[tok[q] * r + i0 + N * ((e0 + 256 * q) % PR) + j] : 0.0f;
+        }
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const int e = e0 + 256 * q, row = e / PR, i = N * (e % PR);
+          if (row >= rows || i >= cols) continue;
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const float x = on[q] ? v[q][j] * sc : 0.0f;
+            if (!is_t && on[q] && a.v_out) a.v_out[tok[q] * r + i0 + i + j] = x;
+            float hi, rest, mid, lo;
+            split_bf16(x, hi, rest);
+            split_bf16(rest, mid, lo);
+            st[0][row * L + i + j] = (uint16_t)(__float_as_uint(hi) >> 16);
+            st[1][row * L + i + j] = (uint16_t)(__float_as_uint(mid) >> 16);
+            st[2][row * L + i + j] = bf16_bits(lo);
+          }
         }
       }
-      float hi, rest;
-      split_bf16(v, hi, rest);
-      float mid, lo;
-      split_bf16(rest, mid, lo);
-      const int at = row * L + (e & 63);
-      st[0][at] = (uint16_t)(__float_as_uint(hi) >> 16);
-      st[1][at] = (uint16_t)(__float_as_uint(mid) >> 16);
-      st[2][at] = bf16_bits(lo);
+    };
+    if (r % 4 == 0) fill(std::integral_constant<int, 4>{});
+    else fill(std::integral_constant<int, 1>{});
+    lds_barrier();
+    if (frags) {
+      for (int u = w; u < 24; u += 4) {            // (term, 16 ranks, 32 tokens)
+        const int term = u >> 3, b = (u >> 1) & 3, slice = u & 1;
+        if (4 * grp + b >= nb) continue;
+        const uint16_t* p = &st[term][(32 * slice + 8 * g + (r16 >> 2)) * L + 16 * b + 4 * (r16 & 3)];
+        const uint2 lo = lds_tr(p), hi = lds_tr(p + 4 * L);
+        const int64_t at = (((int64_t)t * 3 + term) * nb + 4 * grp + b) * 2 + slice;
+        *reinterpret_cast<u32x4*>(frags + at * 512 + lane * 8) = u32x4{lo.x, lo.y, hi.x, hi.y};
+      }
     }
-    __syncthreads();
-    uint16_t* out = src == 0 ? a.t_frags : a.u_frags;
-    for (int u = w; u < 24; u += 4) {              // (term, 16 ranks, 32 tokens)
-      const int term = u >> 3, b = (u >> 1) & 3, slice = u & 1;
-      if (4 * grp + b >= nb) continue;
-      const uint16_t* p = &st[term][(32 * slice + 8 * g + (r16 >> 2)) * L + 16 * b + 4 * (r16 & 3)];
-      const uint2 lo = lds_tr(p), hi = lds_tr(p + 4 * L);
-      const int64_t at = (((int64_t)t * 3 + term) * nb + 4 * grp + b) * 2 + slice;
-      *reinterpret_cast<u32x4*>(out + at * 512 + lane * 8) = u32x4{lo.x, lo.y, hi.x, hi.y};
+    if (!is_t && a.vrows) {
+      // the lo of a pair is what the mid of three is
+      const int pieces = min(64, rp_v - i0) / 8;
+      for (int e = threadIdx.x; e < count * 2 * pieces; e += 256) {
+        const int row = e / (2 * pieces), h = e / pieces & 1, i = 8 * (e % pieces);
+        *reinterpret_cast<u32x4*>(a.vrows + (int64_t)(first + row) * 2 * rp_v + h * rp_v + i0 + i) =
+            *reinterpret_cast<const u32x4*>(&st[h][row * L + i]);
+      }
     }
   }
 }
@@ -637,33 +990,46 @@ struct GramTile {
 };
 
 // tok: the lane's token of the tile (lane = row), -1 past its last.
-template <bool PACKED, bool VEC>
+template <bool PACKED>
 __device__ __forceinline__ void gram_load(const GramSide& q, int64_t M, int64_t c0, int tok,
                                           int lane, GramTile& t) {
   if constexpr (PACKED) {
     const int64_t ldc = (q.d + 63) / 64 * 64;
+    const uint8_t* codes = q.codes + c0 + 16 * (lane & 3);
     const float* sc = q.scale + c0 / 64 * M;
+    int m[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int m = __shfl(tok, 16 * j + (lane >> 2));
-      t.v[j] = u32x4{0, 0, 0, 0};
-      t.s[j] = 0.0f;
+      m[j] = __shfl(tok, 16 * j + (lane >> 2));
+      const int64_t row = max(m[j], 0);
+      t.v[j] = *reinterpret_cast<const u32x4*>(codes + row * ldc);
+      t.s[j] = sc[row];
       t.keep[j] = 0xFFFFu;
-      if (m >= 0) {
-        t.v[j] = *reinterpret_cast<const u32x4*>(q.codes + m * ldc + c0 + 16 * (lane & 3));
-        t.s[j] = sc[m];
-        if (q.keep) {
-          const int64_t col = c0 + 16 * (lane & 3);
-          t.keep[j] = q.keep[m * (q.d / 32) + col / 32] >> (col & 16);
-        }
+      if (q.keep) {
+        const int64_t col = c0 + 16 * (lane & 3);
+        t.keep[j] = q.keep[row * (q.d / 32) + col / 32] >> (col & 16);
       }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t.keep[j] = m[j] >= 0 ? t.keep[j] : 0u;
+  } else if (c0 + 64 <= q.d) {
+    const uint16_t* x = q.x + c0 + 8 * (lane & 7);
+    int m[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      m[j] = __shfl(tok, 8 * j + (lane >> 3));
+      t.v[j] = load_vec(x + max(m[j], 0) * q.d);
+    }
+    if (__shfl(tok, 63) < 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t.v[j] = only_if(m[j] >= 0, t.v[j]);
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int m = __shfl(tok, 8 * j + (lane >> 3));
       t.v[j] = u32x4{0, 0, 0, 0};
-      if (m >= 0) t.v[j] = load8<VEC>(q.x + m * q.d, c0 + 8 * (lane & 7), q.d);
+      if (m >= 0) t.v[j] = load8(q.x + m * q.d, c0 + 8 * (lane & 7), q.d);
     }
   }
 }
@@ -692,50 +1058,73 @@ __device__ __forceinline__ void gram_stage(const GramTile& t, int lane, uint16_t
   }
 }
 
-template <int NB, bool PACKED, bool VEC>
+// sp: {slot, first tile, tokens, }, `first` the split's first position.
+template <int NB, bool PACKED>
 __device__ __forceinline__ void gram_item(const GramArgs8& a, const GramSide& q, int64_t c0,
-                                          const int4& sp, uint16_t* st, f32x4 (&acc)[NB][4]) {
+                                          const int4& sp, int first, uint16_t* st,
+                                          f32x4 (&acc)[NB][4]) {
+  constexpr int CN = NB < 4 ? NB : 4, NC = NB / CN, C = 2 * NC;   // operand chunks of a tile
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  const int t_end = sp.y + sp.z;
-  auto token = [&](int t) {
-    if (!a.plan.head) {
-      const int64_t m = 64 * (int64_t)t + lane;
-      return m < a.M ? (int)m : -1;
-    }
-    const int4 td = a.plan.tile[t];
-    return lane < td.z ? a.plan.order[td.y + lane] : -1;
+  const int tiles = (sp.z + 63) / 64;
+  auto token = [&](int j) {
+    const int at = 64 * j + lane;
+    if (at >= sp.z) return -1;
+    return a.plan.head ? a.plan.order[first + at] : first + at;
   };
+  // chunk c: CN blocks of 16 ranks, three terms, of 32 tokens
+  auto load_v = [&](const uint16_t* fr, int c, u32x4 (&v)[CN][3]) {
+#pragma unroll
+    for (int n = 0; n < CN; ++n)
+#pragma unroll
+      for (int term = 0; term < 3; ++term)
+        v[n][term] = *reinterpret_cast<const u32x4*>(
+            fr + ((term * NB + (c % NC) * CN + n) * 2 + c / NC) * 512);
+  };
+  if (w >= tiles) return;
+  int next = token(w);
   GramTile cur;
-  int t = sp.y + w;
-  if (t < t_end) gram_load<PACKED, VEC>(q, a.M, c0, token(t), lane, cur);
-  for (; t < t_end; t += 4) {
+  gram_load<PACKED>(q, a.M, c0, next, lane, cur);
+  next = token(w + 4);
+  for (int j = w; j < tiles; j += 4) {
+    // in the order of their use: this tile's operands, the next tile's rows
+    const uint16_t* fr = q.frags + (int64_t)(sp.y + j) * 3 * NB * 2 * 512 + lane * 8;
+    u32x4 v[2][CN][3], b[4];
+    load_v(fr, 0, v[0]);
     gram_stage<PACKED>(cur, lane, st);
-    if (t + 4 < t_end) gram_load<PACKED, VEC>(q, a.M, c0, token(t + 4), lane, cur);
-    const uint16_t* fr = q.frags + (int64_t)t * 3 * NB * 2 * 512 + lane * 8;
 #pragma unroll
-    for (int slice = 0; slice < 2; ++slice) {
-      u32x4 b[4];
+    for (int c = 0; c < C; ++c) {
+      if (c + 1 < C) {
+        load_v(fr, c + 1, v[(c + 1) & 1]);
+      }
+      if (c + 2 == C && j + 4 < tiles) {
+        gram_load<PACKED>(q, a.M, c0, next, lane, cur);
+        next = token(j + 8);
+      }
+      if (c % NC == 0) {
+        const int slice = c / NC;
 #pragma unroll
-      for (int cb = 0; cb < 4; ++cb) {
-        const uint16_t* p = st + (32 * slice + 8 * g + (r16 >> 2)) * kGL + 16 * cb + 4 * (r16 & 3);
-        const uint2 lo = lds_tr(p), hi = lds_tr(p + 4 * kGL);
-        b[cb] = u32x4{lo.x, lo.y, hi.x, hi.y};
+        for (int cb = 0; cb < 4; ++cb) {
+          const uint16_t* p = st + (32 * slice + 8 * g + (r16 >> 2)) * kGL + 16 * cb + 4 * (r16 & 3);
+          const uint2 lo = lds_tr(p), hi = lds_tr(p + 4 * kGL);
+          b[cb] = u32x4{lo.x, lo.y, hi.x, hi.y};
+        }
       }
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int n = 0; n < CN; ++n)
 #pragma unroll
-        for (int term = 0; term < 3; ++term) {
-          const u32x4 v = *reinterpret_cast<const u32x4*>(fr + ((term * NB + nb) * 2 + slice) * 512);
+        for (int term = 0; term < 3; ++term)
 #pragma unroll
-          for (int cb = 0; cb < 4; ++cb) acc[nb][cb] = mfma16(v, b[cb], acc[nb][cb]);
-        }
+          for (int cb = 0; cb < 4; ++cb) {
+            f32x4& s = acc[(c % NC) * CN + n][cb];
+            s = mfma16(v[c & 1][n][term], b[cb], s);
+          }
     }
   }
 }
 
-template <int NB, bool PACKED, bool VEC>
-__global__ __launch_bounds__(256) void k_gram8(GramArgs8 a) {
+template <int NB, bool PACKED>
+__global__ __launch_bounds__(256, NB <= 4 ? 2 : 1) void k_gram8(GramArgs8 a) {
   constexpr int LR = 68;                            // a reduced row, FP32
   __shared__ __attribute__((aligned(16))) uint8_t glds[4 * 64 * kGL * 2];
   static_assert(4 * 16 * LR * 4 <= 4 * 64 * kGL * 2, "reduction buffer");
@@ -755,12 +1144,15 @@ __global__ __launch_bounds__(256) void k_gram8(GramArgs8 a) {
     if (side) ct -= ct0;
     const GramSide& q = a.q[side];
     int4 sp;
+    int first;
     int64_t part = -1;
     if (a.plan.head) {
       sp = a.plan.split[si];
+      first = a.plan.split_first[si];
       if (sp.w >= 0) part = a.plan.parts[sp.x].x + sp.w;
     } else {
-      sp = int4{0, si * a.tps, min(a.tps, tiles - si * a.tps), 0};
+      first = 64 * si * a.tps;
+      sp = int4{0, si * a.tps, (int)min((int64_t)64 * a.tps, a.M - first), 0};
       if (splits > 1) part = si;
     }
     const int64_t c0 = (int64_t)ct * 64;
@@ -769,8 +1161,8 @@ __global__ __launch_bounds__(256) void k_gram8(GramArgs8 a) {
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int cb = 0; cb < 4; ++cb) acc[nb][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (PACKED && side == 0) gram_item<NB, true, VEC>(a, q, c0, sp, st, acc);
-    else gram_item<NB, false, VEC>(a, q, c0, sp, st, acc);
+    if (PACKED && side == 0) gram_item<NB, true>(a, q, c0, sp, first, st, acc);
+    else gram_item<NB, false>(a, q, c0, sp, first, st, acc);
 
     // accumulator lane (r16, g): ranks 16 nb + 4 g + v, column c0 + 16 cb + r16
     float* out = part >= 0 ? q.part + part * a.r * q.d : q.out + (int64_t)sp.x * a.r * q.d;
@@ -833,56 +1225,50 @@ hipError_t allow_lds(K kernel, int bytes) {
                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <int NB, bool KN, bool VEC>
+template <int NB, bool KN, bool R8>
 hipError_t launch_shrink_t(const ShrinkArgs& a, unsigned grid, hipStream_t st) {
   constexpr int lds = shrink_lds<NB, KN>();
-  static const hipError_t attr = allow_lds(&k_shrink<NB, KN, VEC>, lds);
+  static const hipError_t attr = allow_lds(&k_shrink<NB, KN, R8>, lds);
   if (attr != hipSuccess) return attr;
-  hipLaunchKernelGGL((k_shrink<NB, KN, VEC>), dim3(grid), dim3(64 * shrink_waves<NB>()), lds, st,
+  hipLaunchKernelGGL((k_shrink<NB, KN, R8>), dim3(grid), dim3(64 * shrink_waves<NB>()), lds, st,
                      a);
   return hipGetLastError();
 }
 template <int NB>
-hipError_t launch_shrink_nb(const ShrinkArgs& a, bool vec, unsigned grid, hipStream_t st) {
-  if (a.kn)
-    return vec ? launch_shrink_t<NB, true, true>(a, grid, st)
-               : launch_shrink_t<NB, true, false>(a, grid, st);
-  return vec ? launch_shrink_t<NB, false, true>(a, grid, st)
-             : launch_shrink_t<NB, false, false>(a, grid, st);
+hipError_t launch_shrink_nb(const ShrinkArgs& a, unsigned grid, hipStream_t st) {
+  if (!a.kn) return launch_shrink_t<NB, false, true>(a, grid, st);
+  return a.r % 8 == 0 ? launch_shrink_t<NB, true, true>(a, grid, st)
+                      : launch_shrink_t<NB, true, false>(a, grid, st);
 }
 
-template <int KS, bool RD, bool VEC>
+template <int KS, bool RD, bool R8, bool DEEP>
 hipError_t launch_expand_t(const ExpandArgs& a, unsigned grid, hipStream_t st) {
-  constexpr int lds = 2 * 64 * (32 * KS + 8) * 2 + (RD ? 4 * 32 * 72 * 2 : 0);
-  static const hipError_t attr = allow_lds(&k_expand<KS, RD, VEC>, lds);
+  constexpr int few = RD ? 4 * 32 * 72 * 2 : 0, many = kTurnBytes + expand_lds<KS, RD>();
+  constexpr int lds = many > few ? many : few;
+  static const hipError_t attr = allow_lds(&k_expand<KS, RD, R8, DEEP>, lds);
   if (attr != hipSuccess) return attr;
-  hipLaunchKernelGGL((k_expand<KS, RD, VEC>), dim3(grid), dim3(256), lds, st, a);
+  hipLaunchKernelGGL((k_expand<KS, RD, R8, DEEP>), dim3(grid), dim3(256), lds, st, a);
   return hipGetLastError();
 }
+template <int KS, bool RD, bool R8>
+hipError_t launch_expand_deep(const ExpandArgs& a, unsigned grid, hipStream_t st) {
+  return a.tpi > 1 ? launch_expand_t<KS, RD, R8, true>(a, grid, st)
+                   : launch_expand_t<KS, RD, R8, false>(a, grid, st);
+}
 template <int KS>
-hipError_t launch_expand_ks(const ExpandArgs& a, bool vec, unsigned grid, hipStream_t st) {
-  if (a.rd)
-    return vec ? launch_expand_t<KS, true, true>(a, grid, st)
-               : launch_expand_t<KS, true, false>(a, grid, st);
-  return vec ? launch_expand_t<KS, false, true>(a, grid, st)
-             : launch_expand_t<KS, false, false>(a, grid, st);
+hipError_t launch_expand_ks(const ExpandArgs& a, unsigned grid, hipStream_t st) {
+  if (a.rd) return launch_expand_deep<KS, true, true>(a, grid, st);
+  return a.r % 8 == 0 ? launch_expand_deep<KS, false, true>(a, grid, st)
+                      : launch_expand_deep<KS, false, false>(a, grid, st);
 }
 
 template <int NB>
-hipError_t launch_gram8_nb(const GramArgs8& a, bool vec, unsigned grid, hipStream_t st) {
-  const bool packed = a.q[0].codes != nullptr;
-  if (packed && vec)
-    hipLaunchKernelGGL((k_gram8<NB, true, true>), dim3(grid), dim3(256), 0, st, a);
-  else if (packed)
-    hipLaunchKernelGGL((k_gram8<NB, true, false>), dim3(grid), dim3(256), 0, st, a);
-  else if (vec)
-    hipLaunchKernelGGL((k_gram8<NB, false, true>), dim3(grid), dim3(256), 0, st, a);
-  else
-    hipLaunchKernelGGL((k_gram8<NB, false, false>), dim3(grid), dim3(256), 0, st, a);
+hipError_t launch_gram8_nb(const GramArgs8& a, unsigned grid, hipStream_t st) {
+  if (a.q[0].codes) hipLaunchKernelGGL((k_gram8<NB, true>), dim3(grid), dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((k_gram8<NB, false>), dim3(grid), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
-bool at16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 constexpr int64_t kMostGrid = 4096;
 
 }  // namespace
@@ -920,56 +1306,56 @@ hipError_t launch_plan(const PlanView& p, const int32_t* index, int64_t M, int64
 hipError_t launch_shrink(const ShrinkArgs& a0, hipStream_t st) {
   ShrinkArgs a = a0;
   a.splits = shrink_splits(a.M, a.K, &a.kper);
+  if (a.splits > 1) a.vrows = nullptr;             // k_finish forms V
   const unsigned grid =
       (unsigned)std::min<int64_t>(plan_most_tiles(a.M, a.slots) * a.splits, kMostGrid);
-  // whole 16-byte pieces: of the tokens' rows, and of the factor's
-  const bool vec = a.K % 8 == 0 && at16(a.P) && at16(a.F) && (!a.kn || a.r % 8 == 0);
-  if (a.r <= 16) return launch_shrink_nb<1>(a, vec, grid, st);
-  if (a.r <= 32) return launch_shrink_nb<2>(a, vec, grid, st);
-  if (a.r <= 64) return launch_shrink_nb<4>(a, vec, grid, st);
-  if (a.r <= 128) return launch_shrink_nb<8>(a, vec, grid, st);
-  return launch_shrink_nb<16>(a, vec, grid, st);
+  if (a.r <= 16) return launch_shrink_nb<1>(a, grid, st);
+  if (a.r <= 32) return launch_shrink_nb<2>(a, grid, st);
+  if (a.r <= 64) return launch_shrink_nb<4>(a, grid, st);
+  if (a.r <= 128) return launch_shrink_nb<8>(a, grid, st);
+  return launch_shrink_nb<16>(a, grid, st);
 }
 
 hipError_t launch_expand(const ExpandArgs& a0, hipStream_t st) {
   ExpandArgs a = a0;
-  int64_t kper;
-  a.splits = shrink_splits(a.M, a.K, &kper);
-  // chunks of whole 256 columns, about 1024 workgroups
-  const int64_t tiles = (a.M + 63) / 64, units = (a.d + 255) / 256;
-  const int64_t want = std::max<int64_t>(1, std::min(units, (1024 + tiles - 1) / tiles));
-  a.cper = (units + want - 1) / want * 256;
-  a.chunks = (int)((a.d + a.cper - 1) / a.cper);
-  const unsigned grid =
-      (unsigned)std::min<int64_t>(plan_most_tiles(a.M, a.slots) * a.chunks, kMostGrid);
-  const bool vec = a.d % 8 == 0 && at16(a.in) && at16(a.out) && at16(a.F) && (a.rd || a.r % 8 == 0);
-  if (a.r <= 32) return launch_expand_ks<1>(a, vec, grid, st);
-  if (a.r <= 64) return launch_expand_ks<2>(a, vec, grid, st);
-  if (a.r <= 128) return launch_expand_ks<4>(a, vec, grid, st);
-  return launch_expand_ks<8>(a, vec, grid, st);
+  a.chunks = (int)((a.d + kExpandCols - 1) / kExpandCols);
+  // more tiles an item where there are enough items
+  const int64_t tiles = (a.M + kPlanTile - 1) / kPlanTile;
+  a.tpi = (int)std::max<int64_t>(1, std::min<int64_t>(8, tiles * a.chunks / EXPAND_WGS));
+  const bool deep = a.tpi > 1;
+  a.subs = deep ? (plan_split_tiles(a.M) + a.tpi - 1) / a.tpi : 1;
+  a.most = (int)(deep ? plan_most_splits(a.M, a.slots) : plan_most_tiles(a.M, a.slots));
+  const int64_t most = (int64_t)a.most * a.subs + (deep ? (a.M + 63) / 64 : 0);
+  const unsigned grid = (unsigned)std::min<int64_t>(most * a.chunks, kMostGrid);
+  if (a.r <= 32) return launch_expand_ks<1>(a, grid, st);
+  if (a.r <= 64) return launch_expand_ks<2>(a, grid, st);
+  if (a.r <= 128) return launch_expand_ks<4>(a, grid, st);
+  return launch_expand_ks<8>(a, grid, st);
 }
 
-hipError_t launch_gram8(const FragArgs& f0, const GramArgs8& a, hipStream_t st) {
-  const int64_t tiles = a.plan.head ? plan_most_tiles(a.M, a.slots) : (a.M + 63) / 64;
-  FragArgs f = f0;
-  f.nb = frag_blocks(a.r);
-  const int groups = (f.nb + 3) / 4;
-  hipLaunchKernelGGL(k_frags, dim3((unsigned)std::min<int64_t>(tiles * groups * 2, kMostGrid)),
-                     dim3(256), 0, st, f);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+hipError_t launch_finish_v(const FinishVArgs& f0, hipStream_t st) {
+  FinishVArgs f = f0;
+  f.nb = frag_blocks(f.r);
+  const int64_t tiles = f.plan.head ? plan_most_tiles(f.M, f.slots) : (f.M + 63) / 64;
+  const int64_t items = tiles * ((f.nb + 3) / 4) * (f.t_frags ? 2 : 1);
+  hipLaunchKernelGGL(k_finish, dim3((unsigned)std::min<int64_t>(items, kMostGrid)), dim3(256), 0, st,
+                     f);
+  return hipGetLastError();
+}
+
+hipError_t launch_gram8(const GramArgs8& a, hipStream_t st) {
+  const int64_t tiles = (a.M + 63) / 64;
+  hipError_t e = hipSuccess;
   const int64_t splits =
       a.plan.head ? plan_most_splits(a.M, a.slots) : (tiles + a.tps - 1) / a.tps;
   const int64_t cols = (a.q[0].d + 63) / 64 + (a.q[1].d + 63) / 64;
   const unsigned grid = (unsigned)std::min<int64_t>(splits * cols, 2 * kMostGrid);
-  const bool vec = a.q[1].d % 8 == 0 && at16(a.q[1].x) &&
-                   (a.q[0].codes || (a.q[0].d % 8 == 0 && at16(a.q[0].x)));
-  switch (f.nb) {
-    case 1: e = launch_gram8_nb<1>(a, vec, grid, st); break;
-    case 2: e = launch_gram8_nb<2>(a, vec, grid, st); break;
-    case 4: e = launch_gram8_nb<4>(a, vec, grid, st); break;
-    case 8: e = launch_gram8_nb<8>(a, vec, grid, st); break;
-    default: e = launch_gram8_nb<16>(a, vec, grid, st);
+  switch (frag_blocks(a.r)) {
+    case 1: e = launch_gram8_nb<1>(a, grid, st); break;
+    case 2: e = launch_gram8_nb<2>(a, grid, st); break;
+    case 4: e = launch_gram8_nb<4>(a, grid, st); break;
+    case 8: e = launch_gram8_nb<8>(a, grid, st); break;
+    default: e = launch_gram8_nb<16>(a, grid, st);
   }
   if (e != hipSuccess) return e;
   // without a plan one split leaves nothing to add

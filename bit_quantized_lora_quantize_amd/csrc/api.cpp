@@ -651,14 +651,16 @@ int bwd_packed_impl(const qlora_nf4_t* q, const qlora_packed_t* X8, const uint16
     s = hip_status(launch_gemm_bwd(g, st));
     if (s) return s;
   }
-  FragArgs fa{};
+  FinishVArgs fa{};
   fa.M = M;
   fa.slots = 1;
   fa.r = (int)r;
+  fa.V = pp.u;
   fa.T = T;
-  fa.U = pp.u;
-  fa.t_frags = pp.t_frags;
   fa.u_frags = pp.u_frags;
+  fa.t_frags = pp.t_frags;
+  s = hip_status(launch_finish_v(fa, st));
+  if (s) return s;
   ga.q[0].codes = X8->codes;
   ga.q[0].scale = X8->scale;
   ga.q[0].keep = rows;
@@ -667,7 +669,7 @@ int bwd_packed_impl(const qlora_nf4_t* q, const qlora_packed_t* X8, const uint16
   ga.q[1].x = dY;
   ga.q[1].frags = pp.t_frags;
   ga.q[1].part = pp.db_part;
-  return hip_status(launch_gram8(fa, ga, st));
+  return hip_status(launch_gram8(ga, st));
 }
 
 }  // namespace

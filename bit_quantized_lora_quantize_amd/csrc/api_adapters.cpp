@@ -30,6 +30,7 @@ Plan plan_view(int64_t M, int64_t slots, const void* base) {
   p.v.begin = c.take<int32_t>(slots + 1);
   p.v.tile = c.take<int4>(plan_most_tiles(M, slots));
   p.v.split = c.take<int4>(plan_most_splits(M, slots));
+  p.v.split_first = c.take<int32_t>(plan_most_splits(M, slots));
   p.v.parts = c.take<int2>(slots);
   p.v.hist = c.take<int32_t>(M > 1024 ? cdiv(M, 1024) * (slots + 1) : 0);
   p.bytes = c.off + 256;
@@ -46,6 +47,7 @@ bool bank_ok(const qlora_adapters_t* b) {
 
 struct AdaptersPlan {
   float* part;        // [splits][M][r]
+  uint16_t* vrows;    // [M][2 vrow_ranks(r)]
   uint16_t* t_frags;  // backward
   uint16_t* u_frags;
   float* da_part;     // [parts][r][d_in]
@@ -57,6 +59,7 @@ AdaptersPlan plan_adapters(bool backward, const qlora_adapters_t* b, int64_t M, 
   Carver c(ws);
   int64_t kper;
   p.part = c.take<float>(shrink_splits(M, backward ? b->d_out : b->d_in, &kper) * M * b->r);
+  p.vrows = c.take<uint16_t>(M * 2 * vrow_ranks(b->r));
   if (backward) {
     const int64_t tiles = plan_most_tiles(M, b->slots);
     p.t_frags = c.take<uint16_t>(frag_elems(tiles, b->r));
@@ -165,17 +168,34 @@ int qlora_adapters_fwd(const qlora_adapters_t* bank, const void* plan, size_t pl
   sa.P = X;
   sa.F = bank->A;
   sa.part = w.part;
+  sa.scale = bank->scale;
+  sa.vrows = w.vrows;
+  sa.v_out = T_save;
   s = hip_status(launch_shrink(sa, st));
   if (s) return s;
+  int64_t kper;
+  const int splits = shrink_splits(M, bank->d_in, &kper);
+  if (splits > 1) {
+    FinishVArgs fa{};
+    fa.plan = v;
+    fa.M = M;
+    fa.slots = bank->slots;
+    fa.r = (int)bank->r;
+    fa.splits = splits;
+    fa.scale = bank->scale;
+    fa.V = w.part;
+    fa.vrows = w.vrows;
+    fa.v_out = T_save;
+    s = hip_status(launch_finish_v(fa, st));
+    if (s) return s;
+  }
   ExpandArgs ea{};
   ea.plan = v;
   ea.M = M;
   ea.slots = bank->slots;
-  ea.K = bank->d_in;
   ea.d = bank->d_out;
   ea.r = (int)bank->r;
-  ea.part = w.part;
-  ea.scale = bank->scale;
+  ea.vrows = w.vrows;
   ea.F = bank->B;
   ea.in = Y0;
   ea.out = Y;
@@ -226,24 +246,7 @@ int qlora_adapters_bwd(const qlora_adapters_t* bank, const void* plan, size_t pl
   sa.part = w.part;
   s = hip_status(launch_shrink(sa, st));
   if (s) return s;
-  if (dX) {
-    ExpandArgs ea{};
-    ea.plan = v;
-    ea.M = M;
-    ea.slots = bank->slots;
-    ea.K = bank->d_out;
-    ea.d = bank->d_in;
-    ea.r = (int)bank->r;
-    ea.rd = true;
-    ea.part = w.part;
-    ea.scale = bank->scale;
-    ea.F = bank->A;
-    ea.in = dX0;
-    ea.out = dX;
-    s = hip_status(launch_expand(ea, st));
-    if (s) return s;
-  }
-  FragArgs fa{};
+  FinishVArgs fa{};
   fa.plan = v;
   fa.M = M;
   fa.slots = bank->slots;
@@ -251,10 +254,28 @@ int qlora_adapters_bwd(const qlora_adapters_t* bank, const void* plan, size_t pl
   int64_t kper;
   fa.splits = shrink_splits(M, bank->d_out, &kper);
   fa.scale = bank->scale;
+  fa.V = w.part;
   fa.T = T;
-  fa.U = w.part;
-  fa.t_frags = w.t_frags;
+  fa.vrows = dX ? w.vrows : nullptr;
   fa.u_frags = w.u_frags;
+  fa.t_frags = w.t_frags;
+  s = hip_status(launch_finish_v(fa, st));
+  if (s) return s;
+  if (dX) {
+    ExpandArgs ea{};
+    ea.plan = v;
+    ea.M = M;
+    ea.slots = bank->slots;
+    ea.d = bank->d_in;
+    ea.r = (int)bank->r;
+    ea.rd = true;
+    ea.vrows = w.vrows;
+    ea.F = bank->A;
+    ea.in = dX0;
+    ea.out = dX;
+    s = hip_status(launch_expand(ea, st));
+    if (s) return s;
+  }
   ga.plan = v;
   ga.q[0].x = X;
   if (X8) {
@@ -266,7 +287,7 @@ int qlora_adapters_bwd(const qlora_adapters_t* bank, const void* plan, size_t pl
   ga.q[1].x = dY;
   ga.q[1].frags = w.t_frags;
   ga.q[1].part = w.db_part;
-  return hip_status(launch_gram8(fa, ga, st));
+  return hip_status(launch_gram8(ga, st));
 }
 
 }  // extern "C"

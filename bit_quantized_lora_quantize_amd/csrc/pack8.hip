@@ -5,11 +5,17 @@
 //   code = the integer nearest to 127 x / a (ties to even), |code| <= 127
 //   restored x = RN_type(RN_fp32(code * scale))
 //
-// The nearest integer is decided exactly: k = rint(x * RN(127 / a)) in FP32 is
-// off by one at most, next to a border, and the sign of |127 x - k a| - a / 2
-// says so.  Both products are exact in FP64 (24 + 8 bits) and, a border's
-// neighbourhood being all that matters, so is their difference.  gfx950 issues
-// FP64 and FP32 operations at one rate, and both kernels are bound by memory.
+// The nearest integer is decided exactly.  t = RN(x * RN(127 / a)) is within
+// 2^-23 t of 127 x / a.
+//   BF16 x, a: a quotient that is no half integer is 2^-17 t or more away from
+//     every one (the difference is a multiple of the last place of x over 2 a,
+//     8-bit numbers both).  So t rounded to 20 bits is a half integer where the
+//     quotient is one, and on the quotient's side of it elsewhere.
+//   FP32: within 4e-5 of a half integer the sign of |127 x - k a| - a / 2 is
+//     taken in FP64, where both products (31 and 32 bits) and their difference
+//     are exact; one vector of 500 gets there.
+// (In FP64 for every value the kernel was bound by its arithmetic: 44 us for
+// 4096 x 11008 BF16.)
 //
 // Blocks whose a is below 2^-119, where 127 / a leaves FP32's range, restore as
 // zeros; a block that holds an infinity or a NaN restores as NaN.
@@ -33,66 +39,94 @@ __device__ __forceinline__ uint32_t max8(uint32_t v) {
   return v;
 }
 
-__device__ __forceinline__ int nearest_code(float x, float inv, float a) {
-  const float k = __builtin_rintf(x * inv);
-  const double d = 127.0 * (double)x - (double)k * (double)a;   // exact near a border
-  const double past = 2.0 * fabs(d) - (double)a;
-  int code = (int)k;
-  // past the border, or on it with an odd k
-  if (past > 0.0 || (past == 0.0 && (code & 1))) code += d > 0.0 ? 1 : -1;
-  return code;
+// Integers nearest to 127 x / a of eight values, as FP32.
+template <typename T>
+__device__ __forceinline__ void nearest_codes(const float* x, float inv, float a, float* k) {
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float t = x[j] * inv, c = t * 17.0f;   // 20 of 24 bits kept
+      k[j] = __builtin_rintf(c - (c - t));
+    }
+  } else {
+    bool near = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float t = x[j] * inv;
+      k[j] = __builtin_rintf(t);
+      near |= fabsf(t - k[j]) > 0.5f - 4e-5f;
+    }
+    if (near) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const double d = 127.0 * (double)x[j] - (double)k[j] * (double)a;
+        const double past = 2.0 * fabs(d) - (double)a;
+        // past the border, or on it with an odd k
+        if (past > 0.0 || (past == 0.0 && ((int)k[j] & 1))) k[j] += d > 0.0 ? 1.0f : -1.0f;
+      }
+    }
+  }
 }
 
-template <typename T, bool WHOLE>
+template <typename T>
 __device__ __forceinline__ void load8(const T* row, int64_t col, int64_t d, float* f) {
-  if (WHOLE || col + 8 <= d) {
-    if constexpr (sizeof(T) == 2) {
-      unpack<T>(load_vec(row + col), f);
-    } else {
-      unpack<T>(load_vec(row + col), f);
-      unpack<T>(load_vec(row + col + 4), f + 4);
-    }
+  if (col + 8 <= d) {
+#pragma unroll
+    for (int j = 0; j < 8; j += kVec<T>) unpack<T>(load_vec(row + col + j), f + j);
     return;
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) f[j] = col + j < d ? to_f32(row[col + j]) : 0.0f;
 }
 
-// A workgroup takes eight rows of four neighbouring blocks.
+// A workgroup takes 32 rows of four neighbouring blocks, a thread eight values
+// of four of the rows (their loads together): 128 bytes of scales of each block
+// column are written by one workgroup.
+constexpr int kPackRows = 4;
+
 template <typename T>
 __global__ __launch_bounds__(256) void k_pack8(const T* __restrict__ X, int64_t M, int64_t d,
                                                uint8_t* __restrict__ codes,
                                                float* __restrict__ scale) {
   const int64_t nb = (d + 63) / 64;
   const int sub = threadIdx.x & 7;              // eight values of the block
-  const int bcol = (threadIdx.x >> 3) & 3;      // block column within the workgroup's four
-  const int rsub = threadIdx.x >> 5;            // row within the workgroup's eight
+  const int bcol = (threadIdx.x >> 3) & 3;      // block within the workgroup's four
+  const int rsub = threadIdx.x >> 5;
   const int64_t cgroups = (nb + 3) / 4;
-  const int64_t rgroups = (M + 7) / 8;
+  const int64_t rgroups = (M + 8 * kPackRows - 1) / (8 * kPackRows);
   for (int64_t w = blockIdx.x; w < cgroups * rgroups; w += gridDim.x) {
-    const int64_t b = (w % cgroups) * 4 + bcol, m = (w / cgroups) * 8 + rsub;
-    if (b >= nb || m >= M) continue;
-    float f[8];
-    load8<T, false>(X + m * d, b * 64 + 8 * sub, d, f);
-    uint32_t top = 0;
+    const int64_t b = (w % cgroups) * 4 + bcol, m0 = (w / cgroups) * 8 * kPackRows + rsub;
+    if (b >= nb) continue;                      // (the same for a block's eight lanes)
+    float f[kPackRows][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[j]) & 0x7FFFFFFFu);
-    top = max8(top);
-    const float a = __uint_as_float(top);
-    float s = fminf(a / 127.0f, kMostScale);
-    const float inv = 127.0f / a;
-    uint32_t c[2] = {0, 0};
-    if (!(a < INFINITY)) {
-      s = __uint_as_float(0x7FC00000u);
-    } else if (a < kTiny) {
-      s = 0.0f;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        c[j >> 2] |= ((uint32_t)nearest_code(f[j], inv, a) & 0xFFu) << (8 * (j & 3));
+    for (int i = 0; i < kPackRows; ++i) {
+      const int64_t m = m0 + 8 * i < M ? m0 + 8 * i : M - 1;
+      load8(X + m * d, b * 64 + 8 * sub, d, f[i]);
     }
-    *reinterpret_cast<uint2*>(codes + (m * nb + b) * 64 + 8 * sub) = make_uint2(c[0], c[1]);
-    if (sub == 0) scale[b * M + m] = s;
+#pragma unroll
+    for (int i = 0; i < kPackRows; ++i) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[i][j]) & 0x7FFFFFFFu);
+      top = max8(top);
+      const float a = __uint_as_float(top);
+      float s = fminf(a / 127.0f, kMostScale);
+      uint32_t c[2] = {0, 0};
+      if (!(a < INFINITY)) {
+        s = __uint_as_float(0x7FC00000u);
+      } else if (a < kTiny) {
+        s = 0.0f;
+      } else {
+        float k[8];
+        nearest_codes<T>(f[i], 127.0f / a, a, k);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c[j >> 2] |= ((uint32_t)(int)k[j] & 0xFFu) << (8 * (j & 3));
+      }
+      const int64_t m = m0 + 8 * i;
+      if (m >= M) continue;
+      *reinterpret_cast<uint2*>(codes + (m * nb + b) * 64 + 8 * sub) = make_uint2(c[0], c[1]);
+      if (sub == 0) scale[b * M + m] = s;
+    }
   }
 }
 
@@ -130,8 +164,8 @@ __global__ __launch_bounds__(256) void k_unpack8(const uint8_t* __restrict__ cod
   }
 }
 
-unsigned pack_grid(int64_t M, int64_t d) {
-  const int64_t wgs = ((d + 255) / 256) * ((M + 7) / 8);
+unsigned pack_grid(int64_t M, int64_t d, int rows) {
+  const int64_t wgs = ((d + 255) / 256) * ((M + rows - 1) / rows);
   return (unsigned)std::min<int64_t>(wgs, int64_t(1) << 20);
 }
 
@@ -140,10 +174,10 @@ unsigned pack_grid(int64_t M, int64_t d) {
 hipError_t launch_pack8(int type, const void* X, int64_t M, int64_t d, uint8_t* codes,
                         float* scale, hipStream_t st) {
   if (type == QLORA_F32)
-    hipLaunchKernelGGL(k_pack8<float>, dim3(pack_grid(M, d)), dim3(256), 0, st,
+    hipLaunchKernelGGL(k_pack8<float>, dim3(pack_grid(M, d, 8 * kPackRows)), dim3(256), 0, st,
                        static_cast<const float*>(X), M, d, codes, scale);
   else
-    hipLaunchKernelGGL(k_pack8<uint16_t>, dim3(pack_grid(M, d)), dim3(256), 0, st,
+    hipLaunchKernelGGL(k_pack8<uint16_t>, dim3(pack_grid(M, d, 8 * kPackRows)), dim3(256), 0, st,
                        static_cast<const uint16_t*>(X), M, d, codes, scale);
   return hipGetLastError();
 }
@@ -151,10 +185,10 @@ hipError_t launch_pack8(int type, const void* X, int64_t M, int64_t d, uint8_t* 
 hipError_t launch_unpack8(const uint8_t* codes, const float* scale, int64_t M, int64_t d, int type,
                           void* X, hipStream_t st) {
   if (type == QLORA_F32)
-    hipLaunchKernelGGL(k_unpack8<float>, dim3(pack_grid(M, d)), dim3(256), 0, st, codes, scale, M,
+    hipLaunchKernelGGL(k_unpack8<float>, dim3(pack_grid(M, d, 8)), dim3(256), 0, st, codes, scale, M,
                        d, static_cast<float*>(X));
   else
-    hipLaunchKernelGGL(k_unpack8<uint16_t>, dim3(pack_grid(M, d)), dim3(256), 0, st, codes, scale,
+    hipLaunchKernelGGL(k_unpack8<uint16_t>, dim3(pack_grid(M, d, 8)), dim3(256), 0, st, codes, scale,
                        M, d, static_cast<uint16_t*>(X));
   return hipGetLastError();
 }

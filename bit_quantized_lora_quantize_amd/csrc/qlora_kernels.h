@@ -582,7 +582,8 @@ struct PlanView {
   int32_t* order;  // [M] token at each position
   int32_t* begin;  // [slots + 1] first position of each slot (batches of several spans)
   int4* tile;      // {slot (-1: none), first position, tokens, 0}
-  int4* split;     // {slot, first tile, tiles, number among its slot's splits (-1: the only one)}
+  int4* split;     // {slot, first tile, tokens, number among its slot's splits (-1: the only one)}
+  int32_t* split_first;   // their first positions
   int2* parts;     // [slots] {its splits' first partial result, its splits}
   int32_t* hist;   // scratch of the plan's own kernels
 };
@@ -609,13 +610,18 @@ hipError_t launch_plan(const PlanView& p, const int32_t* index, int64_t M, int64
                        hipStream_t st);
 
 // Ranges of the long axis K that k_shrink sums apart.
+#ifndef SHRINK_WGS
+#define SHRINK_WGS 1024
+#endif
 inline int shrink_splits(int64_t M, int64_t K, int64_t* kper) {
   const int64_t tiles = std::max<int64_t>(1, (M + kPlanTile - 1) / kPlanTile);
-  int64_t s = std::min<int64_t>((512 + tiles - 1) / tiles, (K + 255) / 256);
-  s = std::max<int64_t>(1, std::min<int64_t>(s, 16));
+  int64_t s = std::min<int64_t>((SHRINK_WGS + tiles - 1) / tiles, (K + 255) / 256);
+  s = std::max<int64_t>(1, std::min<int64_t>(s, tiles >= 32 ? 8 : 16));
   *kper = ((K + s - 1) / s + 255) / 256 * 256;
   return (int)((K + *kper - 1) / *kper);
 }
+// Ranks of a row of V in k_expand's operand (hi, then lo).
+inline int64_t vrow_ranks(int64_t r) { return r <= 32 ? 32 : (r <= 64 ? 64 : (r <= 128 ? 128 : 256)); }
 struct ShrinkArgs {
   PlanView plan;
   int64_t M, slots, K, kper;
@@ -624,40 +630,47 @@ struct ShrinkArgs {
   const uint16_t* P;    // [M][K]
   const uint16_t* F;    // [slots] of them
   float* part;          // [splits][M][r], by position
+  // with one split, instead of part:
+  const float* scale;   // [slots]
+  uint16_t* vrows;      // [M][2 vrow_ranks(r)] by position, or NULL (part)
+  float* v_out;         // [M][r] by token, or NULL
 };
 hipError_t launch_shrink(const ShrinkArgs& a, hipStream_t st);
 
-struct ExpandArgs {
+struct FinishVArgs {
   PlanView plan;
-  int64_t M, slots, K, d, cper;
-  int r, splits, chunks;   // splits, chunks, cper: set by launch_expand
-  bool rd;                 // F as [r][d] (else [d][r])
-  const float* part;       // of launch_shrink with the same K
-  const float* scale;      // [slots]
-  const uint16_t* F;       // [slots] of them
-  const uint16_t* in;      // [M][d], NULL: zeros; may be out
-  uint16_t* out;
-  float* v_out;            // [M][r] or NULL: scale * sums, by token, 0 without an adapter
+  int64_t M, slots;
+  int r, nb;               // nb: set by launch_finish_v
+  int splits;              // partial sums in V by position; 0: V by token, as it is
+  const float* scale;      // [slots], with splits
+  const float* V;
+  const float* T;          // [M][r] by token, with t_frags
+  uint16_t* vrows;         // outputs, each or NULL
+  float* v_out;
+  uint16_t* u_frags;       // V's
+  uint16_t* t_frags;       // T's
 };
-hipError_t launch_expand(const ExpandArgs& a, hipStream_t st);
-
+hipError_t launch_finish_v(const FinishVArgs& a, hipStream_t st);
 // Blocks of 16 ranks in the operands of the contractions.
 inline int frag_blocks(int64_t r) {
   return r <= 16 ? 1 : (r <= 32 ? 2 : (r <= 64 ? 4 : (r <= 128 ? 8 : 16)));
 }
 // Elements of one side's operands for `tiles` tiles.
 inline int64_t frag_elems(int64_t tiles, int64_t r) { return tiles * 3 * frag_blocks(r) * 1024; }
-struct FragArgs {
+
+struct ExpandArgs {
   PlanView plan;
-  int64_t M, slots;
-  int r, nb;               // nb: set by launch_gram8
-  int splits;              // of U's partial sums by position; 0: U by token, scaled
-  const float* scale;      // [slots], with splits
-  const float* T;          // [M][r] by token
-  const float* U;
-  uint16_t* t_frags;
-  uint16_t* u_frags;
+  int64_t M, slots, d;
+  int r, chunks, subs, tpi, most;   // all but r set by launch_expand
+  bool rd;                 // F as [r][d] (else [d][r])
+  const uint16_t* vrows;   // [M][2 vrow_ranks(r)] by position
+  const uint16_t* F;       // [slots] of them
+  const uint16_t* in;      // [M][d], NULL: zeros; may be out
+  uint16_t* out;
+  float* v_out;            // [M][r] or NULL: zeros for tokens without an adapter
 };
+hipError_t launch_expand(const ExpandArgs& a, hipStream_t st);
+
 struct GramSide {
   const uint16_t* x;       // BF16 [M][d], or
   const uint8_t* codes;    // 8-bit codes [M][round_up(d, 64)] (side 0 only) with
@@ -674,7 +687,7 @@ struct GramArgs8 {
   int tps;                 // without a plan: tiles a split
   GramSide q[2];           // dA from (U, X), dB from (T, dY)
 };
-hipError_t launch_gram8(const FragArgs& f, const GramArgs8& a, hipStream_t st);
+hipError_t launch_gram8(const GramArgs8& a, hipStream_t st);
 // Zeros in both outputs.
 hipError_t launch_gram_zero(const GramArgs8& a, hipStream_t st);
 
