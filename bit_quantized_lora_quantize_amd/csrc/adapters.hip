@@ -23,15 +23,6 @@
 #include "qlora_kernels.h"
 #include "row_ops.h"
 
-#ifndef EXPAND_OCC
-#define EXPAND_OCC 3
-#endif
-#ifndef EXPAND_WGS
-#define EXPAND_WGS 1024
-#endif
-#ifndef EXPAND_AHEAD
-#define EXPAND_AHEAD 2
-#endif
 
 namespace qlora {
 
@@ -48,14 +39,38 @@ __device__ __forceinline__ uint2 lds_tr(const uint16_t* p) {
 
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu); }
 
-// Eight elements of a row from column `col` on, zero at and past `end`.  Rows
-// start at any element: the vector need not be aligned.
-__device__ __forceinline__ u32x4 load8(const uint16_t* row, int64_t col, int64_t end) {
-  if (col + 8 <= end) return load_vec(row + col);
-  uint32_t h[8];
+// Rows start at any element: vectors need not be aligned.  Where eight elements
+// from `col` on would pass the row's end, the last eight of the row are loaded
+// (from at8) and moved down (past8 elements dropped at the front, zeros behind),
+// so that no lane waits for single elements; rows of fewer than eight take those
+// (few8).
+__device__ __forceinline__ int64_t at8(int64_t col, int64_t end) { return col < end - 8 ? col : end - 8; }
+__device__ __forceinline__ u32x4 past8(u32x4 v, int64_t drop) {
+  const int s = (int)(drop < 8 ? drop : 8);
+  u32x4 o;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) h[e] = col + e < end ? (uint32_t)row[col + e] : 0u;
-  return u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
+  for (int j = 0; j < 4; ++j) o[j] = s & 4 ? (j < 2 ? v[j + 2] : 0u) : v[j];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = s & 2 ? (j < 3 ? o[j + 1] : 0u) : o[j];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = s & 1 ? (o[j] >> 16) | (j < 3 ? o[j + 1] << 16 : 0u) : o[j];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = s & 8 ? 0u : o[j];
+  return o;
+}
+__device__ __forceinline__ u32x4 few8(const uint16_t* row, int64_t col, int64_t end) {
+  u32x4 o = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t x = row[col + e < end ? col + e : end - 1];
+    o[e >> 1] |= col + e < end ? x << (16 * (e & 1)) : 0u;
+  }
+  return o;
+}
+// Eight elements from column `col` on, zero at and past `end`.
+__device__ __forceinline__ u32x4 load8(const uint16_t* row, int64_t col, int64_t end) {
+  if (end < 8) return few8(row, col, end);
+  return past8(load_vec(row + at8(col, end)), col - at8(col, end));
 }
 __device__ __forceinline__ u32x4 only_if(bool ok, u32x4 v) {
 #pragma unroll
@@ -293,30 +308,24 @@ __global__ __launch_bounds__(64) void k_plan_place(PlanView p, const int32_t* __
 //
 // Item = one tile and one of `splits` ranges of K.  The four wavefronts of a
 // workgroup take the range's steps in turn, each all 64 tokens and all ranks:
-// no wavefront loads what another loads, and the loop has no barrier.  Their
-// sums are added through LDS at the end, in wavefront order.  KN: a step's rows
+// no wavefront loads what another loads, and the loop has no barrier.  A step's
+// loads are 16 a wavefront and not a step ahead: two workgroups a compute unit
+// hide more than a second set of registers does (16384 x 4096, rank 64: 49 us;
+// a step ahead, one workgroup: 65; read at 5.7 TB/s it would be 24).  The sums
+// are added through LDS at the end, in wavefront order.  KN: a step's rows
 // of F go through LDS of the wavefront's own, which the transposing reads turn
 // into operands.
 // ---------------------------------------------------------------------------
-#ifndef SHRINK_W
-#define SHRINK_W 4
-#endif
-#ifndef SHRINK_SK
-#define SHRINK_SK 2
-#endif
-#ifndef SHRINK_AHEAD
-#define SHRINK_AHEAD 0
-#endif
+constexpr int kShrinkWaves = 4;
+// K slices of 32 per step: two, whole lines of a row, where their loads fit the
+// registers beside the sums.
 template <int NB>
-constexpr int shrink_waves() { return NB <= 4 ? SHRINK_W : 4; }
-// K slices of 32 per step
-template <int NB>
-constexpr int shrink_slices() { return NB <= 4 ? SHRINK_SK : 1; }
+constexpr int shrink_slices() { return NB <= 4 ? 2 : 1; }
 template <int NB, bool KN>
 constexpr int shrink_lds() {
   constexpr int CN = NB < 4 ? NB : 4;
-  constexpr int red = shrink_waves<NB>() * 16 * 16 * CN * 4;
-  constexpr int stage = KN ? shrink_waves<NB>() * 32 * shrink_slices<NB>() * (16 * NB + 8) * 2 : 0;
+  constexpr int red = kShrinkWaves * 16 * 16 * CN * 4;
+  constexpr int stage = KN ? kShrinkWaves * 32 * shrink_slices<NB>() * (16 * NB + 8) * 2 : 0;
   return red > stage ? red : stage;
 }
 
@@ -329,11 +338,11 @@ __device__ __forceinline__ void put_vrow(uint16_t* vrows, int64_t pos, int i, in
   row[rp + i] = bf16_bits(lo);
 }
 
-// One item with RB blocks of 16 tokens.  R8: F's rows of r are whole 16-byte
-// pieces (KN).
-template <int NB, bool KN, bool R8, int RB>
+// One item with RB blocks of 16 tokens.  FAST: K of eight or
+// more and, KN, rows of F that are whole 16-byte pieces.
+template <int NB, bool KN, bool FAST, int RB>
 __device__ __forceinline__ void shrink_item(const ShrinkArgs& a, const int4& td, int s, uint8_t* lds) {
-  constexpr int W = shrink_waves<NB>(), CN = NB < 4 ? NB : 4, SK = shrink_slices<NB>();
+  constexpr int W = kShrinkWaves, CN = NB < 4 ? NB : 4, SK = shrink_slices<NB>();
   constexpr int LF = 16 * NB + 8;                  // staged row of F, elements
   constexpr int STEP = 32 * SK;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -350,7 +359,8 @@ __device__ __forceinline__ void shrink_item(const ShrinkArgs& a, const int4& td,
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb) {
     const int row = min(16 * rb + r16, count - 1);
-    xp[rb] = a.P + (int64_t)a.plan.order[first + row] * K + 8 * g;
+    const int64_t tok = a.plan.head ? a.plan.order[first + row] : first + row;
+    xp[rb] = a.P + tok * K;
   }
 
   f32x4 acc[RB][NB];
@@ -359,24 +369,27 @@ __device__ __forceinline__ void shrink_item(const ShrinkArgs& a, const int4& td,
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) acc[rb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // whole steps: loads without conditions, a step ahead (F's first: their
-  // addresses wait for nothing)
-  auto load = [&](int64_t k, u32x4 (&x)[SK][RB], u32x4 (&f)[SK * NB]) {
+  // whole steps: loads without conditions (F's first: their addresses wait for
+  // nothing)
+  auto load = [&](int64_t k, const int (&off)[SK], int rows, u32x4 (&x)[SK][RB], u32x4 (&f)[SK * NB]) {
 #pragma unroll
     for (int u = 0; u < SK * NB; ++u) {
       if (KN) {
-        const int piece = lane + 64 * u, row = piece / (2 * NB), col = 8 * (piece % (2 * NB));
+        const int piece = lane + 64 * u, row = min(piece / (2 * NB), rows), col = 8 * (piece % (2 * NB));
         f[u] = load_vec(F + (k + row) * r + (col < r ? col : 0));
       } else {
         const int i = min(16 * (u / SK) + r16, r - 1);
-        f[u] = load_vec(F + i * K + k + 32 * (u % SK) + 8 * g);
+        f[u] = load_vec(F + i * K + k + off[u % SK]);
       }
     }
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
-      for (int sl = 0; sl < SK; ++sl) x[sl][rb] = load_vec(xp[rb] + k + 32 * sl);
+      for (int sl = 0; sl < SK; ++sl) x[sl][rb] = load_vec(xp[rb] + k + off[sl]);
   };
+  int off[SK];                                     // the lane's columns of a step
+#pragma unroll
+  for (int sl = 0; sl < SK; ++sl) off[sl] = 32 * sl + 8 * g;
   auto compute = [&](const u32x4 (&x)[SK][RB], const u32x4 (&f)[SK * NB]) {
     if (KN) {
 #pragma unroll
@@ -402,46 +415,53 @@ __device__ __forceinline__ void shrink_item(const ShrinkArgs& a, const int4& td,
   int64_t k = k_begin + STEP * w;
   // (a piece of F's rows of odd r may reach into the next row, which the last
   // row of all does not have)
-  const int64_t k_whole = k_begin + (k_end - k_begin - (KN && !R8 && k_end == K ? 1 : 0)) / STEP * STEP;
+  const int64_t k_whole = k_begin + (k_end - k_begin - (KN && !FAST && k_end == K ? 1 : 0)) / STEP * STEP;
   if (k < k_whole) {
     const int64_t k_last = k + (k_whole - 1 - k) / (STEP * W) * (STEP * W);
-    if constexpr (SHRINK_AHEAD) {
-      u32x4 xa[SK][RB], fa[SK * NB], xb[SK][RB], fb[SK * NB];
-      load(k, xa, fa);
-      for (; k <= k_last; k += 2 * STEP * W) {
-        load(min(k + STEP * W, k_last), xb, fb);
-        __builtin_amdgcn_sched_barrier(0);
-        compute(xa, fa);
-        load(min(k + 2 * STEP * W, k_last), xa, fa);
-        __builtin_amdgcn_sched_barrier(0);
-        if (k + STEP * W <= k_last) compute(xb, fb);
-      }
-    } else {
-      u32x4 x[SK][RB], f[SK * NB];
-      for (; k <= k_last; k += STEP * W) {
-        load(k, x, f);
-        __builtin_amdgcn_sched_barrier(0);
-        compute(x, f);
-      }
+    u32x4 x[SK][RB], f[SK * NB];
+    for (; k <= k_last; k += STEP * W) {
+      load(k, off, STEP - 1, x, f);
+      __builtin_amdgcn_sched_barrier(0);           // all of a step's loads before its products
+      compute(x, f);
     }
     k = k_last + STEP * W;
   }
   // the last, partial step
   for (; k < k_end; k += STEP * W) {
     u32x4 x[SK][RB], f[SK * NB];
+    if constexpr (FAST) {
+      // K ends it (the ranges before the last are whole steps)
+      int end_off[SK];
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb)
+      for (int sl = 0; sl < SK; ++sl) end_off[sl] = (int)(at8(k + off[sl], k_end) - k);
+      load(k, end_off, (int)(k_end - 1 - k), x, f);
+#pragma unroll
+      for (int sl = 0; sl < SK; ++sl) {
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) x[sl][rb] = past8(x[sl][rb], off[sl] - end_off[sl]);
+        if (!KN) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) f[nb * SK + sl] = past8(f[nb * SK + sl], off[sl] - end_off[sl]);
+        }
+      }
+      if (KN) {
+#pragma unroll
+        for (int u = 0; u < SK * NB; ++u) f[u] = only_if(k + (lane + 64 * u) / (2 * NB) < k_end, f[u]);
+      }
+    } else {
 #pragma unroll
       for (int sl = 0; sl < SK; ++sl)
-        x[sl][rb] = load8(xp[rb] - 8 * g, k + 32 * sl + 8 * g, k_end);
 #pragma unroll
-    for (int u = 0; u < SK * NB; ++u) {
-      if (KN) {
-        const int piece = lane + 64 * u, row = piece / (2 * NB), col = 8 * (piece % (2 * NB));
-        f[u] = k + row < k_end ? load8(F + (k + row) * r, col, r) : u32x4{0, 0, 0, 0};
-      } else {
-        const int i = min(16 * (u / SK) + r16, r - 1);
-        f[u] = load8(F + i * K, k + 32 * (u % SK) + 8 * g, k_end);
+        for (int rb = 0; rb < RB; ++rb) x[sl][rb] = load8(xp[rb], k + off[sl], k_end);
+#pragma unroll
+      for (int u = 0; u < SK * NB; ++u) {
+        if (KN) {
+          const int piece = lane + 64 * u, row = piece / (2 * NB), col = 8 * (piece % (2 * NB));
+          const int64_t at = k + row < k_end ? k + row : k_end - 1;
+          f[u] = only_if(k + row < k_end, load8(F + at * r, col, r));
+        } else {
+          f[u] = load8(F + min(16 * (u / SK) + r16, r - 1) * K, k + off[u % SK], k_end);
+        }
       }
     }
     compute(x, f);
@@ -486,31 +506,32 @@ __device__ __forceinline__ void shrink_item(const ShrinkArgs& a, const int4& td,
   lds_barrier();
 }
 
-#ifndef SHRINK_OCC
-#define SHRINK_OCC 2
-#endif
-template <int NB>
-constexpr int shrink_occ() { return NB <= 4 ? SHRINK_OCC : 1; }
-template <int NB, bool KN, bool R8>
-__global__ __launch_bounds__(64 * shrink_waves<NB>(), shrink_occ<NB>()) void k_shrink(ShrinkArgs a) {
+template <int NB, bool KN, bool FAST>
+__global__ __launch_bounds__(64 * kShrinkWaves, NB <= 4 ? 2 : 1) void k_shrink(ShrinkArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t slds[];
-  // the grid has no more workgroups than the list room for items
-  int4 td = a.plan.tile[blockIdx.x / a.splits];
-  if (!plan_fits(a.plan, a.M, a.slots) || td.z <= 0) return;
-  const int items = a.plan.head[kPlanTiles] * a.splits;
+  int4 td = {0, 0, 0, 0};
+  int tiles = (int)((a.M + 63) / 64);
+  if (a.plan.head) {
+    // the grid has no more workgroups than the list room for items
+    td = a.plan.tile[blockIdx.x / a.splits];
+    if (!plan_fits(a.plan, a.M, a.slots) || td.z <= 0) return;
+    tiles = a.plan.head[kPlanTiles];
+  }
+  const int items = tiles * a.splits;
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
     const int t = item / a.splits, s = item % a.splits;
-    if (item != (int)blockIdx.x) td = a.plan.tile[t];
+    if (!a.plan.head) td = int4{0, 64 * t, (int)min((int64_t)64, a.M - 64 * (int64_t)t), 0};
+    else if (item != (int)blockIdx.x) td = a.plan.tile[t];
     // few tokens: no registers and loads for blocks of tokens that are not there
-    if (td.z <= 16) shrink_item<NB, KN, R8, 1>(a, td, s, slds);
-    else shrink_item<NB, KN, R8, 4>(a, td, s, slds);
+    if (td.z <= 16) shrink_item<NB, KN, FAST, 1>(a, td, s, slds);
+    else shrink_item<NB, KN, FAST, 4>(a, td, s, slds);
   }
 }
 
 // The sums of k_shrink's partial results, in order: up to Q pieces of N ranks
-// from part + at[] on, `stride` between the splits.  Few splits: every load at
-// once; many: one piece's at once.
-template <int Q, int N>
+// part + at[] on, `stride` between the at most SM splits.  Every load is
+// issued before the first sum.
+template <int SM, int Q, int N>
 __device__ __forceinline__ void sum_parts(const float* part, const int (&at)[Q], const bool (&on)[Q],
                                           int splits, int64_t stride, float (&v)[Q][N]) {
   typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
@@ -527,37 +548,20 @@ __device__ __forceinline__ void sum_parts(const float* part, const int (&at)[Q],
   for (int q = 0; q < Q; ++q)
 #pragma unroll
     for (int j = 0; j < N; ++j) v[q][j] = 0.0f;
-  if (splits <= 4) {
-    float x[4][Q][N];
+  float x[SM][Q][N];
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+  for (int s = 0; s < SM; ++s)
 #pragma unroll
-      for (int q = 0; q < Q; ++q)
-        if (s < splits && on[q]) get(part + s * stride + at[q], x[s][q]);
+    for (int q = 0; q < Q; ++q)
+      if (s < splits && on[q]) get(part + s * stride + at[q], x[s][q]);
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+  for (int s = 0; s < SM; ++s)
 #pragma unroll
-      for (int q = 0; q < Q; ++q)
-        if (s < splits && on[q]) {
+    for (int q = 0; q < Q; ++q)
+      if (s < splits && on[q]) {
 #pragma unroll
-          for (int j = 0; j < N; ++j) v[q][j] = s == 0 ? x[s][q][j] : v[q][j] + x[s][q][j];
-        }
-    return;
-  }
-#pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    if (!on[q]) continue;
-    float x[16][N];
-#pragma unroll
-    for (int s = 0; s < 16; ++s)
-      if (s < splits) get(part + s * stride + at[q], x[s]);
-#pragma unroll
-    for (int s = 0; s < 16; ++s)
-      if (s < splits) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) v[q][j] = s == 0 ? x[s][j] : v[q][j] + x[s][j];
+        for (int j = 0; j < N; ++j) v[q][j] = s == 0 ? x[s][q][j] : v[q][j] + x[s][q][j];
       }
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -626,7 +630,41 @@ __device__ __forceinline__ void store8(uint16_t* row, int64_t col, int64_t end, 
   }
 }
 
-template <int KS, bool RD, bool R8, bool DEEP>
+// V of the lane's operand (ranks 32 ks + 8 g .. +8 of the token at `pos`) as hi
+// and lo: read, or SUMS, from k_shrink's partial results (r a multiple of 4).
+// `save`: also to the caller, by token.
+template <int KS, bool SUMS>
+__device__ __forceinline__ void expand_v(const ExpandArgs& a, int pos, int ks, float sc, bool save,
+                                         u32x4& vh, u32x4& vl) {
+  const int g = (threadIdx.x & 63) >> 4, i = 32 * ks + 8 * g;
+  if constexpr (!SUMS) {
+    const uint16_t* v = a.vrows + (int64_t)pos * 64 * KS + i;
+    vh = *reinterpret_cast<const u32x4*>(v);
+    vl = *reinterpret_cast<const u32x4*>(v + 32 * KS);
+  } else {
+    const int r = a.r;
+    const int at[2] = {pos * r + (i < r ? i : 0), pos * r + (i + 4 < r ? i + 4 : 0)};
+    const bool on[2] = {i < r, i + 4 < r};
+    float v[2][4];
+    sum_parts<kShrinkSplits, 2, 4>(a.part, at, on, a.splits, a.M * r, v);
+    float* out = save ? a.v_out + (int64_t)a.plan.order[pos] * r + i : nullptr;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[q][j] = on[q] ? v[q][j] * sc : 0.0f;
+        if (save && on[q]) out[4 * q + j] = v[q][j];
+      }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float x = v[j >> 1][2 * (j & 1)], y = v[j >> 1][2 * (j & 1) + 1];
+      vh[j] = pack_bf16x2(x, y);
+      vl[j] = pack_bf16x2(x - bf16lo_to_f32(vh[j]), y - bf16hi_to_f32(vh[j]));
+    }
+  }
+}
+
+template <int KS, bool RD, bool R8, bool DEEP, bool SUMS>
 __device__ __forceinline__ void expand_many(const ExpandArgs& a, int slot, int first, int tokens,
                                             int64_t c0, uint8_t* lds) {
   constexpr int L = expand_ld<KS, RD>();
@@ -650,20 +688,21 @@ __device__ __forceinline__ void expand_many(const ExpandArgs& a, int slot, int f
     tok[0] = a.plan.order[place(j, l8)];
     tok[1] = a.plan.order[place(j, 8 + l8)];
   };
-  auto load = [&](int j, const int (&tok)[2], Rows& t) {
-    const uint16_t* v = a.vrows + (int64_t)place(j, r16) * 64 * KS + 8 * g;
+  const float sc = SUMS ? a.scale[slot] : 1.0f;
+  auto load_v = [&](int j, Rows& t) {
+    const bool save = SUMS && a.v_out && c0 == 0 && 64 * j + 16 * w + r16 < tokens;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      t.v[ks][0] = *reinterpret_cast<const u32x4*>(v + 32 * ks);
-      t.v[ks][1] = *reinterpret_cast<const u32x4*>(v + 32 * (KS + ks));
-    }
+    for (int ks = 0; ks < KS; ++ks)
+      expand_v<KS, SUMS>(a, place(j, r16), ks, sc, save, t.v[ks][0], t.v[ks][1]);
+  };
+  auto load_y = [&](const int (&tok)[2], Rows& t) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       t.at[h] = tok[h] * d + c0 + c8;
       if (!a.in) continue;
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        t.y[u][h] = whole ? load_vec(a.in + t.at[h] + 64 * u) : load8(a.in + tok[h] * d, c0 + 64 * u + c8, d);
+        t.y[u][h] = d >= 8 ? load_vec(a.in + tok[h] * d + at8(c0 + 64 * u + c8, d)) : few8(a.in + tok[h] * d, c8, d);
     }
   };
   auto work = [&](int j, Rows& t) {
@@ -687,12 +726,14 @@ __device__ __forceinline__ void expand_many(const ExpandArgs& a, int slot, int f
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float* s = turn + (8 * h + l8) * kTurn + c8;
-        const u32x4 o = expand_result(a.in ? t.y[u][h] : u32x4{0, 0, 0, 0},
-                                      *reinterpret_cast<const f32x4*>(s),
+        const int64_t col = c0 + 64 * u + c8;
+        u32x4 y = {0, 0, 0, 0};
+        if (a.in) y = whole || d < 8 ? t.y[u][h] : past8(t.y[u][h], col - at8(col, d));
+        const u32x4 o = expand_result(y, *reinterpret_cast<const f32x4*>(s),
                                       *reinterpret_cast<const f32x4*>(s + 4));
         if (64 * j + 16 * w + 8 * h + l8 >= tokens) continue;
         if (whole) store_vec(a.out + t.at[h] + 64 * u, o);
-        else store8(a.out + t.at[h] - c0 - c8, c0 + 64 * u + c8, d, o);
+        else store8(a.out + t.at[h] - c0 - c8, col, d, o);
       }
     }
   };
@@ -702,7 +743,8 @@ __device__ __forceinline__ void expand_many(const ExpandArgs& a, int slot, int f
   int next[2];
   if (mine) {
     token(0, next);
-    load(0, next, ta);                             // in flight while F is staged
+    load_y(next, ta);                              // in flight while F is staged
+    if (!SUMS) load_v(0, ta);
     if (DEEP) token(1, next);
   }
   lds_barrier();                                   // the last item's F is no longer read
@@ -711,8 +753,8 @@ __device__ __forceinline__ void expand_many(const ExpandArgs& a, int slot, int f
 #pragma unroll 4
     for (int e = threadIdx.x; e < 32 * KS * P; e += 256) {
       const int i = e / P, cc = 8 * (e % P);
-      u32x4 v = {0, 0, 0, 0};
-      if (i < r) v = whole ? load_vec(F + (int64_t)i * d + c0 + cc) : load8(F + (int64_t)i * d, c0 + cc, d);
+      const uint16_t* row = F + (int64_t)(i < r ? i : 0) * d;
+      const u32x4 v = only_if(i < r, whole ? load_vec(row + c0 + cc) : load8(row, c0 + cc, d));
       *reinterpret_cast<u32x4*>(fl + i * L + cc) = v;
     }
   } else {
@@ -720,26 +762,30 @@ __device__ __forceinline__ void expand_many(const ExpandArgs& a, int slot, int f
 #pragma unroll 4
     for (int e = threadIdx.x; e < kExpandCols * P; e += 256) {
       const int n = e / P, i = 8 * (e % P);
-      u32x4 v = {0, 0, 0, 0};
-      if (c0 + n < d && i < r) v = R8 ? load_vec(F + (c0 + n) * r + i) : load8(F + (c0 + n) * r, i, r);
+      const bool ok = c0 + n < d && i < r;
+      const uint16_t* row = F + (c0 + n < d ? c0 + n : 0) * r;
+      const u32x4 v = only_if(ok, R8 ? load_vec(row + (i < r ? i : 0)) : load8(row, i, r));
       *reinterpret_cast<u32x4*>(fl + n * L + i) = v;
     }
   }
   lds_barrier();
   if (!mine) return;
   if constexpr (!DEEP) {
+    if (SUMS) load_v(0, ta);
     work(0, ta);
   } else {
     Rows tb;
     for (int j = 0; j < tiles; j += 2) {
       if (j + 1 < tiles) {
-        load(j + 1, next, tb);
+        load_v(j + 1, tb);
+        load_y(next, tb);
         token(j + 2, next);
       }
       work(j, ta);
       if (j + 1 >= tiles) break;
       if (j + 2 < tiles) {
-        load(j + 2, next, ta);
+        load_v(j + 2, ta);
+        load_y(next, ta);
         token(j + 3, next);
       }
       work(j + 1, tb);
@@ -748,7 +794,7 @@ __device__ __forceinline__ void expand_many(const ExpandArgs& a, int slot, int f
 }
 
 // Up to 16 tokens: wavefront w takes columns 64 w .. of the item's.
-template <int KS, bool RD, bool R8>
+template <int KS, bool RD, bool R8, bool SUMS>
 __device__ __forceinline__ void expand_few(const ExpandArgs& a, int slot, int first, int tokens,
                                            int64_t c0, uint8_t* lds) {
   constexpr int LF = 72;                           // staged row of F
@@ -784,7 +830,8 @@ __device__ __forceinline__ void expand_few(const ExpandArgs& a, int slot, int fi
     }
   const int pos = first + min(r16, tokens - 1);
   const int64_t tok = a.plan.order[pos];
-  const uint16_t* v = a.vrows + (int64_t)pos * 64 * KS + 8 * g;
+  const float sc = SUMS ? a.scale[slot] : 1.0f;
+  const bool save = SUMS && a.v_out && col0 == 0 && r16 < tokens;
   u32x4 y[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -794,8 +841,8 @@ __device__ __forceinline__ void expand_few(const ExpandArgs& a, int slot, int fi
   }
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks) {
-    const u32x4 vh = *reinterpret_cast<const u32x4*>(v + 32 * ks);
-    const u32x4 vl = *reinterpret_cast<const u32x4*>(v + 32 * (KS + ks));
+    u32x4 vh, vl;
+    expand_v<KS, SUMS>(a, pos, ks, sc, save, vh, vl);
     if (RD) {
 #pragma unroll
       for (int u = 0; u < 4; ++u)
@@ -836,8 +883,8 @@ __device__ __forceinline__ void expand_none(const ExpandArgs& a, const int4& td,
 }
 
 // DEEP: items of several tiles, from the list of splits; else single tiles.
-template <int KS, bool RD, bool R8, bool DEEP>
-__global__ __launch_bounds__(256, KS > 4 ? 1 : (DEEP || KS > 2 ? 2 : EXPAND_OCC)) void k_expand(ExpandArgs a) {
+template <int KS, bool RD, bool R8, bool DEEP, bool SUMS>
+__global__ __launch_bounds__(256, KS > 4 ? 1 : (DEEP || KS > 2 ? 2 : 3)) void k_expand(ExpandArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t elds[];
   // the grid has no more workgroups than the lists room for items
   const int g0 = min((int)blockIdx.x / a.chunks / a.subs, a.most - 1);
@@ -863,8 +910,8 @@ __global__ __launch_bounds__(256, KS > 4 ? 1 : (DEEP || KS > 2 ? 2 : EXPAND_OCC)
     const int skip = DEEP ? group % a.subs * a.tpi * 64 : 0;
     const int tokens = DEEP ? min(rec.z - skip, a.tpi * 64) : rec.z;
     if (tokens <= 0) continue;
-    if (tokens <= 16) expand_few<KS, RD, R8>(a, rec.x, first + skip, tokens, c0, elds);
-    else expand_many<KS, RD, R8, DEEP>(a, rec.x, first + skip, tokens, c0, elds);
+    if (tokens <= 16) expand_few<KS, RD, R8, SUMS>(a, rec.x, first + skip, tokens, c0, elds);
+    else expand_many<KS, RD, R8, DEEP, SUMS>(a, rec.x, first + skip, tokens, c0, elds);
   }
 }
 
@@ -878,32 +925,39 @@ __global__ __launch_bounds__(256, KS > 4 ? 1 : (DEEP || KS > 2 ? 2 : EXPAND_OCC)
 // and 32 tokens one KB in the order of an MFMA's lanes; zero past the tile's
 // tokens and past the rank.
 // ---------------------------------------------------------------------------
+template <int SM>
 __global__ __launch_bounds__(256) void k_finish(FinishVArgs a) {
   constexpr int L = 72;
-  __shared__ __attribute__((aligned(16))) uint16_t st[3][64 * L];
-  if (a.plan.head && !plan_fits(a.plan, a.M, a.slots)) return;
+  __shared__ __attribute__((aligned(16))) uint16_t st[3][32 * L];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
   const int r = a.r, nb = a.nb, groups = (nb + 3) / 4, sides = a.t_frags ? 2 : 1;
-  const int rp = (r + 31) / 32 * 32;
-  const int rp_v = rp <= 64 ? rp : (rp <= 128 ? 128 : 256);   // k_expand's width
-  const int tiles = a.plan.head ? a.plan.head[kPlanTiles] : (int)((a.M + 63) / 64);
-  for (int item = blockIdx.x; item < tiles * groups * sides; item += gridDim.x) {
-    const bool is_t = item % sides == 1;
-    const int grp = item / sides % groups, t = item / sides / groups;
-    int4 td = {0, 64 * t, (int)min((int64_t)64, a.M - 64 * (int64_t)t), 0};
-    if (a.plan.head) td = a.plan.tile[t];
-    const int first = td.y, count = td.z, i0 = 64 * grp;
-    const bool by_part = !is_t && a.splits > 0;
-    const float sc = by_part ? a.scale[td.x] : 1.0f;
-    const float* v_in = is_t ? a.T : a.V;
+  const int per_tile = 2 * groups * sides;         // item = 32 tokens of a tile, 64 ranks, side
+  int4 td = {0, 0, 0, 0};
+  int tiles = (int)((a.M + 63) / 64);
+  if (a.plan.head) {
+    td = a.plan.tile[min((int)blockIdx.x / per_tile, a.most - 1)];
+    if (!plan_fits(a.plan, a.M, a.slots)) return;
+    tiles = a.plan.head[kPlanTiles];
+  }
+  for (int item = blockIdx.x; item < tiles * per_tile; item += gridDim.x) {
+    const int t = item / per_tile, sub = item % per_tile;
+    const int slice = sub & 1, grp = (sub >> 1) % groups;
+    const bool is_t = (sub >> 1) / groups == 1;
+    if (!a.plan.head) td = int4{0, 64 * t, (int)min((int64_t)64, a.M - 64 * (int64_t)t), 0};
+    else if (item != (int)blockIdx.x) td = a.plan.tile[t];
+    const int first = td.y + 32 * slice, count = min(32, td.z - 32 * slice), i0 = 64 * grp;
     uint16_t* frags = is_t ? a.t_frags : a.u_frags;
+    if (count <= 0 && !frags) continue;
+    const bool by_part = !is_t && a.splits > 0;
+    const float sc = by_part && a.scale ? a.scale[td.x] : a.one_scale;
+    const float* v_in = is_t ? a.T : a.V;
     const int64_t stride = a.M * r;
-    const int cols = min(64, max(16 * nb, a.vrows && !is_t ? rp_v : 0) - i0);
-    const int rows = frags ? 64 : (count + 15) / 16 * 16;
+    const int cols = min(64, max(16 * nb, a.vrows && !is_t ? a.rp : 0) - i0);
+    const int rows = frags ? 32 : (count + 15) / 16 * 16;
     lds_barrier();
     auto fill = [&](auto ranks) {
-      constexpr int N = decltype(ranks)::value, Q = 4, PR = 64 / N;
+      constexpr int N = decltype(ranks)::value, Q = 2, PR = 64 / N;
 #pragma unroll 1
       for (int e0 = threadIdx.x; e0 < rows * PR; e0 += 256 * Q) {
         float v[Q][N];
@@ -919,7 +973,7 @@ __global__ __launch_bounds__(256) void k_finish(FinishVArgs a) {
           if (on[q] && (!by_part || a.v_out)) tok[q] = a.plan.head ? a.plan.order[first + row] : first + row;
         }
         if (by_part) {
-          sum_parts<Q, N>(v_in + (int64_t)first * r, at, on, a.splits, stride, v);
+          sum_parts<SM, Q, N>(v_in + (int64_t)first * r, at, on, a.splits, stride, v);
         } else {
 #pragma unroll
           for (int q = 0; q < Q; ++q)
@@ -933,7 +987,7 @@ __global__ __launch_bounds__(256) void k_finish(FinishVArgs a) {
           if (row >= rows || i >= cols) continue;
 #pragma unroll
           for (int j = 0; j < N; ++j) {
-            const float x = on[q] ? v[q][j] * sc : 0.0f;
+            const float x = on[q] ? (by_part ? v[q][j] * sc : v[q][j]) : 0.0f;
             if (!is_t && on[q] && a.v_out) a.v_out[tok[q] * r + i0 + i + j] = x;
             float hi, rest, mid, lo;
             split_bf16(x, hi, rest);
@@ -949,10 +1003,10 @@ __global__ __launch_bounds__(256) void k_finish(FinishVArgs a) {
     else fill(std::integral_constant<int, 1>{});
     lds_barrier();
     if (frags) {
-      for (int u = w; u < 24; u += 4) {            // (term, 16 ranks, 32 tokens)
-        const int term = u >> 3, b = (u >> 1) & 3, slice = u & 1;
+      for (int u = w; u < 12; u += 4) {            // (term, 16 ranks)
+        const int term = u >> 2, b = u & 3;
         if (4 * grp + b >= nb) continue;
-        const uint16_t* p = &st[term][(32 * slice + 8 * g + (r16 >> 2)) * L + 16 * b + 4 * (r16 & 3)];
+        const uint16_t* p = &st[term][(8 * g + (r16 >> 2)) * L + 16 * b + 4 * (r16 & 3)];
         const uint2 lo = lds_tr(p), hi = lds_tr(p + 4 * L);
         const int64_t at = (((int64_t)t * 3 + term) * nb + 4 * grp + b) * 2 + slice;
         *reinterpret_cast<u32x4*>(frags + at * 512 + lane * 8) = u32x4{lo.x, lo.y, hi.x, hi.y};
@@ -960,12 +1014,25 @@ __global__ __launch_bounds__(256) void k_finish(FinishVArgs a) {
     }
     if (!is_t && a.vrows) {
       // the lo of a pair is what the mid of three is
-      const int pieces = min(64, rp_v - i0) / 8;
+      const int pieces = min(64, a.rp - i0) / 8;
       for (int e = threadIdx.x; e < count * 2 * pieces; e += 256) {
         const int row = e / (2 * pieces), h = e / pieces & 1, i = 8 * (e % pieces);
-        *reinterpret_cast<u32x4*>(a.vrows + (int64_t)(first + row) * 2 * rp_v + h * rp_v + i0 + i) =
+        *reinterpret_cast<u32x4*>(a.vrows + (int64_t)(first + row) * 2 * a.rp + h * a.rp + i0 + i) =
             *reinterpret_cast<const u32x4*>(&st[h][row * L + i]);
       }
+    }
+  }
+  // gradients of slots without tokens
+  if (!a.zero_a) return;
+  const int64_t na = (int64_t)r * a.d_a, n = na + (int64_t)r * a.d_b;
+  const int64_t chunk = 4096;
+  const int64_t per_slot = (n + chunk - 1) / chunk;
+  for (int64_t item = blockIdx.x; item < a.slots * per_slot; item += gridDim.x) {
+    const int slot = (int)(item / per_slot);
+    if (a.plan.parts[slot].y != 0) continue;
+    for (int64_t e = item % per_slot * chunk + threadIdx.x; e < min(n, (item % per_slot + 1) * chunk); e += 256) {
+      if (e < na) a.zero_a[slot * na + e] = 0.0f;
+      else a.zero_b[slot * (n - na) + e - na] = 0.0f;
     }
   }
 }
@@ -1094,9 +1161,7 @@ __device__ __forceinline__ void gram_item(const GramArgs8& a, const GramSide& q,
     gram_stage<PACKED>(cur, lane, st);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if (c + 1 < C) {
-        load_v(fr, c + 1, v[(c + 1) & 1]);
-      }
+      if (c + 1 < C) load_v(fr, c + 1, v[(c + 1) & 1]);
       if (c + 2 == C && j + 4 < tiles) {
         gram_load<PACKED>(q, a.M, c0, next, lane, cur);
         next = token(j + 8);
@@ -1128,27 +1193,37 @@ __global__ __launch_bounds__(256, NB <= 4 ? 2 : 1) void k_gram8(GramArgs8 a) {
   constexpr int LR = 68;                            // a reduced row, FP32
   __shared__ __attribute__((aligned(16))) uint8_t glds[4 * 64 * kGL * 2];
   static_assert(4 * 16 * LR * 4 <= 4 * 64 * kGL * 2, "reduction buffer");
-  if (a.plan.head && !plan_fits(a.plan, a.M, a.slots)) return;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
   uint16_t* st = reinterpret_cast<uint16_t*>(glds) + w * 64 * kGL;
   float* red = reinterpret_cast<float*>(glds);
   const int tiles = (int)((a.M + 63) / 64);
-  const int splits = a.plan.head ? a.plan.head[kPlanSplits] : (tiles + a.tps - 1) / a.tps;
   const int ct0 = (int)((a.q[0].d + 63) / 64), ct1 = (int)((a.q[1].d + 63) / 64);
-  const int64_t items = (int64_t)splits * (ct0 + ct1);
+  const int ct01 = ct0 + ct1;
+  int splits = (tiles + a.tps - 1) / a.tps;
+  int4 sp = {0, 0, 0, 0};
+  int first = 0;
+  if (a.plan.head) {
+    // (in bounds whatever the plan holds: the grid stops at its room)
+    const int s0 = (int)min((int64_t)blockIdx.x / ct01, (int64_t)a.most - 1);
+    sp = a.plan.split[s0];
+    first = a.plan.split_first[s0];
+    if (!plan_fits(a.plan, a.M, a.slots)) return;
+    splits = a.plan.head[kPlanSplits];
+  }
+  const int64_t items = (int64_t)splits * ct01;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int si = (int)(item / (ct0 + ct1));
-    int ct = (int)(item % (ct0 + ct1));
+    const int si = (int)(item / ct01);
+    int ct = (int)(item % ct01);
     const int side = ct >= ct0 ? 1 : 0;
     if (side) ct -= ct0;
     const GramSide& q = a.q[side];
-    int4 sp;
-    int first;
     int64_t part = -1;
     if (a.plan.head) {
-      sp = a.plan.split[si];
-      first = a.plan.split_first[si];
+      if (item != blockIdx.x) {
+        sp = a.plan.split[si];
+        first = a.plan.split_first[si];
+      }
       if (sp.w >= 0) part = a.plan.parts[sp.x].x + sp.w;
     } else {
       first = 64 * si * a.tps;
@@ -1168,13 +1243,13 @@ __global__ __launch_bounds__(256, NB <= 4 ? 2 : 1) void k_gram8(GramArgs8 a) {
     float* out = part >= 0 ? q.part + part * a.r * q.d : q.out + (int64_t)sp.x * a.r * q.d;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      __syncthreads();
+      lds_barrier();
 #pragma unroll
       for (int cb = 0; cb < 4; ++cb)
 #pragma unroll
         for (int v = 0; v < 4; ++v)
           red[(w * 16 + 4 * g + v) * LR + 16 * cb + r16] = acc[nb][cb][v];
-      __syncthreads();
+      lds_barrier();
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int e = threadIdx.x + 256 * u;
@@ -1186,12 +1261,12 @@ __global__ __launch_bounds__(256, NB <= 4 ? 2 : 1) void k_gram8(GramArgs8 a) {
           out[side ? (c0 + c) * a.r + 16 * nb + i : (16 * nb + i) * q.d + c0 + c] = sum;
       }
     }
-    __syncthreads();
+    lds_barrier();
   }
 }
 
-// Gradients of slots with several splits (their parts added in order) and of
-// slots without tokens (zeros).
+// Gradients of slots with several splits: their parts added in order (none:
+// zeros).
 __global__ __launch_bounds__(256) void k_gram_sum(GramArgs8 a, int n_parts) {
   if (a.plan.head && !plan_fits(a.plan, a.M, a.slots)) return;
   const int64_t size0 = a.r * a.q[0].d, size1 = a.r * a.q[1].d;
@@ -1202,7 +1277,7 @@ __global__ __launch_bounds__(256) void k_gram_sum(GramArgs8 a, int n_parts) {
     int64_t ch = item % (ch0 + ch1);
     int2 pt = int2{0, n_parts};
     if (a.plan.head) pt = a.plan.parts[slot];
-    if (pt.y == 1) continue;
+    if (pt.y == 1 || (a.plan.head && pt.y == 0)) continue;
     const int side = ch >= ch0 ? 1 : 0;
     if (side) ch -= ch0;
     const GramSide& q = a.q[side];
@@ -1219,57 +1294,66 @@ __global__ __launch_bounds__(256) void k_gram_sum(GramArgs8 a, int n_parts) {
   }
 }
 
+constexpr int64_t kMostGrid = 4096;
+
 template <typename K>
 hipError_t allow_lds(K kernel, int bytes) {
   return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <int NB, bool KN, bool R8>
+template <int NB, bool KN, bool FAST>
 hipError_t launch_shrink_t(const ShrinkArgs& a, unsigned grid, hipStream_t st) {
   constexpr int lds = shrink_lds<NB, KN>();
-  static const hipError_t attr = allow_lds(&k_shrink<NB, KN, R8>, lds);
+  static const hipError_t attr = allow_lds(&k_shrink<NB, KN, FAST>, lds);
   if (attr != hipSuccess) return attr;
-  hipLaunchKernelGGL((k_shrink<NB, KN, R8>), dim3(grid), dim3(64 * shrink_waves<NB>()), lds, st,
-                     a);
+  hipLaunchKernelGGL((k_shrink<NB, KN, FAST>), dim3(grid), dim3(64 * kShrinkWaves), lds, st, a);
   return hipGetLastError();
 }
 template <int NB>
 hipError_t launch_shrink_nb(const ShrinkArgs& a, unsigned grid, hipStream_t st) {
-  if (!a.kn) return launch_shrink_t<NB, false, true>(a, grid, st);
-  return a.r % 8 == 0 ? launch_shrink_t<NB, true, true>(a, grid, st)
-                      : launch_shrink_t<NB, true, false>(a, grid, st);
+  const bool fast = a.K >= 8 && (!a.kn || a.r % 8 == 0);
+  if (a.kn) return fast ? launch_shrink_t<NB, true, true>(a, grid, st)
+                        : launch_shrink_t<NB, true, false>(a, grid, st);
+  return fast ? launch_shrink_t<NB, false, true>(a, grid, st)
+              : launch_shrink_t<NB, false, false>(a, grid, st);
 }
 
-template <int KS, bool RD, bool R8, bool DEEP>
+template <int KS, bool RD, bool R8, bool DEEP, bool SUMS>
 hipError_t launch_expand_t(const ExpandArgs& a, unsigned grid, hipStream_t st) {
   constexpr int few = RD ? 4 * 32 * 72 * 2 : 0, many = kTurnBytes + expand_lds<KS, RD>();
   constexpr int lds = many > few ? many : few;
-  static const hipError_t attr = allow_lds(&k_expand<KS, RD, R8, DEEP>, lds);
+  static const hipError_t attr = allow_lds(&k_expand<KS, RD, R8, DEEP, SUMS>, lds);
   if (attr != hipSuccess) return attr;
-  hipLaunchKernelGGL((k_expand<KS, RD, R8, DEEP>), dim3(grid), dim3(256), lds, st, a);
+  hipLaunchKernelGGL((k_expand<KS, RD, R8, DEEP, SUMS>), dim3(grid), dim3(256), lds, st, a);
   return hipGetLastError();
 }
 template <int KS, bool RD, bool R8>
-hipError_t launch_expand_deep(const ExpandArgs& a, unsigned grid, hipStream_t st) {
-  return a.tpi > 1 ? launch_expand_t<KS, RD, R8, true>(a, grid, st)
-                   : launch_expand_t<KS, RD, R8, false>(a, grid, st);
+hipError_t launch_expand_mode(const ExpandArgs& a, unsigned grid, hipStream_t st) {
+  // (expand_sums: the forward of few tokens and ranks)
+  if constexpr (!RD && KS <= 2)
+    if (a.part) return launch_expand_t<KS, RD, R8, false, true>(a, grid, st);
+  return a.tpi > 1 ? launch_expand_t<KS, RD, R8, true, false>(a, grid, st)
+                   : launch_expand_t<KS, RD, R8, false, false>(a, grid, st);
 }
 template <int KS>
 hipError_t launch_expand_ks(const ExpandArgs& a, unsigned grid, hipStream_t st) {
-  if (a.rd) return launch_expand_deep<KS, true, true>(a, grid, st);
-  return a.r % 8 == 0 ? launch_expand_deep<KS, false, true>(a, grid, st)
-                      : launch_expand_deep<KS, false, false>(a, grid, st);
+  if (a.rd) return launch_expand_mode<KS, true, true>(a, grid, st);
+  return a.r % 8 == 0 ? launch_expand_mode<KS, false, true>(a, grid, st)
+                      : launch_expand_mode<KS, false, false>(a, grid, st);
 }
 
 template <int NB>
-hipError_t launch_gram8_nb(const GramArgs8& a, unsigned grid, hipStream_t st) {
+hipError_t launch_gram8_nb(GramArgs8 a, hipStream_t st) {
+  const int64_t tiles = (a.M + 63) / 64;
+  a.most = (int)(a.plan.head ? plan_most_splits(a.M, a.slots) : (tiles + a.tps - 1) / a.tps);
+  const int64_t cols = (a.q[0].d + 63) / 64 + (a.q[1].d + 63) / 64;
+  const unsigned grid = (unsigned)std::min<int64_t>(a.most * cols, 2 * kMostGrid);
   if (a.q[0].codes) hipLaunchKernelGGL((k_gram8<NB, true>), dim3(grid), dim3(256), 0, st, a);
   else hipLaunchKernelGGL((k_gram8<NB, false>), dim3(grid), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
-constexpr int64_t kMostGrid = 4096;
 
 }  // namespace
 
@@ -1307,8 +1391,8 @@ hipError_t launch_shrink(const ShrinkArgs& a0, hipStream_t st) {
   ShrinkArgs a = a0;
   a.splits = shrink_splits(a.M, a.K, &a.kper);
   if (a.splits > 1) a.vrows = nullptr;             // k_finish forms V
-  const unsigned grid =
-      (unsigned)std::min<int64_t>(plan_most_tiles(a.M, a.slots) * a.splits, kMostGrid);
+  const int64_t tiles = a.plan.head ? plan_most_tiles(a.M, a.slots) : (a.M + 63) / 64;
+  const unsigned grid = (unsigned)std::min<int64_t>(tiles * a.splits, kMostGrid);
   if (a.r <= 16) return launch_shrink_nb<1>(a, grid, st);
   if (a.r <= 32) return launch_shrink_nb<2>(a, grid, st);
   if (a.r <= 64) return launch_shrink_nb<4>(a, grid, st);
@@ -1321,7 +1405,8 @@ hipError_t launch_expand(const ExpandArgs& a0, hipStream_t st) {
   a.chunks = (int)((a.d + kExpandCols - 1) / kExpandCols);
   // more tiles an item where there are enough items
   const int64_t tiles = (a.M + kPlanTile - 1) / kPlanTile;
-  a.tpi = (int)std::max<int64_t>(1, std::min<int64_t>(8, tiles * a.chunks / EXPAND_WGS));
+  a.tpi = (int)std::max<int64_t>(1, std::min<int64_t>(8, tiles * a.chunks / 1024));
+  if (a.part) a.tpi = 1;
   const bool deep = a.tpi > 1;
   a.subs = deep ? (plan_split_tiles(a.M) + a.tpi - 1) / a.tpi : 1;
   a.most = (int)(deep ? plan_most_splits(a.M, a.slots) : plan_most_tiles(a.M, a.slots));
@@ -1337,29 +1422,31 @@ hipError_t launch_finish_v(const FinishVArgs& f0, hipStream_t st) {
   FinishVArgs f = f0;
   f.nb = frag_blocks(f.r);
   const int64_t tiles = f.plan.head ? plan_most_tiles(f.M, f.slots) : (f.M + 63) / 64;
-  const int64_t items = tiles * ((f.nb + 3) / 4) * (f.t_frags ? 2 : 1);
-  hipLaunchKernelGGL(k_finish, dim3((unsigned)std::min<int64_t>(items, kMostGrid)), dim3(256), 0, st,
-                     f);
+  f.most = (int)tiles;
+  if (f.rp == 0) f.rp = (int)vrow_ranks(f.r);
+  int64_t items = tiles * 2 * ((f.nb + 3) / 4) * (f.t_frags ? 2 : 1);
+  if (f.zero_a) items = std::max<int64_t>(items, std::min<int64_t>(f.slots * ((f.r * (f.d_a + f.d_b) + 4095) / 4096), 1024));
+  const dim3 grid((unsigned)std::min<int64_t>(items, kMostGrid));
+  if (f.splits <= 4) hipLaunchKernelGGL(k_finish<4>, grid, dim3(256), 0, st, f);
+  else hipLaunchKernelGGL(k_finish<kShrinkSplits>, grid, dim3(256), 0, st, f);
   return hipGetLastError();
 }
 
 hipError_t launch_gram8(const GramArgs8& a, hipStream_t st) {
   const int64_t tiles = (a.M + 63) / 64;
   hipError_t e = hipSuccess;
-  const int64_t splits =
-      a.plan.head ? plan_most_splits(a.M, a.slots) : (tiles + a.tps - 1) / a.tps;
-  const int64_t cols = (a.q[0].d + 63) / 64 + (a.q[1].d + 63) / 64;
-  const unsigned grid = (unsigned)std::min<int64_t>(splits * cols, 2 * kMostGrid);
+  const int64_t splits = (tiles + a.tps - 1) / std::max(a.tps, 1);
   switch (frag_blocks(a.r)) {
-    case 1: e = launch_gram8_nb<1>(a, grid, st); break;
-    case 2: e = launch_gram8_nb<2>(a, grid, st); break;
-    case 4: e = launch_gram8_nb<4>(a, grid, st); break;
-    case 8: e = launch_gram8_nb<8>(a, grid, st); break;
-    default: e = launch_gram8_nb<16>(a, grid, st);
+    case 1: e = launch_gram8_nb<1>(a, st); break;
+    case 2: e = launch_gram8_nb<2>(a, st); break;
+    case 4: e = launch_gram8_nb<4>(a, st); break;
+    case 8: e = launch_gram8_nb<8>(a, st); break;
+    default: e = launch_gram8_nb<16>(a, st);
   }
   if (e != hipSuccess) return e;
-  // without a plan one split leaves nothing to add
-  if (!a.plan.head && splits <= 1) return hipSuccess;
+  // with one split a slot at most nothing is left to add
+  if (a.plan.head ? a.M <= int64_t(kPlanTile) * plan_split_tiles(a.M) : splits <= 1)
+    return hipSuccess;
   const int64_t chunks = (a.r * a.q[0].d + 1023) / 1024 + (a.r * a.q[1].d + 1023) / 1024;
   hipLaunchKernelGGL(k_gram_sum, dim3((unsigned)std::min<int64_t>(a.slots * chunks, 2 * kMostGrid)),
                      dim3(256), 0, st, a, (int)splits);

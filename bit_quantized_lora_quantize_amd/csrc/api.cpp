@@ -197,7 +197,7 @@ BwdPlan plan_bwd(int64_t d_out, int64_t d_in, int64_t M, int64_t r, void* ws) {
 // Backward from an input kept in 8 bits, after the region of plan_bwd: U in
 // FP32, the operands of the token contractions and their partial results.
 struct PackedPlan {
-  float* u;                     // [M][r]
+  float* u;                     // [splits][M][r]: partial sums of U
   uint16_t *t_frags, *u_frags;
   int tps;                      // tiles a token split
   float *da_part, *db_part;     // [splits][r][d_in], [splits][d_out][r]
@@ -212,7 +212,8 @@ PackedPlan plan_packed(size_t base_bytes, int64_t d_out, int64_t d_in, int64_t M
   const int64_t tiles = cdiv(M, kPlanTile);
   p.tps = plan_split_tiles(std::max<int64_t>(M, 1));
   const int64_t splits = cdiv(tiles, p.tps), parts = splits > 1 ? splits : 0;
-  p.u = c.take<float>(M * r);
+  int64_t kper;
+  p.u = c.take<float>(shrink_splits(M, d_out, &kper) * M * r);
   p.t_frags = c.take<uint16_t>(frag_elems(tiles, r));
   p.u_frags = c.take<uint16_t>(frag_elems(tiles, r));
   p.da_part = c.take<float>(parts * r * d_in);
@@ -634,16 +635,33 @@ int bwd_packed_impl(const qlora_nf4_t* q, const qlora_packed_t* X8, const uint16
     }
     sc /= 1.0f - drop->p;
   }
-  // U = s dY B as in bwd_impl, in FP32 and, for the input gradient, as hi | lo
-  const bool b_as_stored = M > kSmallM && d_out % 8 == 0 && r % 8 == 0 && aligned16(B);
-  if (!b_as_stored) {
-    s = hip_status(launch_transpose_bf16(B, d_out, r, p.bt, p.ldbt, st));
-    if (s) return s;
-  }
-  RankRowsArgs ra{dY, b_as_stored ? B : p.bt, M, r, d_out, b_as_stored ? r : p.ldbt, sc, pp.u,
-                  dX ? p.u_hl : nullptr, p.rp, nullptr, nullptr, 0};
-  ra.q_kn = b_as_stored;
-  s = rank_product(ra, p.r_part, st);
+  // U = s dY B (partial sums), then as the input gradient's hi | lo rows and,
+  // with T, as the contractions' operands
+  ShrinkArgs sa{};
+  sa.M = M;
+  sa.slots = 1;
+  sa.K = d_out;
+  sa.r = (int)r;
+  sa.kn = true;
+  sa.P = dY;
+  sa.F = B;
+  sa.part = pp.u;
+  s = hip_status(launch_shrink(sa, st));
+  if (s) return s;
+  int64_t kper;
+  FinishVArgs fa{};
+  fa.M = M;
+  fa.slots = 1;
+  fa.r = (int)r;
+  fa.rp = (int)p.rp;
+  fa.splits = shrink_splits(M, d_out, &kper);
+  fa.one_scale = sc;
+  fa.V = pp.u;
+  fa.T = T;
+  fa.vrows = dX ? p.u_hl : nullptr;
+  fa.u_frags = pp.u_frags;
+  fa.t_frags = pp.t_frags;
+  s = hip_status(launch_finish_v(fa, st));
   if (s) return s;
   if (dX) {
     GemmArgs g{q->codes, q->scale_codes, q->scale2, q->scale_mean, dY, p.u_hl, A, dX,
@@ -651,16 +669,6 @@ int bwd_packed_impl(const qlora_nf4_t* q, const qlora_packed_t* X8, const uint16
     s = hip_status(launch_gemm_bwd(g, st));
     if (s) return s;
   }
-  FinishVArgs fa{};
-  fa.M = M;
-  fa.slots = 1;
-  fa.r = (int)r;
-  fa.V = pp.u;
-  fa.T = T;
-  fa.u_frags = pp.u_frags;
-  fa.t_frags = pp.t_frags;
-  s = hip_status(launch_finish_v(fa, st));
-  if (s) return s;
   ga.q[0].codes = X8->codes;
   ga.q[0].scale = X8->scale;
   ga.q[0].keep = rows;

@@ -175,7 +175,8 @@ int qlora_adapters_fwd(const qlora_adapters_t* bank, const void* plan, size_t pl
   if (s) return s;
   int64_t kper;
   const int splits = shrink_splits(M, bank->d_in, &kper);
-  if (splits > 1) {
+  const bool sums = splits > 1 && expand_sums(M, bank->r);
+  if (splits > 1 && !sums) {
     FinishVArgs fa{};
     fa.plan = v;
     fa.M = M;
@@ -196,6 +197,9 @@ int qlora_adapters_fwd(const qlora_adapters_t* bank, const void* plan, size_t pl
   ea.d = bank->d_out;
   ea.r = (int)bank->r;
   ea.vrows = w.vrows;
+  ea.part = sums ? w.part : nullptr;
+  ea.splits = splits;
+  ea.scale = bank->scale;
   ea.F = bank->B;
   ea.in = Y0;
   ea.out = Y;
@@ -259,6 +263,10 @@ int qlora_adapters_bwd(const qlora_adapters_t* bank, const void* plan, size_t pl
   fa.vrows = dX ? w.vrows : nullptr;
   fa.u_frags = w.u_frags;
   fa.t_frags = w.t_frags;
+  fa.zero_a = dA;
+  fa.zero_b = dB;
+  fa.d_a = bank->d_in;
+  fa.d_b = bank->d_out;
   s = hip_status(launch_finish_v(fa, st));
   if (s) return s;
   if (dX) {
@@ -277,6 +285,7 @@ int qlora_adapters_bwd(const qlora_adapters_t* bank, const void* plan, size_t pl
     if (s) return s;
   }
   ga.plan = v;
+  ga.tps = plan_split_tiles(M);
   ga.q[0].x = X;
   if (X8) {
     ga.q[0].codes = X8->codes;

@@ -587,11 +587,13 @@ struct PlanView {
   int2* parts;     // [slots] {its splits' first partial result, its splits}
   int32_t* hist;   // scratch of the plan's own kernels
 };
-// Tiles of a token split of the weight gradients: four splits or more from 256
-// tokens a split on, at most about 64 splits of one slot.
+// Tiles of a token split of the weight gradients: 8 to 16 (four splits of one
+// slot where that gives them), more where one slot would have 64 splits and more.
+// Half as many (2048 tokens, 4096 x 4096, rank 64) took 26 us instead of 20 and
+// 10 instead of 6 to add the parts.
 inline int plan_split_tiles(int64_t M) {
   const int64_t tiles = (M + kPlanTile - 1) / kPlanTile;
-  const int64_t four = std::min<int64_t>(16, std::max<int64_t>(4, (tiles + 3) / 4));
+  const int64_t four = std::min<int64_t>(16, std::max<int64_t>(8, (tiles + 3) / 4));
   return (int)std::max<int64_t>(four, (tiles + 63) / 64);
 }
 // Bounds of what the device counts.
@@ -609,14 +611,15 @@ inline int64_t plan_most_parts(int64_t M) {
 hipError_t launch_plan(const PlanView& p, const int32_t* index, int64_t M, int64_t slots,
                        hipStream_t st);
 
-// Ranges of the long axis K that k_shrink sums apart.
-#ifndef SHRINK_WGS
-#define SHRINK_WGS 1024
-#endif
+// Ranges of the long axis K that k_shrink sums apart, for about 1024 items: two
+// workgroups a compute unit, several times over, so that one's start and end
+// overlap another's loads.  16384 tokens: K 4096, rank 64 in four ranges 49 us, in
+// two 58, in one 82; K 11008, rank 16 in four 79, in two 100.
+constexpr int kShrinkSplits = 8;   // at most
 inline int shrink_splits(int64_t M, int64_t K, int64_t* kper) {
   const int64_t tiles = std::max<int64_t>(1, (M + kPlanTile - 1) / kPlanTile);
-  int64_t s = std::min<int64_t>((SHRINK_WGS + tiles - 1) / tiles, (K + 255) / 256);
-  s = std::max<int64_t>(1, std::min<int64_t>(s, tiles >= 32 ? 8 : 16));
+  int64_t s = std::min<int64_t>((1024 + tiles - 1) / tiles, (K + 255) / 256);
+  s = std::max<int64_t>(1, std::min<int64_t>(s, kShrinkSplits));
   *kper = ((K + s - 1) / s + 255) / 256 * 256;
   return (int)((K + *kper - 1) / *kper);
 }
@@ -640,15 +643,21 @@ hipError_t launch_shrink(const ShrinkArgs& a, hipStream_t st);
 struct FinishVArgs {
   PlanView plan;
   int64_t M, slots;
-  int r, nb;               // nb: set by launch_finish_v
+  int r, nb, most;         // nb, most: set by launch_finish_v
+  int rp;                  // ranks of a row of vrows; 0: vrow_ranks(r)
   int splits;              // partial sums in V by position; 0: V by token, as it is
-  const float* scale;      // [slots], with splits
+  const float* scale;      // [slots], with splits; NULL: one_scale
+  float one_scale;
   const float* V;
   const float* T;          // [M][r] by token, with t_frags
   uint16_t* vrows;         // outputs, each or NULL
   float* v_out;
   uint16_t* u_frags;       // V's
   uint16_t* t_frags;       // T's
+  // with a plan: gradients of the slots without tokens, to be cleared, or NULL
+  float* zero_a;           // [slots][r d_a]
+  float* zero_b;           // [slots][r d_b]
+  int64_t d_a, d_b;
 };
 hipError_t launch_finish_v(const FinishVArgs& a, hipStream_t st);
 // Blocks of 16 ranks in the operands of the contractions.
@@ -663,12 +672,20 @@ struct ExpandArgs {
   int64_t M, slots, d;
   int r, chunks, subs, tpi, most;   // all but r set by launch_expand
   bool rd;                 // F as [r][d] (else [d][r])
-  const uint16_t* vrows;   // [M][2 vrow_ranks(r)] by position
+  const uint16_t* vrows;   // [M][2 vrow_ranks(r)] by position, or
+  const float* part;       // (expand_sums) k_shrink's partial sums,
+  int splits;              // so many, with
+  const float* scale;      // [slots]
   const uint16_t* F;       // [slots] of them
   const uint16_t* in;      // [M][d], NULL: zeros; may be out
   uint16_t* out;
-  float* v_out;            // [M][r] or NULL: zeros for tokens without an adapter
+  float* v_out;            // [M][r] or NULL: V (from partial sums), zeros without an adapter
 };
+// Whether the forward's expansion adds the partial sums itself, in every
+// workgroup again, rather than have k_finish do it once in a launch of its own:
+// one token 9 us in two kernels and 12 in three, 64 decoding 15 and 16.5, 1531
+// tokens (4096 -> 1003, rank 20) 20 and 24.5.
+inline bool expand_sums(int64_t M, int64_t r) { return M <= 2048 && r <= 64 && r % 4 == 0; }
 hipError_t launch_expand(const ExpandArgs& a, hipStream_t st);
 
 struct GramSide {
@@ -684,7 +701,8 @@ struct GramSide {
 struct GramArgs8 {
   PlanView plan;
   int64_t M, slots, r;
-  int tps;                 // without a plan: tiles a split
+  int tps;                 // tiles a split
+  int most;                // set by launch_gram8
   GramSide q[2];           // dA from (U, X), dB from (T, dY)
 };
 hipError_t launch_gram8(const GramArgs8& a, hipStream_t st);

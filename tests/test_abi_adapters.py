@@ -169,7 +169,7 @@ def test_bounds_of_the_plans_lists():
             counts.append(take)
             left -= take
         tiles = cdiv(M, 64)
-        tps = max(min(16, max(4, cdiv(tiles, 4))), cdiv(tiles, 64))
+        tps = max(min(16, max(8, cdiv(tiles, 4))), cdiv(tiles, 64))
         t = [cdiv(c, 64) for c in counts]
         s = [cdiv(x, tps) for x in t]
         assert sum(t) + cdiv(left, 64) <= min(M, M // 64 + slots + 1)

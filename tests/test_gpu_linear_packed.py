@@ -58,8 +58,9 @@ def test_backward(M, d_in, d_out, r):
     want, bound = _exact(w, back, T, dY, A, B, 2.0)
     for name, got in (("dA", dA), ("dB", dB), ("dX", dX)):
         ref.inside(got, want[name], bound[name], name)
-    # dX does not see X: the same bits as from the BF16 input
-    assert torch.equal(dX, q.qlora_linear_bwd(w, back, dYd, Ad, Bd, alpha, T_saved=T)[0])
+    # dX does not see X: two roundings of the same sum from the BF16 input's
+    other = q.qlora_linear_bwd(w, back, dYd, Ad, Bd, alpha, T_saved=T)[0]
+    ref.inside(dX, ref.f64(other), 2 * bound["dX"], "dX against the BF16 input's")
     none, dA2, dB2 = q.qlora_linear_bwd_packed(w, X8, dYd, Ad, Bd, alpha, T, need_dx=False)
     assert none is None and torch.equal(dA2, dA) and torch.equal(dB2, dB)
 
@@ -85,8 +86,8 @@ def test_dropout(M, saved):
     want, bound = _exact(w, back, T, dY, A, B, s, keep)
     for name, got in (("dA", dA), ("dB", dB), ("dX", dX)):
         ref.inside(got, want[name], bound[name], name)
-    again = q.qlora_linear_bwd_dropout(w, back, dYd, Ad, Bd, 32.0, drop, T_saved=T)
-    assert torch.equal(dX, again[0])
+    other = q.qlora_linear_bwd_dropout(w, back, dYd, Ad, Bd, 32.0, drop, T_saved=T)[0]
+    ref.inside(dX, ref.f64(other), 2 * bound["dX"], "dX against the BF16 input's")
 
 
 def test_without_dropped_elements_as_without_dropout():
