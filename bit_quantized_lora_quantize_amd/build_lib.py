@@ -47,7 +47,7 @@ SAN_FLAGS = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=und
 TIMED_SOURCES = ["quant.hip", "gemv.hip", "gemm.hip", "api.cpp"]
 
 SOURCES = ["quant.hip", "quant_blocked.hip", "lora.hip", "gemv.hip", "gemm.hip", "merge.hip", "optim.hip", "dropout.hip", "noalloc.hip",
-           "norm.hip", "logits.hip", "pack8.hip", "adapters.hip", "api.cpp", "api_train.cpp",
+           "norm.hip", "logits.hip", "pack8.hip", "adapters.hip", "dx_few.hip", "api.cpp", "api_train.cpp",
            "api_adapters.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -85,6 +85,16 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// Ranks past 64 are worked on in groups of 64, items of their own: the groups of
+// one item are eight workgroups apart, so that they run on one XCD and share what
+// they read in its L2.  (All 128 ranks in one workgroup left one wavefront a SIMD.)
+__device__ __forceinline__ int64_t ranked(int64_t item, int groups, int64_t items, int& group) {
+  const int64_t block = item / (8 * groups), rest = item % (8 * groups);
+  const int64_t left = items - 8 * block, width = left < 8 ? left : 8;
+  group = (int)(rest / width);
+  return 8 * block + rest % width;
+}
+
 // A plan of other sizes than the call's: nothing is done for it.
 __device__ __forceinline__ bool plan_fits(const PlanView& p, int64_t M, int64_t slots) {
   return p.head[kPlanMagicAt] == kPlanMagic && p.head[kPlanTokens] == (int)M &&
@@ -320,7 +330,7 @@ constexpr int kShrinkWaves = 4;
 // K slices of 32 per step: two, whole lines of a row, where their loads fit the
 // registers beside the sums.
 template <int NB>
-constexpr int shrink_slices() { return NB <= 4 ? 2 : 1; }
+constexpr int shrink_slices() { return 2; }
 template <int NB, bool KN>
 constexpr int shrink_lds() {
   constexpr int CN = NB < 4 ? NB : 4;
@@ -341,7 +351,7 @@ __device__ __forceinline__ void put_vrow(uint16_t* vrows, int64_t pos, int i, in
 // One item with RB blocks of 16 tokens.  FAST: K of eight or
 // more and, KN, rows of F that are whole 16-byte pieces.
 template <int NB, bool KN, bool FAST, int RB>
-__device__ __forceinline__ void shrink_item(const ShrinkArgs& a, const int4& td, int s, uint8_t* lds) {
+__device__ __forceinline__ void shrink_item(const ShrinkArgs& a, const int4& td, int s, int i0, uint8_t* lds) {
   constexpr int W = kShrinkWaves, CN = NB < 4 ? NB : 4, SK = shrink_slices<NB>();
   constexpr int LF = 16 * NB + 8;                  // staged row of F, elements
   constexpr int STEP = 32 * SK;
@@ -375,10 +385,10 @@ __device__ __forceinline__ void shrink_item(const ShrinkArgs& a, const int4& td,
 #pragma unroll
     for (int u = 0; u < SK * NB; ++u) {
       if (KN) {
-        const int piece = lane + 64 * u, row = min(piece / (2 * NB), rows), col = 8 * (piece % (2 * NB));
+        const int piece = lane + 64 * u, row = min(piece / (2 * NB), rows), col = i0 + 8 * (piece % (2 * NB));
         f[u] = load_vec(F + (k + row) * r + (col < r ? col : 0));
       } else {
-        const int i = min(16 * (u / SK) + r16, r - 1);
+        const int i = min(i0 + 16 * (u / SK) + r16, r - 1);
         f[u] = load_vec(F + i * K + k + off[u % SK]);
       }
     }
@@ -456,11 +466,11 @@ __device__ __forceinline__ void shrink_item(const ShrinkArgs& a, const int4& td,
 #pragma unroll
       for (int u = 0; u < SK * NB; ++u) {
         if (KN) {
-          const int piece = lane + 64 * u, row = piece / (2 * NB), col = 8 * (piece % (2 * NB));
+          const int piece = lane + 64 * u, row = piece / (2 * NB), col = i0 + 8 * (piece % (2 * NB));
           const int64_t at = k + row < k_end ? k + row : k_end - 1;
           f[u] = only_if(k + row < k_end, load8(F + at * r, col, r));
         } else {
-          f[u] = load8(F + min(16 * (u / SK) + r16, r - 1) * K, k + off[u % SK], k_end);
+          f[u] = load8(F + min(i0 + 16 * (u / SK) + r16, r - 1) * K, k + off[u % SK], k_end);
         }
       }
     }
@@ -486,7 +496,7 @@ __device__ __forceinline__ void shrink_item(const ShrinkArgs& a, const int4& td,
       for (int e0 = 0; e0 < 256 * CN; e0 += 64 * W) {
         const int e = e0 + threadIdx.x;
         if (256 * CN % (64 * W) != 0 && e >= 256 * CN) break;
-        const int row = e / (16 * CN), i = 16 * n0 + e % (16 * CN);
+        const int row = e / (16 * CN), i = i0 + 16 * n0 + e % (16 * CN);
         float sum = red[e];
 #pragma unroll
         for (int ww = 1; ww < W; ++ww) sum += red[ww * 256 * CN + e];
@@ -494,7 +504,7 @@ __device__ __forceinline__ void shrink_item(const ShrinkArgs& a, const int4& td,
         if (a.vrows) {
           const int pos = first + 16 * rb + row;
           const float v = i < r ? sum * sc : 0.0f;
-          put_vrow(a.vrows, pos, i, 32 * ((NB + 1) / 2), v);
+          put_vrow(a.vrows, pos, i, a.rp, v);
           if (NB == 1) put_vrow(a.vrows, pos, i + 16, 32, 0.0f);
           if (a.v_out && i < r) a.v_out[(int64_t)a.plan.order[pos] * r + i] = v;
         } else if (i < r) {
@@ -507,24 +517,27 @@ __device__ __forceinline__ void shrink_item(const ShrinkArgs& a, const int4& td,
 }
 
 template <int NB, bool KN, bool FAST>
-__global__ __launch_bounds__(64 * kShrinkWaves, NB <= 4 ? 2 : 1) void k_shrink(ShrinkArgs a) {
+__global__ __launch_bounds__(64 * kShrinkWaves, 2) void k_shrink(ShrinkArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t slds[];
   int4 td = {0, 0, 0, 0};
+  const int t0 = min((int)(blockIdx.x / a.groups) / a.splits, a.most - 1);
   int tiles = (int)((a.M + 63) / 64);
   if (a.plan.head) {
     // the grid has no more workgroups than the list room for items
-    td = a.plan.tile[blockIdx.x / a.splits];
-    if (!plan_fits(a.plan, a.M, a.slots) || td.z <= 0) return;
+    td = a.plan.tile[t0];
+    if (!plan_fits(a.plan, a.M, a.slots)) return;
     tiles = a.plan.head[kPlanTiles];
   }
   const int items = tiles * a.splits;
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+  for (int it = blockIdx.x; it < items * a.groups; it += gridDim.x) {
+    int group;
+    const int item = (int)ranked(it, a.groups, items, group);
     const int t = item / a.splits, s = item % a.splits;
     if (!a.plan.head) td = int4{0, 64 * t, (int)min((int64_t)64, a.M - 64 * (int64_t)t), 0};
-    else if (item != (int)blockIdx.x) td = a.plan.tile[t];
+    else if (t != t0) td = a.plan.tile[t];
     // few tokens: no registers and loads for blocks of tokens that are not there
-    if (td.z <= 16) shrink_item<NB, KN, FAST, 1>(a, td, s, slds);
-    else shrink_item<NB, KN, FAST, 4>(a, td, s, slds);
+    if (td.z <= 16) shrink_item<NB, KN, FAST, 1>(a, td, s, 64 * group, slds);
+    else shrink_item<NB, KN, FAST, 4>(a, td, s, 64 * group, slds);
   }
 }
 
@@ -1128,9 +1141,8 @@ __device__ __forceinline__ void gram_stage(const GramTile& t, int lane, uint16_t
 // sp: {slot, first tile, tokens, }, `first` the split's first position.
 template <int NB, bool PACKED>
 __device__ __forceinline__ void gram_item(const GramArgs8& a, const GramSide& q, int64_t c0,
-                                          const int4& sp, int first, uint16_t* st,
-                                          f32x4 (&acc)[NB][4]) {
-  constexpr int CN = NB < 4 ? NB : 4, NC = NB / CN, C = 2 * NC;   // operand chunks of a tile
+                                          const int4& sp, int first, int group,
+                                          uint16_t* st, f32x4 (&acc)[NB][4]) {
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
   const int tiles = (sp.z + 63) / 64;
@@ -1139,14 +1151,13 @@ __device__ __forceinline__ void gram_item(const GramArgs8& a, const GramSide& q,
     if (at >= sp.z) return -1;
     return a.plan.head ? a.plan.order[first + at] : first + at;
   };
-  // chunk c: CN blocks of 16 ranks, three terms, of 32 tokens
-  auto load_v = [&](const uint16_t* fr, int c, u32x4 (&v)[CN][3]) {
+  // the group's blocks of 16 ranks, three terms, of 32 tokens
+  auto load_v = [&](const uint16_t* fr, int slice, u32x4 (&v)[NB][3]) {
 #pragma unroll
-    for (int n = 0; n < CN; ++n)
+    for (int n = 0; n < NB; ++n)
 #pragma unroll
       for (int term = 0; term < 3; ++term)
-        v[n][term] = *reinterpret_cast<const u32x4*>(
-            fr + ((term * NB + (c % NC) * CN + n) * 2 + c / NC) * 512);
+        v[n][term] = *reinterpret_cast<const u32x4*>(fr + ((term * a.nb + NB * group + n) * 2 + slice) * 512);
   };
   if (w >= tiles) return;
   int next = token(w);
@@ -1155,41 +1166,36 @@ __device__ __forceinline__ void gram_item(const GramArgs8& a, const GramSide& q,
   next = token(w + 4);
   for (int j = w; j < tiles; j += 4) {
     // in the order of their use: this tile's operands, the next tile's rows
-    const uint16_t* fr = q.frags + (int64_t)(sp.y + j) * 3 * NB * 2 * 512 + lane * 8;
-    u32x4 v[2][CN][3], b[4];
+    const uint16_t* fr = q.frags + (int64_t)(sp.y + j) * 3 * a.nb * 2 * 512 + lane * 8;
+    u32x4 v[2][NB][3];
     load_v(fr, 0, v[0]);
     gram_stage<PACKED>(cur, lane, st);
+    load_v(fr, 1, v[1]);
+    if (j + 4 < tiles) {
+      gram_load<PACKED>(q, a.M, c0, next, lane, cur);
+      next = token(j + 8);
+    }
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      if (c + 1 < C) load_v(fr, c + 1, v[(c + 1) & 1]);
-      if (c + 2 == C && j + 4 < tiles) {
-        gram_load<PACKED>(q, a.M, c0, next, lane, cur);
-        next = token(j + 8);
-      }
-      if (c % NC == 0) {
-        const int slice = c / NC;
+    for (int slice = 0; slice < 2; ++slice) {
+      u32x4 b[4];
 #pragma unroll
-        for (int cb = 0; cb < 4; ++cb) {
-          const uint16_t* p = st + (32 * slice + 8 * g + (r16 >> 2)) * kGL + 16 * cb + 4 * (r16 & 3);
-          const uint2 lo = lds_tr(p), hi = lds_tr(p + 4 * kGL);
-          b[cb] = u32x4{lo.x, lo.y, hi.x, hi.y};
-        }
+      for (int cb = 0; cb < 4; ++cb) {
+        const uint16_t* p = st + (32 * slice + 8 * g + (r16 >> 2)) * kGL + 16 * cb + 4 * (r16 & 3);
+        const uint2 lo = lds_tr(p), hi = lds_tr(p + 4 * kGL);
+        b[cb] = u32x4{lo.x, lo.y, hi.x, hi.y};
       }
 #pragma unroll
-      for (int n = 0; n < CN; ++n)
+      for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int term = 0; term < 3; ++term)
 #pragma unroll
-          for (int cb = 0; cb < 4; ++cb) {
-            f32x4& s = acc[(c % NC) * CN + n][cb];
-            s = mfma16(v[c & 1][n][term], b[cb], s);
-          }
+          for (int cb = 0; cb < 4; ++cb) acc[n][cb] = mfma16(v[slice][n][term], b[cb], acc[n][cb]);
     }
   }
 }
 
 template <int NB, bool PACKED>
-__global__ __launch_bounds__(256, NB <= 4 ? 2 : 1) void k_gram8(GramArgs8 a) {
+__global__ __launch_bounds__(256, 2) void k_gram8(GramArgs8 a) {
   constexpr int LR = 68;                            // a reduced row, FP32
   __shared__ __attribute__((aligned(16))) uint8_t glds[4 * 64 * kGL * 2];
   static_assert(4 * 16 * LR * 4 <= 4 * 64 * kGL * 2, "reduction buffer");
@@ -1202,17 +1208,20 @@ __global__ __launch_bounds__(256, NB <= 4 ? 2 : 1) void k_gram8(GramArgs8 a) {
   const int ct01 = ct0 + ct1;
   int splits = (tiles + a.tps - 1) / a.tps;
   int4 sp = {0, 0, 0, 0};
-  int first = 0;
+  int first = 0, s_at = 0;
   if (a.plan.head) {
     // (in bounds whatever the plan holds: the grid stops at its room)
-    const int s0 = (int)min((int64_t)blockIdx.x / ct01, (int64_t)a.most - 1);
+    const int s0 = (int)min((int64_t)blockIdx.x / a.groups / ct01, (int64_t)a.most - 1);
+    s_at = s0;
     sp = a.plan.split[s0];
     first = a.plan.split_first[s0];
     if (!plan_fits(a.plan, a.M, a.slots)) return;
     splits = a.plan.head[kPlanSplits];
   }
   const int64_t items = (int64_t)splits * ct01;
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+  for (int64_t it = blockIdx.x; it < items * a.groups; it += gridDim.x) {
+    int group;
+    const int64_t item = ranked(it, a.groups, items, group);
     const int si = (int)(item / ct01);
     int ct = (int)(item % ct01);
     const int side = ct >= ct0 ? 1 : 0;
@@ -1220,7 +1229,8 @@ __global__ __launch_bounds__(256, NB <= 4 ? 2 : 1) void k_gram8(GramArgs8 a) {
     const GramSide& q = a.q[side];
     int64_t part = -1;
     if (a.plan.head) {
-      if (item != blockIdx.x) {
+      if (si != s_at) {
+        s_at = si;
         sp = a.plan.split[si];
         first = a.plan.split_first[si];
       }
@@ -1236,10 +1246,11 @@ __global__ __launch_bounds__(256, NB <= 4 ? 2 : 1) void k_gram8(GramArgs8 a) {
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int cb = 0; cb < 4; ++cb) acc[nb][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (PACKED && side == 0) gram_item<NB, true>(a, q, c0, sp, first, st, acc);
-    else gram_item<NB, false>(a, q, c0, sp, first, st, acc);
+    if (PACKED && side == 0) gram_item<NB, true>(a, q, c0, sp, first, group, st, acc);
+    else gram_item<NB, false>(a, q, c0, sp, first, group, st, acc);
 
-    // accumulator lane (r16, g): ranks 16 nb + 4 g + v, column c0 + 16 cb + r16
+    // accumulator lane (r16, g): ranks 16 nb + 4 g + v of the group, column c0 + 16 cb + r16
+    const int i0 = 16 * NB * group;
     float* out = part >= 0 ? q.part + part * a.r * q.d : q.out + (int64_t)sp.x * a.r * q.d;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
@@ -1257,8 +1268,8 @@ __global__ __launch_bounds__(256, NB <= 4 ? 2 : 1) void k_gram8(GramArgs8 a) {
         float sum = red[i * LR + c];
 #pragma unroll
         for (int ww = 1; ww < 4; ++ww) sum += red[(ww * 16 + i) * LR + c];
-        if (16 * nb + i < a.r && c0 + c < q.d)
-          out[side ? (c0 + c) * a.r + 16 * nb + i : (16 * nb + i) * q.d + c0 + c] = sum;
+        const int rank = i0 + 16 * nb + i;
+        if (rank < a.r && c0 + c < q.d) out[side ? (c0 + c) * a.r + rank : rank * q.d + c0 + c] = sum;
       }
     }
     lds_barrier();
@@ -1348,7 +1359,9 @@ hipError_t launch_gram8_nb(GramArgs8 a, hipStream_t st) {
   const int64_t tiles = (a.M + 63) / 64;
   a.most = (int)(a.plan.head ? plan_most_splits(a.M, a.slots) : (tiles + a.tps - 1) / a.tps);
   const int64_t cols = (a.q[0].d + 63) / 64 + (a.q[1].d + 63) / 64;
-  const unsigned grid = (unsigned)std::min<int64_t>(a.most * cols, 2 * kMostGrid);
+  a.nb = frag_blocks(a.r);
+  a.groups = a.nb / NB;
+  const unsigned grid = (unsigned)std::min<int64_t>(a.most * cols * a.groups, 2 * kMostGrid);
   if (a.q[0].codes) hipLaunchKernelGGL((k_gram8<NB, true>), dim3(grid), dim3(256), 0, st, a);
   else hipLaunchKernelGGL((k_gram8<NB, false>), dim3(grid), dim3(256), 0, st, a);
   return hipGetLastError();
@@ -1392,12 +1405,13 @@ hipError_t launch_shrink(const ShrinkArgs& a0, hipStream_t st) {
   a.splits = shrink_splits(a.M, a.K, &a.kper);
   if (a.splits > 1) a.vrows = nullptr;             // k_finish forms V
   const int64_t tiles = a.plan.head ? plan_most_tiles(a.M, a.slots) : (a.M + 63) / 64;
-  const unsigned grid = (unsigned)std::min<int64_t>(tiles * a.splits, kMostGrid);
+  a.groups = std::max(1, frag_blocks(a.r) / 4);
+  a.rp = (int)vrow_ranks(a.r);
+  a.most = (int)tiles;
+  const unsigned grid = (unsigned)std::min<int64_t>(tiles * a.splits * a.groups, kMostGrid);
   if (a.r <= 16) return launch_shrink_nb<1>(a, grid, st);
   if (a.r <= 32) return launch_shrink_nb<2>(a, grid, st);
-  if (a.r <= 64) return launch_shrink_nb<4>(a, grid, st);
-  if (a.r <= 128) return launch_shrink_nb<8>(a, grid, st);
-  return launch_shrink_nb<16>(a, grid, st);
+  return launch_shrink_nb<4>(a, grid, st);
 }
 
 hipError_t launch_expand(const ExpandArgs& a0, hipStream_t st) {
@@ -1439,9 +1453,7 @@ hipError_t launch_gram8(const GramArgs8& a, hipStream_t st) {
   switch (frag_blocks(a.r)) {
     case 1: e = launch_gram8_nb<1>(a, st); break;
     case 2: e = launch_gram8_nb<2>(a, st); break;
-    case 4: e = launch_gram8_nb<4>(a, st); break;
-    case 8: e = launch_gram8_nb<8>(a, st); break;
-    default: e = launch_gram8_nb<16>(a, st);
+    default: e = launch_gram8_nb<4>(a, st);
   }
   if (e != hipSuccess) return e;
   // with one split a slot at most nothing is left to add

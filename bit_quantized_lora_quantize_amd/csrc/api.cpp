@@ -201,6 +201,7 @@ struct PackedPlan {
   uint16_t *t_frags, *u_frags;
   int tps;                      // tiles a token split
   float *da_part, *db_part;     // [splits][r][d_in], [splits][d_out][r]
+  float* dx;                    // few tokens: [splits][M][d_in]
   size_t bytes;
 };
 
@@ -218,6 +219,9 @@ PackedPlan plan_packed(size_t base_bytes, int64_t d_out, int64_t d_in, int64_t M
   p.u_frags = c.take<uint16_t>(frag_elems(tiles, r));
   p.da_part = c.take<float>(parts * r * d_in);
   p.db_part = c.take<float>(parts * r * d_out);
+  int64_t nper;
+  const int ds = dx_few(M, d_out, d_in) ? dx_few_splits(M, d_out, d_in, &nper) : 0;
+  p.dx = c.take<float>(ds > 1 ? ds * M * d_in : 0);
   p.bytes = c.off + 256;
   return p;
 }
@@ -663,7 +667,12 @@ int bwd_packed_impl(const qlora_nf4_t* q, const qlora_packed_t* X8, const uint16
   fa.t_frags = pp.t_frags;
   s = hip_status(launch_finish_v(fa, st));
   if (s) return s;
-  if (dX) {
+  if (dX && dx_few(M, d_out, d_in)) {
+    DxFewArgs g{q->codes, q->scale_codes, q->scale2, q->scale_mean, dY, p.u_hl, A,    dX,
+                pp.dx,    M,              d_out,     d_in,          r,  p.rp,   keep, dp.ldw};
+    s = hip_status(launch_dx_few(g, st));
+    if (s) return s;
+  } else if (dX) {
     GemmArgs g{q->codes, q->scale_codes, q->scale2, q->scale_mean, dY, p.u_hl, A, dX,
                M,        d_out,          d_in,      r,            keep, dp.ldw};
     s = hip_status(launch_gemm_bwd(g, st));

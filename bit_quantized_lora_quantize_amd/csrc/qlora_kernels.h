@@ -468,6 +468,43 @@ struct GemmArgs {
 hipError_t launch_gemm_fwd(const GemmArgs& a, hipStream_t st);
 hipError_t launch_gemm_bwd(const GemmArgs& a, hipStream_t st);
 
+// ------------------------------------------------- input gradient, few tokens
+constexpr int kDxSplits = 8;   // at most
+// Ranges of the outputs that k_dx_few sums apart, for about 1024 items.
+inline int dx_few_splits(int64_t M, int64_t d_out, int64_t d_in, int64_t* nper) {
+  const int64_t items = std::max<int64_t>(1, (M + 63) / 64 * (d_in / 64));
+  int64_t s = std::min<int64_t>((1024 + items - 1) / items, (d_out + 127) / 128);
+  s = std::max<int64_t>(1, std::min<int64_t>(s, kDxSplits));
+  *nper = ((d_out + s - 1) / s + 127) / 128 * 128;
+  return (int)((d_out + *nper - 1) / *nper);
+}
+// Whether it takes the place of the fused GEMM: while the GEMM has fewer than 64
+// tiles of 256 x 256 (whole backward, 4096 -> 4096, rank 16: 1 token 29 us and
+// 109, 512 tokens 76 and 119, 1024 tokens, 64 tiles, 114 and 125; 2048 tokens,
+// 128 tiles, 205 and 137), and for rows of dY that are no whole 16-byte pieces,
+// which the GEMM loads by element (2048 tokens 4096 -> 4099 396 and 667, 8192
+// tokens 1388 and 1424, 8192 tokens -> 4100 819 and 1240).
+inline bool dx_few(int64_t M, int64_t d_out, int64_t d_in) {
+  return d_out % 8 != 0 || (M + 255) / 256 * ((d_in + 255) / 256) < 64;
+}
+struct DxFewArgs {
+  const uint8_t* codes;
+  const uint8_t* scodes;
+  const float* scale2;
+  const float* mean;
+  const uint16_t* dY;      // [M][d_out]
+  const uint16_t* u_hl;    // [M][2 rp] BF16 hi | lo of U
+  const uint16_t* A;       // [r][d_in]
+  uint16_t* dX;            // [M][d_in]
+  float* part;             // [splits][M][d_in]
+  int64_t M, d_out, d_in, r, rp;
+  const uint32_t* keep;    // as GemmArgs
+  int64_t keep_ld;
+  int64_t nper;            // nper, splits: set by launch_dx_few
+  int splits;
+};
+hipError_t launch_dx_few(const DxFewArgs& a, hipStream_t st);
+
 // ------------------------------------------------- norms
 // Element types are QLORA_BF16 / QLORA_F32; the operations are stated at
 // qlora_norm_fwd and qlora_norm_bwd.
@@ -628,7 +665,8 @@ inline int64_t vrow_ranks(int64_t r) { return r <= 32 ? 32 : (r <= 64 ? 64 : (r 
 struct ShrinkArgs {
   PlanView plan;
   int64_t M, slots, K, kper;
-  int r, splits;        // splits, kper: set by launch_shrink
+  int r;
+  int splits, groups, rp, most;   // and kper: set by launch_shrink
   bool kn;              // F as [K][r] (else [r][K])
   const uint16_t* P;    // [M][K]
   const uint16_t* F;    // [slots] of them
@@ -702,7 +740,7 @@ struct GramArgs8 {
   PlanView plan;
   int64_t M, slots, r;
   int tps;                 // tiles a split
-  int most;                // set by launch_gram8
+  int most, nb, groups;    // set by launch_gram8
   GramSide q[2];           // dA from (U, X), dB from (T, dY)
 };
 hipError_t launch_gram8(const GramArgs8& a, hipStream_t st);

@@ -44,7 +44,7 @@ def _exact(w, X, T, dY, A, B, s, keep=None, rest=1.0):
 
 @pytest.mark.parametrize("M,d_in,d_out,r", [(1, 64, 64, 8), (5, 128, 77, 3), (16, 256, 200, 16), (17, 64, 128, 16), (100, 320, 136, 20),
                                             (130, 512, 257, 64), (333, 192, 520, 50), (257, 256, 264, 128), (90, 128, 96, 256),
-                                            (2500, 128, 128, 16)])
+                                            (2500, 128, 128, 16), (700, 192, 1100, 16), (16400, 64, 64, 8), (16390, 64, 67, 8)])
 def test_backward(M, d_in, d_out, r):
     say(f"packed backward M={M} {d_in}->{d_out} r={r}")
     w, X, dY, A, B = _layer(M + r, M, d_in, d_out, r)
@@ -65,28 +65,29 @@ def test_backward(M, d_in, d_out, r):
     assert none is None and torch.equal(dA2, dA) and torch.equal(dB2, dB)
 
 
-@pytest.mark.parametrize("M", [7, 16, 40, 200])
+@pytest.mark.parametrize("M", [7, 16, 40, 200, 16700])
 @pytest.mark.parametrize("saved", [False, True])
 def test_dropout(M, saved):
-    d_in, d_out, r, p = 128, 96, 16, 0.25
+    d_in, d_out, r, p = (128, 96, 16, 0.25) if M < 1000 else (64, 64, 8, 0.25)
     w, X, dY, A, B = _layer(M, M, d_in, d_out, r)
     drop = q.Dropout(p, seed=77, offset=5)
     if saved:
         drop = drop.saved_mask(M, d_in)
     Xd, dYd, Ad, Bd = (t.to(DEV) for t in (X, dY, A, B))
     T = torch.empty(M, r, device=DEV)
-    q.qlora_linear_fwd_dropout(w, Xd, Ad, Bd, 32.0, drop, T_save=T)
+    alpha = 2.0 * r
+    q.qlora_linear_fwd_dropout(w, Xd, Ad, Bd, alpha, drop, T_save=T)
     ones = torch.ones(M, d_in, dtype=torch.bfloat16, device=DEV)
     keep = ref.f64(q.qlora_dropout_mask(ones, q.Dropout(p, seed=77, offset=5))[0])
     assert 0.5 < float(keep.mean()) < 0.95
     X8 = q.qlora_pack8(Xd)
     back = q.qlora_unpack8(X8)
-    dX, dA, dB = q.qlora_linear_bwd_packed(w, X8, dYd, Ad, Bd, 32.0, T, dropout=drop)
+    dX, dA, dB = q.qlora_linear_bwd_packed(w, X8, dYd, Ad, Bd, alpha, T, dropout=drop)
     s = float(torch.tensor(2.0) / (torch.tensor(1.0) - torch.tensor(p)))
     want, bound = _exact(w, back, T, dY, A, B, s, keep)
     for name, got in (("dA", dA), ("dB", dB), ("dX", dX)):
         ref.inside(got, want[name], bound[name], name)
-    other = q.qlora_linear_bwd_dropout(w, back, dYd, Ad, Bd, 32.0, drop, T_saved=T)[0]
+    other = q.qlora_linear_bwd_dropout(w, back, dYd, Ad, Bd, alpha, drop, T_saved=T)[0]
     ref.inside(dX, ref.f64(other), 2 * bound["dX"], "dX against the BF16 input's")
 
 
