@@ -10,11 +10,12 @@
 //
 // k_plan_* sort the tokens by slot (stable, so that every sum over tokens has
 // one order) into tiles of up to 64 tokens of one slot; the other kernels walk
-// that list, whose length only the device knows.  Two launches make a forward:
-// k_shrink (FP32 partial sums over ranges of the long axis) and k_expand, which
-// adds the partials, and with them the shared projection's output.  A backward
-// adds k_frags (T and U as matrix operands) and k_gram (the contractions over
-// tokens).  Products are BF16 on the matrix cores with FP32 sums; T and U are
+// that list, whose length only the device knows.  k_shrink forms T or U as FP32
+// partial sums over ranges of the long axis, k_finish adds those and writes them
+// as matrix operands, k_expand multiplies by the other factor and adds the shared
+// projection's output (for few tokens it adds the partials too: two launches make
+// such a forward).  A backward adds k_gram8, the contractions over tokens, and
+// k_gram_sum, which adds their splits.  Products are BF16 on the matrix cores with FP32 sums; T and U are
 // FP32 and enter them as sums of BF16 terms: two (16 bits) where the result is
 // rounded to BF16, three (24 bits, all of FP32) where it is FP32.
 #include <type_traits>
@@ -581,7 +582,7 @@ __device__ __forceinline__ void sum_parts(const float* part, const int (&at)[Q],
 // out[token][n] = RN(in[token][n] + sum_i V[token][i] F[n][i]),
 // V of k_shrink or k_finish as BF16 hi + lo.  F is stored [d][r] (B in the
 // forward) or, RD, [r][d] (A in the backward).  Item = a few tiles of one slot
-// and 256 columns, whose part of F stays in LDS: a wavefront takes 16 tokens of a
+// and 256 columns (fewer at ranks past 64), whose part of F stays in LDS: a wavefront takes 16 tokens of a
 // tile at a time, 512 bytes of each row, and loads the next tile's while it works
 // on this one, without a barrier.  Neighbouring items are the neighbouring
 // columns of the same tokens, so that what the chip works on at a time is whole
@@ -594,7 +595,9 @@ __device__ __forceinline__ void sum_parts(const float* part, const int (&at)[Q],
 // Items of up to 16 tokens (decoding) have nothing to reuse F for: there each
 // wavefront takes 64 columns and reads F from memory.
 // ---------------------------------------------------------------------------
-constexpr int kExpandCols = 256;
+// Columns of an item: as many as leave LDS for two or three workgroups.
+template <int KS>
+constexpr int expand_cols() { return KS <= 2 ? 256 : (KS == 4 ? 128 : 64); }
 constexpr int kTurn = 68;   // a row of 64 sums in the wavefront's LDS, FP32
 
 // The column that row j of MFMA block b (0..3) stands for in a unit of 64.
@@ -602,12 +605,12 @@ __device__ __forceinline__ int unit_column(int j, int b) {
   return 32 * (b >> 1) + 8 * (j >> 2) + 4 * (b & 1) + (j & 3);
 }
 
-// F's part in LDS: rows n of 32 KS + 8 ranks, or RD rows i of 264 columns; zero
+// F's part in LDS: rows n of 32 KS + 8 ranks, or RD rows i of its columns + 8; zero
 // past r and past d.
 template <int KS, bool RD>
-constexpr int expand_ld() { return RD ? kExpandCols + 8 : 32 * KS + 8; }
+constexpr int expand_ld() { return RD ? expand_cols<KS>() + 8 : 32 * KS + 8; }
 template <int KS, bool RD>
-constexpr int expand_lds() { return (RD ? 32 * KS : kExpandCols) * expand_ld<KS, RD>() * 2; }
+constexpr int expand_lds() { return (RD ? 32 * KS : expand_cols<KS>()) * expand_ld<KS, RD>() * 2; }
 constexpr int kTurnBytes = 4 * 16 * kTurn * 4;
 
 // Block b's operand of unit u, ranks 32 ks .. +32.
@@ -680,20 +683,20 @@ __device__ __forceinline__ void expand_v(const ExpandArgs& a, int pos, int ks, f
 template <int KS, bool RD, bool R8, bool DEEP, bool SUMS>
 __device__ __forceinline__ void expand_many(const ExpandArgs& a, int slot, int first, int tokens,
                                             int64_t c0, uint8_t* lds) {
-  constexpr int L = expand_ld<KS, RD>();
+  constexpr int L = expand_ld<KS, RD>(), COLS = expand_cols<KS>(), U = COLS / 64;
   uint16_t* fl = reinterpret_cast<uint16_t*>(lds + kTurnBytes);
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float* turn = reinterpret_cast<float*>(lds) + w * 16 * kTurn;
   const int r16 = lane & 15, g = lane >> 4, l8 = lane >> 3, c8 = 8 * (lane & 7);
   const int r = a.r, tiles = (tokens + 63) / 64;
   const int64_t d = a.d;
-  const bool whole = c0 + kExpandCols <= d;
+  const bool whole = c0 + COLS <= d;
   const uint16_t* F = a.F + (int64_t)slot * r * d;
 
   // Of a tile's 16 tokens: as an operand's column lane r16's, of its rows in
   // memory the lane's two, l8 and 8 + l8 (past the last token: that one again).
   struct Rows {
-    u32x4 y[4][2], v[KS][2];
+    u32x4 y[U][2], v[KS][2];
     int64_t at[2];
   };
   auto place = [&](int j, int row) { return first + min(64 * j + 16 * w + row, tokens - 1); };
@@ -714,13 +717,13 @@ __device__ __forceinline__ void expand_many(const ExpandArgs& a, int slot, int f
       t.at[h] = tok[h] * d + c0 + c8;
       if (!a.in) continue;
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < U; ++u)
         t.y[u][h] = d >= 8 ? load_vec(a.in + tok[h] * d + at8(c0 + 64 * u + c8, d)) : few8(a.in + tok[h] * d, c8, d);
     }
   };
   auto work = [&](int j, Rows& t) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < U; ++u) {
       if (c0 + 64 * u >= d) break;
       f32x4 acc[4];
 #pragma unroll
@@ -762,7 +765,7 @@ __device__ __forceinline__ void expand_many(const ExpandArgs& a, int slot, int f
   }
   lds_barrier();                                   // the last item's F is no longer read
   if (RD) {
-    constexpr int P = kExpandCols / 8;
+    constexpr int P = COLS / 8;
 #pragma unroll 4
     for (int e = threadIdx.x; e < 32 * KS * P; e += 256) {
       const int i = e / P, cc = 8 * (e % P);
@@ -773,7 +776,7 @@ __device__ __forceinline__ void expand_many(const ExpandArgs& a, int slot, int f
   } else {
     constexpr int P = 4 * KS;
 #pragma unroll 4
-    for (int e = threadIdx.x; e < kExpandCols * P; e += 256) {
+    for (int e = threadIdx.x; e < COLS * P; e += 256) {
       const int n = e / P, i = 8 * (e % P);
       const bool ok = c0 + n < d && i < r;
       const uint16_t* row = F + (c0 + n < d ? c0 + n : 0) * r;
@@ -816,7 +819,7 @@ __device__ __forceinline__ void expand_few(const ExpandArgs& a, int slot, int fi
   const int r = a.r;
   const int64_t d = a.d, col0 = c0 + 64 * w;
   if (RD) lds_barrier();                           // another item's F is no longer read
-  if (col0 >= d) return;
+  if (64 * w >= expand_cols<KS>() || col0 >= d) return;
   const bool whole = col0 + 64 <= d;
   uint16_t* stage = reinterpret_cast<uint16_t*>(lds) + w * 32 * LF;
   const uint16_t* F = a.F + (int64_t)slot * r * d;
@@ -880,8 +883,8 @@ __device__ __forceinline__ void expand_few(const ExpandArgs& a, int slot, int fi
 }
 
 // Tokens without an adapter: their rows' columns copied, T zero.
-__device__ __forceinline__ void expand_none(const ExpandArgs& a, const int4& td, int64_t c0) {
-  const int64_t n = min((int64_t)kExpandCols, a.d - c0);
+__device__ __forceinline__ void expand_none(const ExpandArgs& a, const int4& td, int64_t c0, int cols) {
+  const int64_t n = min((int64_t)cols, a.d - c0);
   const int vecs = (int)((n + 7) / 8);
   if (a.in != a.out) {
     for (int e = threadIdx.x; e < td.z * vecs; e += 256) {
@@ -911,10 +914,10 @@ __global__ __launch_bounds__(256, KS > 4 ? 1 : (DEEP || KS > 2 ? 2 : 3)) void k_
   for (int item = blockIdx.x; item < with_one + none; item += gridDim.x) {
     if (item >= with_one) {
       expand_none(a, a.plan.tile[tiles + (item - with_one) / a.chunks],
-                  (int64_t)((item - with_one) % a.chunks) * kExpandCols);
+                  (int64_t)((item - with_one) % a.chunks) * expand_cols<KS>(), expand_cols<KS>());
       continue;
     }
-    const int64_t c0 = (int64_t)(item % a.chunks) * kExpandCols;
+    const int64_t c0 = (int64_t)(item % a.chunks) * expand_cols<KS>();
     const int group = item / a.chunks;
     if (item != (int)blockIdx.x) {
       rec = DEEP ? a.plan.split[group / a.subs] : a.plan.tile[group];
@@ -1057,7 +1060,9 @@ __global__ __launch_bounds__(256) void k_finish(FinishVArgs a) {
 // tokens x 64 columns in LDS of their own (where 8-bit codes become BF16) and
 // read the column operands transposed; their sums are added through LDS in
 // wavefront order.  A slot's only split is its gradient; else the splits'
-// results are added by k_gram_sum.
+// results are added by k_gram_sum.  A split of one tile has nothing to add: there
+// each wavefront takes a column tile (141 tokens of 11 slots, 10880 to 5184
+// features, 20 ranks: 22 us against 28 with three of four wavefronts idle).
 // ---------------------------------------------------------------------------
 constexpr int kGL = 72;   // staged row, elements
 
@@ -1138,12 +1143,13 @@ __device__ __forceinline__ void gram_stage(const GramTile& t, int lane, uint16_t
   }
 }
 
-// sp: {slot, first tile, tokens, }, `first` the split's first position.
+// A wavefront's part of a split: tiles w, w + 4, ...  sp: {slot, first tile,
+// tokens, }, `first` the split's first position.
 template <int NB, bool PACKED>
 __device__ __forceinline__ void gram_item(const GramArgs8& a, const GramSide& q, int64_t c0,
-                                          const int4& sp, int first, int group,
+                                          const int4& sp, int first, int w, int group,
                                           uint16_t* st, f32x4 (&acc)[NB][4]) {
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
   const int r16 = lane & 15, g = lane >> 4;
   const int tiles = (sp.z + 63) / 64;
   auto token = [&](int j) {
@@ -1167,16 +1173,20 @@ __device__ __forceinline__ void gram_item(const GramArgs8& a, const GramSide& q,
   for (int j = w; j < tiles; j += 4) {
     // in the order of their use: this tile's operands, the next tile's rows
     const uint16_t* fr = q.frags + (int64_t)(sp.y + j) * 3 * a.nb * 2 * 512 + lane * 8;
-    u32x4 v[2][NB][3];
+    // (at 64 ranks two slices' operands cost registers that spill: 4096 tokens,
+    // 4096 to 4096 features, 64 ranks, 4 slots 45.7 us, with one slice's 38.9)
+    constexpr bool AHEAD = NB < 4;
+    u32x4 v[1 + AHEAD][NB][3];
     load_v(fr, 0, v[0]);
     gram_stage<PACKED>(cur, lane, st);
-    load_v(fr, 1, v[1]);
+    if (AHEAD) load_v(fr, 1, v[AHEAD]);
     if (j + 4 < tiles) {
       gram_load<PACKED>(q, a.M, c0, next, lane, cur);
       next = token(j + 8);
     }
 #pragma unroll
     for (int slice = 0; slice < 2; ++slice) {
+      if (!AHEAD && slice == 1) load_v(fr, 1, v[0]);
       u32x4 b[4];
 #pragma unroll
       for (int cb = 0; cb < 4; ++cb) {
@@ -1189,7 +1199,7 @@ __device__ __forceinline__ void gram_item(const GramArgs8& a, const GramSide& q,
 #pragma unroll
         for (int term = 0; term < 3; ++term)
 #pragma unroll
-          for (int cb = 0; cb < 4; ++cb) acc[n][cb] = mfma16(v[slice][n][term], b[cb], acc[n][cb]);
+          for (int cb = 0; cb < 4; ++cb) acc[n][cb] = mfma16(v[AHEAD * slice][n][term], b[cb], acc[n][cb]);
     }
   }
 }
@@ -1240,18 +1250,39 @@ __global__ __launch_bounds__(256, 2) void k_gram8(GramArgs8 a) {
       sp = int4{0, si * a.tps, (int)min((int64_t)64 * a.tps, a.M - first), 0};
       if (splits > 1) part = si;
     }
+    // one tile: each wavefront a column tile of its own, and nothing to add
+    const bool alone = sp.z <= 64;
+    if (alone) {
+      if (ct & 3) continue;
+      ct += w;
+    }
     const int64_t c0 = (int64_t)ct * 64;
     f32x4 acc[NB][4];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int cb = 0; cb < 4; ++cb) acc[nb][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (PACKED && side == 0) gram_item<NB, true>(a, q, c0, sp, first, group, st, acc);
-    else gram_item<NB, false>(a, q, c0, sp, first, group, st, acc);
+    float* out = part >= 0 ? q.part + part * a.r * q.d : q.out + (int64_t)sp.x * a.r * q.d;
+    if (!alone || c0 < q.d) {
+      if (PACKED && side == 0) gram_item<NB, true>(a, q, c0, sp, first, alone ? 0 : w, group, st, acc);
+      else gram_item<NB, false>(a, q, c0, sp, first, alone ? 0 : w, group, st, acc);
+    }
+    if (alone) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int cb = 0; cb < 4; ++cb)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int64_t c = c0 + 16 * cb + r16;
+            const int rank = 16 * NB * group + 16 * nb + 4 * g + v;
+            if (rank < a.r && c < q.d) out[side ? c * a.r + rank : rank * q.d + c] = acc[nb][cb][v];
+          }
+      continue;
+    }
 
     // accumulator lane (r16, g): ranks 16 nb + 4 g + v of the group, column c0 + 16 cb + r16
     const int i0 = 16 * NB * group;
-    float* out = part >= 0 ? q.part + part * a.r * q.d : q.out + (int64_t)sp.x * a.r * q.d;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       lds_barrier();
@@ -1416,7 +1447,8 @@ hipError_t launch_shrink(const ShrinkArgs& a0, hipStream_t st) {
 
 hipError_t launch_expand(const ExpandArgs& a0, hipStream_t st) {
   ExpandArgs a = a0;
-  a.chunks = (int)((a.d + kExpandCols - 1) / kExpandCols);
+  const int64_t cols = a.r <= 64 ? expand_cols<2>() : (a.r <= 128 ? expand_cols<4>() : expand_cols<8>());
+  a.chunks = (int)((a.d + cols - 1) / cols);
   // more tiles an item where there are enough items
   const int64_t tiles = (a.M + kPlanTile - 1) / kPlanTile;
   a.tpi = (int)std::max<int64_t>(1, std::min<int64_t>(8, tiles * a.chunks / 1024));

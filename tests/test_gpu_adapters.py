@@ -1,5 +1,8 @@
 """Adapters of many requests on the GPU, forward and backward, against their
 definition in 64 bits with a bound for every element."""
+import math
+import random
+
 import pytest
 import torch
 
@@ -43,7 +46,8 @@ def _backward(b, plan, d, T, packed=False):
 
 
 # tokens, d_in, d_out, rank, slots, longest run
-SHAPES = [(1, 64, 64, 8, 1, 1), (1, 1, 1, 1, 1, 1), (2, 8, 24, 3, 2, 1), (15, 100, 72, 16, 3, 1), (16, 256, 264, 16, 16, 1),
+SHAPES = [(5, 3, 2100, 8, 2, 1), (70, 5, 7, 4, 2, 30), (2300, 40, 520, 6, 3, 300), (2100, 300, 64, 64, 4, 900),
+          (1, 64, 64, 8, 1, 1), (1, 1, 1, 1, 1, 1), (2, 8, 24, 3, 2, 1), (15, 100, 72, 16, 3, 1), (16, 256, 264, 16, 16, 1),
           (17, 63, 65, 17, 4, 2), (40, 520, 129, 32, 40, 1), (63, 128, 1000, 8, 2, 70), (64, 1000, 128, 20, 1, 64),
           (65, 512, 512, 64, 2, 65), (130, 320, 200, 48, 3, 50), (257, 72, 520, 100, 5, 30), (300, 517, 333, 7, 4, 90),
           (333, 1000, 517, 8, 3, 40), (129, 264, 136, 128, 2, 129), (200, 136, 264, 160, 3, 40), (70, 264, 512, 256, 2, 40),
@@ -65,9 +69,13 @@ def test_forward_and_backward(shape, base):
     assert torch.equal(again.dA, kept.dA)
 
 
-@pytest.mark.parametrize("M,d_in,d_out,r,slots", [(4096, 512, 264, 16, 3), (9000, 64, 128, 8, 1), (6000, 256, 64, 64, 2)])
+@pytest.mark.parametrize("M,d_in,d_out,r,slots", [(4096, 512, 264, 16, 3), (9000, 64, 128, 8, 1), (6000, 256, 64, 64, 2),
+                                                    (9000, 72, 4100, 30, 3), (9001, 2051, 64, 64, 2), (9000, 64, 4096, 100, 2),
+                                                    (8500, 4100, 72, 100, 2), (8200, 64, 2051, 200, 1), (8200, 2056, 40, 200, 2)])
 def test_many_tokens_of_one_slot(M, d_in, d_out, r, slots):
-    """Slots of several token splits, whose partial results are added."""
+    """Slots of several token splits, whose partial results are added; wide rows,
+    of which an item of the expansion takes several tiles, at every rank's width
+    of its items."""
     b = ref.batch(M, M, d_in, d_out, r, slots, 3000, none=0.05)
     out, plan, d = _forward(b)
     _backward(b, plan, d, out.T)
@@ -387,3 +395,15 @@ def test_large_offsets():
     plan = q.qlora_adapters_plan(torch.tensor([299, 299], dtype=torch.int32, device=DEV), slots)
     o = q.qlora_adapters_fwd(x, bank, plan)
     assert (o.Y[0] == 256).all() and (o.Y[1] == 258).all()
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_shapes_at_random(seed):
+    """Sizes over the range, odd ones among them, and requests of any length."""
+    g = random.Random(seed)
+    spread = lambda lo, hi: int(round(math.exp(g.uniform(math.log(lo), math.log(hi)))))  # noqa: E731
+    shape = (spread(1, 3000), spread(1, 1500), spread(1, 1500), spread(1, 256), spread(1, 60), spread(1, 600))
+    say(f"adapters {shape}")
+    b = ref.batch(seed, *shape, base=seed % 3 > 0)
+    out, plan, d = _forward(b)
+    _backward(b, plan, d, out.T, packed=seed % 2 == 0)
