@@ -14,8 +14,9 @@ answers:
     D = G W_down^T + lora     H2, N2 = norm(D + H1)     logits = N2 W_head^T + lora
 
 The SiLU and its derivative are PyTorch's; everything else runs in the library.
+With kept="8bit" the layers keep their inputs for the backward in 8 bits.
 
-Usage: python examples/tuning_step.py [--loss preference|policy] [--steps N]
+Usage: python examples/tuning_step.py [--loss preference|policy] [--steps N] [--kept bf16|8bit]
 """
 import argparse
 import os
@@ -32,7 +33,8 @@ RANK, ALPHA = 16, 32.0
 class Adapter:
     """An NF4 weight [d_out, d_in] with its LoRA factors and their AdamW state."""
 
-    def __init__(self, d_out, d_in, gen, dev):
+    def __init__(self, d_out, d_in, gen, dev, kept):
+        self.kept = kept
         self.w = q.qlora_quantize_nf4(torch.randn(d_out, d_in, generator=gen, device=dev) * 0.02)
         self.params = []
         for shape, std in (((RANK, d_in), 1.0 / RANK), ((d_out, RANK), 0.0)):
@@ -45,13 +47,14 @@ class Adapter:
         t = torch.empty((x.shape[0], RANK), dtype=torch.float32, device=x.device)
         y = q.qlora_linear_fwd(self.w, x, a, b, alpha, T_save=t)
         if save:
-            self.x, self.t = x, t
+            self.x, self.t = q.qlora_pack8(x) if self.kept == "8bit" else x, t
         return y
 
     def backward(self, dy):
         a, b = self.params
-        dx, _, _ = q.qlora_linear_bwd(self.w, self.x, dy, a.param_bf16, b.param_bf16, ALPHA,
-                                      T_saved=self.t, dA=a.grad, dB=b.grad)
+        back = q.qlora_linear_bwd_packed if self.kept == "8bit" else q.qlora_linear_bwd
+        dx, _, _ = back(self.w, self.x, dy, a.param_bf16, b.param_bf16, ALPHA,
+                        T_saved=self.t, dA=a.grad, dB=b.grad)
         return dx
 
 
@@ -72,12 +75,12 @@ class Norm:
 
 
 class Model:
-    def __init__(self, d, ff, vocab, seed, dev):
+    def __init__(self, d, ff, vocab, seed, dev, kept="bf16"):
         gen = torch.Generator(device=dev)
         gen.manual_seed(seed)
         self.embedding = torch.randn(vocab, d, generator=gen, device=dev).to(torch.bfloat16)
-        self.up, self.down = Adapter(ff, d, gen, dev), Adapter(d, ff, gen, dev)
-        self.head = Adapter(vocab, d, gen, dev)
+        self.up, self.down = Adapter(ff, d, gen, dev, kept), Adapter(d, ff, gen, dev, kept)
+        self.head = Adapter(vocab, d, gen, dev, kept)
         self.n1, self.n2 = Norm(d, dev), Norm(d, dev)
         params = [p for layer in (self.up, self.down, self.head) for p in layer.params]
         self.params = q.AdamwParamSet(params + [self.n1.p, self.n2.p])
@@ -126,11 +129,11 @@ def answers(pairs, longest, vocab, seed, dev):
 
 
 def run(loss="preference", steps=10, pairs=4, longest=48, d=512, ff=1024, vocab=4000, lr=2e-3,
-        seed=0, device="cuda", show=print):
+        seed=0, device="cuda", show=print, kept="bf16"):
     """The loss of every step (the policy loss is taken over two updates per
     batch of log-probabilities, so that its ratio moves)."""
     dev = torch.device(device, torch.cuda.current_device()) if device == "cuda" else device
-    model = Model(d, ff, vocab, seed, dev)
+    model = Model(d, ff, vocab, seed, dev, kept)
     tokens, targets, offsets = answers(pairs, longest, vocab, seed, dev)
     ref, _ = q.qlora_token_logp(model.logits(tokens, alpha=0.0, save=False), targets)
     gen = torch.Generator().manual_seed(seed + 1)
@@ -159,5 +162,6 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser()
     ap.add_argument("--loss", choices=("preference", "policy"), default="preference")
     ap.add_argument("--steps", type=int, default=10)
+    ap.add_argument("--kept", choices=("bf16", "8bit"), default="bf16")
     a = ap.parse_args()
-    run(a.loss, a.steps)
+    run(a.loss, a.steps, kept=a.kept)
