@@ -287,12 +287,18 @@ __global__ __launch_bounds__(256) void k_plan_lists(PlanView p, int M, int slots
   __shared__ int cnt[kPlanMaxSlots + 2], tile0[kPlanMaxSlots + 2], split0[kPlanMaxSlots + 2];
   __shared__ int4 red[4];
   for (int s = threadIdx.x; s <= slots; s += 256) {
+    // eight spans' counts at a time: the loop is bound by the latency of its loads
     int sum = 0;
-    for (int b = 0; b < spans; ++b) {
-      const int64_t at = (int64_t)b * (slots + 1) + s;
-      const int c = hist[at];
-      hist[at] = sum;
-      sum += c;
+    for (int b0 = 0; b0 < spans; b0 += 8) {
+      int32_t* h = hist + (int64_t)b0 * (slots + 1) + s;
+      int c[8];
+#pragma unroll
+      for (int b = 0; b < 8; ++b) c[b] = b0 + b < spans ? h[(int64_t)b * (slots + 1)] : 0;
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        if (b0 + b < spans) h[(int64_t)b * (slots + 1)] = sum;
+        sum += c[b];
+      }
     }
     cnt[s] = sum;
   }

@@ -355,6 +355,37 @@ def test_captured_and_replayed():
         assert all(torch.equal(x, y) for x, y in zip(got, held))
 
 
+def test_two_graphs_share_a_workspace_and_a_plan():
+    """One projection's forward and another's backward captured apart over the same
+    scratch memory and the same plan, replayed in turn in both orders."""
+    b1, b2 = ref.batch(14, 300, 200, 90, 24, 3, 40), ref.batch(14, 300, 64, 264, 70, 3, 40)
+    d1, d2 = _gpu(b1), _gpu(b2)
+    n1, n2 = _bank(d1), _bank(d2)
+    plan = q.qlora_adapters_plan(d1["index"], 3)
+    room = max(q.qlora_adapters_workspace_bytes(n, 300, backward=True) for n in (n1, n2))
+    ws = torch.empty(room, dtype=torch.uint8, device=DEV)
+    T2 = q.qlora_adapters_fwd(d2["X"], n2, plan).T
+    calls = [lambda **kw: q.qlora_adapters_fwd(d1["X"], n1, plan, Y0=d1["Y0"], **kw),
+             lambda **kw: q.qlora_adapters_bwd(d2["dY"], d2["X"], T2, n2, plan, dX0=d2["dX0"], **kw)]
+    want = [call() for call in calls]
+    torch.cuda.synchronize()
+    graphs, held = [], []
+    for call in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            held.append(call(workspace=ws))
+    for turn in ((0, 1), (1, 0), (1, 1), (0, 0), (0, 1)):
+        ws.fill_(255)
+        for out in held:
+            for x in out:
+                x.zero_()
+        for i in turn:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in set(turn):
+            assert all(torch.equal(x, y) for x, y in zip(held[i], want[i]))
+
+
 def test_large_offsets():
     """Rows past 2^31 elements of X and Y, slots past 2^31 bytes of the factors."""
     M, d_in, d_out, r, slots = 70000, 32000, 8, 8, 2
