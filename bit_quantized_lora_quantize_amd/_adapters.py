@@ -74,8 +74,14 @@ class Packed8:
     @staticmethod
     def empty(M: int, d: int, device="cuda") -> "Packed8":
         nb = _blocks(d)
-        return Packed8(M, d, torch.empty((M, nb * _lib.BLOCK), dtype=_I8, device=device),
-                       torch.empty((nb, M), dtype=_F32, device=device))
+        p = Packed8.__new__(Packed8)   # buffers made here have no shapes to check
+        p.M, p.d = M, d
+        p.codes = torch.empty((M, nb * _lib.BLOCK), dtype=_I8, device=device)
+        p.scale = torch.empty((nb, M), dtype=_F32, device=device)
+        if p.codes.get_device() < 0:
+            raise ValueError(f"device: expected a GPU, got {p.codes.device}")
+        p.c = _Packed(M, d, p.codes.data_ptr(), p.scale.data_ptr())
+        return p
 
     @property
     def device(self):

@@ -178,6 +178,8 @@ def test_bounds_of_the_plans_lists():
 
 
 def test_binding_refuses_tensors_off_the_gpu():
+    with pytest.raises(ValueError):
+        q.Packed8.empty(2, 64, "cpu")
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         q.qlora_pack8(x)
