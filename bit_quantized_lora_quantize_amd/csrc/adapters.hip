@@ -1073,69 +1073,56 @@ __global__ __launch_bounds__(256) void k_finish(FinishVArgs a) {
 constexpr int kGL = 72;   // staged row, elements
 
 // 64 tokens x 64 columns: BF16 as eight 16-byte pieces a lane (row 8 j + l / 8),
-// codes as four (row 16 j + l / 4) with their rows' scales.
+// codes as four (row 16 j + l / 4) with their rows' scales.  As loaded: rows past
+// the split's last repeat it, pieces past the row's end are its last eight.
 struct GramTile {
   u32x4 v[8];
   float s[4];
   uint32_t keep[4];
 };
 
-// tok: the lane's token of the tile (lane = row), -1 past its last.
-template <bool PACKED>
+// tok: the lane's token of the tile (lane = row).  NARROW: rows of fewer than
+// eight (their code costs the others registers).
+template <bool PACKED, bool NARROW>
 __device__ __forceinline__ void gram_load(const GramSide& q, int64_t M, int64_t c0, int tok,
                                           int lane, GramTile& t) {
   if constexpr (PACKED) {
     const int64_t ldc = (q.d + 63) / 64 * 64;
     const uint8_t* codes = q.codes + c0 + 16 * (lane & 3);
     const float* sc = q.scale + c0 / 64 * M;
-    int m[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      m[j] = __shfl(tok, 16 * j + (lane >> 2));
-      const int64_t row = max(m[j], 0);
+      const int64_t row = __shfl(tok, 16 * j + (lane >> 2));
       t.v[j] = *reinterpret_cast<const u32x4*>(codes + row * ldc);
       t.s[j] = sc[row];
-      t.keep[j] = 0xFFFFu;
-      if (q.keep) {
-        const int64_t col = c0 + 16 * (lane & 3);
-        t.keep[j] = q.keep[row * (q.d / 32) + col / 32] >> (col & 16);
-      }
+      if (q.keep) t.keep[j] = q.keep[row * (q.d / 32) + (c0 + 16 * (lane & 3)) / 32];
     }
+  } else if (!NARROW || q.d >= 8) {
+    const uint16_t* x = q.x + at8(c0 + 8 * (lane & 7), q.d);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) t.keep[j] = m[j] >= 0 ? t.keep[j] : 0u;
-  } else if (c0 + 64 <= q.d) {
-    const uint16_t* x = q.x + c0 + 8 * (lane & 7);
-    int m[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      m[j] = __shfl(tok, 8 * j + (lane >> 3));
-      t.v[j] = load_vec(x + max(m[j], 0) * q.d);
-    }
-    if (__shfl(tok, 63) < 0) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) t.v[j] = only_if(m[j] >= 0, t.v[j]);
-    }
+    for (int j = 0; j < 8; ++j) t.v[j] = load_vec(x + __shfl(tok, 8 * j + (lane >> 3)) * q.d);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int m = __shfl(tok, 8 * j + (lane >> 3));
-      t.v[j] = u32x4{0, 0, 0, 0};
-      if (m >= 0) t.v[j] = load8(q.x + m * q.d, c0 + 8 * (lane & 7), q.d);
-    }
+    for (int j = 0; j < 8; ++j)
+      t.v[j] = few8(q.x + __shfl(tok, 8 * j + (lane >> 3)) * q.d, c0 + 8 * (lane & 7), q.d);
   }
 }
 
-template <bool PACKED>
-__device__ __forceinline__ void gram_stage(const GramTile& t, int lane, uint16_t* st) {
+// rows: the tile's tokens; those behind are zeros.
+template <bool PACKED, bool NARROW>
+__device__ __forceinline__ void gram_stage(const GramSide& q, int64_t c0, int rows, GramTile& t,
+                                           int lane, uint16_t* st) {
   if constexpr (PACKED) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      uint32_t keep = q.keep ? t.keep[j] >> (16 * (lane & 1)) : 0xFFFFu;
+      keep = 16 * j + (lane >> 2) < rows ? keep : 0u;
       u32x4 o[2];
 #pragma unroll
       for (int h = 0; h < 8; ++h) {
         const uint32_t c = t.v[j][h >> 1] >> (16 * (h & 1));
         const uint32_t b = pack_bf16x2((float)(int8_t)c * t.s[j], (float)(int8_t)(c >> 8) * t.s[j]);
-        const uint32_t k = t.keep[j] >> (2 * h);
+        const uint32_t k = keep >> (2 * h);
         o[h >> 2][h & 3] = b & (((k & 1) ? 0xFFFFu : 0u) | ((k & 2) ? 0xFFFF0000u : 0u));
       }
       u32x4* p = reinterpret_cast<u32x4*>(st + (16 * j + (lane >> 2)) * kGL + 16 * (lane & 3));
@@ -1143,6 +1130,15 @@ __device__ __forceinline__ void gram_stage(const GramTile& t, int lane, uint16_t
       p[1] = o[1];
     }
   } else {
+    if (c0 + 64 > q.d && (!NARROW || q.d >= 8)) {
+      const int64_t col = c0 + 8 * (lane & 7);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t.v[j] = past8(t.v[j], col - at8(col, q.d));
+    }
+    if (rows < 64) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t.v[j] = only_if(8 * j + (lane >> 3) < rows, t.v[j]);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       *reinterpret_cast<u32x4*>(st + (8 * j + (lane >> 3)) * kGL + 8 * (lane & 7)) = t.v[j];
@@ -1151,17 +1147,22 @@ __device__ __forceinline__ void gram_stage(const GramTile& t, int lane, uint16_t
 
 // A wavefront's part of a split: tiles w, w + 4, ...  sp: {slot, first tile,
 // tokens, }, `first` the split's first position.
-template <int NB, bool PACKED>
+// AHEAD: the operands of both halves of a tile before the next tile's rows.  Loads
+// return in order, so behind those the second half's wait for memory (4096
+// tokens, 4096 to 4096 features, 64 ranks, 4 slots: 39.4 us, ahead 33.5); at 64
+// ranks the kernel for codes has no registers for it (6385 tokens, 4736 to 2605
+// features, 50 ranks 44 us, ahead, with spills, 52).
+template <int NB, bool PACKED, bool NARROW, bool AHEAD>
 __device__ __forceinline__ void gram_item(const GramArgs8& a, const GramSide& q, int64_t c0,
                                           const int4& sp, int first, int w, int group,
                                           uint16_t* st, f32x4 (&acc)[NB][4]) {
   const int lane = threadIdx.x & 63;
   const int r16 = lane & 15, g = lane >> 4;
   const int tiles = (sp.z + 63) / 64;
+  if (w >= tiles) return;
   auto token = [&](int j) {
-    const int at = 64 * j + lane;
-    if (at >= sp.z) return -1;
-    return a.plan.head ? a.plan.order[first + at] : first + at;
+    const int at = first + min(64 * j + lane, sp.z - 1);
+    return a.plan.head ? a.plan.order[at] : at;
   };
   // the group's blocks of 16 ranks, three terms, of 32 tokens
   auto load_v = [&](const uint16_t* fr, int slice, u32x4 (&v)[NB][3]) {
@@ -1171,23 +1172,19 @@ __device__ __forceinline__ void gram_item(const GramArgs8& a, const GramSide& q,
       for (int term = 0; term < 3; ++term)
         v[n][term] = *reinterpret_cast<const u32x4*>(fr + ((term * a.nb + NB * group + n) * 2 + slice) * 512);
   };
-  if (w >= tiles) return;
   int next = token(w);
   GramTile cur;
-  gram_load<PACKED>(q, a.M, c0, next, lane, cur);
+  gram_load<PACKED, NARROW>(q, a.M, c0, next, lane, cur);
   next = token(w + 4);
   for (int j = w; j < tiles; j += 4) {
-    // in the order of their use: this tile's operands, the next tile's rows
+    // in the order of their use
     const uint16_t* fr = q.frags + (int64_t)(sp.y + j) * 3 * a.nb * 2 * 512 + lane * 8;
-    // (at 64 ranks two slices' operands cost registers that spill: 4096 tokens,
-    // 4096 to 4096 features, 64 ranks, 4 slots 45.7 us, with one slice's 38.9)
-    constexpr bool AHEAD = NB < 4;
     u32x4 v[1 + AHEAD][NB][3];
     load_v(fr, 0, v[0]);
-    gram_stage<PACKED>(cur, lane, st);
+    gram_stage<PACKED, NARROW>(q, c0, sp.z - 64 * j, cur, lane, st);
     if (AHEAD) load_v(fr, 1, v[AHEAD]);
     if (j + 4 < tiles) {
-      gram_load<PACKED>(q, a.M, c0, next, lane, cur);
+      gram_load<PACKED, NARROW>(q, a.M, c0, next, lane, cur);
       next = token(j + 8);
     }
 #pragma unroll
@@ -1210,9 +1207,10 @@ __device__ __forceinline__ void gram_item(const GramArgs8& a, const GramSide& q,
   }
 }
 
-template <int NB, bool PACKED>
+template <int NB, bool PACKED, bool NARROW>
 __global__ __launch_bounds__(256, 2) void k_gram8(GramArgs8 a) {
   constexpr int LR = 68;                            // a reduced row, FP32
+  constexpr bool AHEAD = NB < 4 || !PACKED;
   __shared__ __attribute__((aligned(16))) uint8_t glds[4 * 64 * kGL * 2];
   static_assert(4 * 16 * LR * 4 <= 4 * 64 * kGL * 2, "reduction buffer");
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1270,8 +1268,8 @@ __global__ __launch_bounds__(256, 2) void k_gram8(GramArgs8 a) {
       for (int cb = 0; cb < 4; ++cb) acc[nb][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
     float* out = part >= 0 ? q.part + part * a.r * q.d : q.out + (int64_t)sp.x * a.r * q.d;
     if (!alone || c0 < q.d) {
-      if (PACKED && side == 0) gram_item<NB, true>(a, q, c0, sp, first, alone ? 0 : w, group, st, acc);
-      else gram_item<NB, false>(a, q, c0, sp, first, alone ? 0 : w, group, st, acc);
+      if (PACKED && side == 0) gram_item<NB, true, NARROW, AHEAD>(a, q, c0, sp, first, alone ? 0 : w, group, st, acc);
+      else gram_item<NB, false, NARROW, AHEAD>(a, q, c0, sp, first, alone ? 0 : w, group, st, acc);
     }
     if (alone) {
 #pragma unroll
@@ -1399,8 +1397,13 @@ hipError_t launch_gram8_nb(GramArgs8 a, hipStream_t st) {
   a.nb = frag_blocks(a.r);
   a.groups = a.nb / NB;
   const unsigned grid = (unsigned)std::min<int64_t>(a.most * cols * a.groups, 2 * kMostGrid);
-  if (a.q[0].codes) hipLaunchKernelGGL((k_gram8<NB, true>), dim3(grid), dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((k_gram8<NB, false>), dim3(grid), dim3(256), 0, st, a);
+  auto run = [&](auto narrow) {
+    constexpr bool NARROW = decltype(narrow)::value;
+    if (a.q[0].codes) hipLaunchKernelGGL((k_gram8<NB, true, NARROW>), dim3(grid), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((k_gram8<NB, false, NARROW>), dim3(grid), dim3(256), 0, st, a);
+  };
+  if (std::min(a.q[0].d, a.q[1].d) < 8) run(std::true_type{});
+  else run(std::false_type{});
   return hipGetLastError();
 }
 
