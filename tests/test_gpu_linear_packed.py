@@ -42,7 +42,7 @@ def _exact(w, X, T, dY, A, B, s, keep=None, rest=1.0):
     return out, bound
 
 
-@pytest.mark.parametrize("M,d_in,d_out,r", [(1, 64, 64, 8), (5, 128, 77, 3), (16, 256, 200, 16), (17, 64, 128, 16), (100, 320, 136, 20),
+@pytest.mark.parametrize("M,d_in,d_out,r", [(9, 64, 3, 4), (300, 128, 7, 64), (1, 64, 1, 1), (1, 64, 64, 8), (5, 128, 77, 3), (16, 256, 200, 16), (17, 64, 128, 16), (100, 320, 136, 20),
                                             (130, 512, 257, 64), (333, 192, 520, 50), (257, 256, 264, 128), (90, 128, 96, 256),
                                             (2500, 128, 128, 16), (700, 192, 1100, 16), (16400, 64, 64, 8), (16390, 64, 67, 8)])
 def test_backward(M, d_in, d_out, r):
