@@ -430,9 +430,7 @@ __device__ __forceinline__ void shrink_item(const ShrinkArgs& a, const int4& td,
       }
   };
   int64_t k = k_begin + STEP * w;
-  // (a piece of F's rows of odd r may reach into the next row, which the last
-  // row of all does not have)
-  const int64_t k_whole = k_begin + (k_end - k_begin - (KN && !FAST && k_end == K ? 1 : 0)) / STEP * STEP;
+  const int64_t k_whole = shrink_whole_end(k_begin, k_end, K, r, KN && !FAST, STEP);
   if (k < k_whole) {
     const int64_t k_last = k + (k_whole - 1 - k) / (STEP * W) * (STEP * W);
     u32x4 x[SK][RB], f[SK * NB];
@@ -443,7 +441,7 @@ __device__ __forceinline__ void shrink_item(const ShrinkArgs& a, const int4& td,
     }
     k = k_last + STEP * W;
   }
-  // the last, partial step
+  // what is left: a partial step, or one and a whole one that the rule keeps out
   for (; k < k_end; k += STEP * W) {
     u32x4 x[SK][RB], f[SK * NB];
     if constexpr (FAST) {

@@ -660,6 +660,17 @@ inline int shrink_splits(int64_t M, int64_t K, int64_t* kper) {
   *kper = ((K + s - 1) / s + 255) / 256 * 256;
   return (int)((K + *kper - 1) / *kper);
 }
+// Where the steps of a range [k_begin, k_end) of K end that k_shrink loads
+// without conditions.  Rows of F stored [K][r] are taken in pieces of eight: where
+// those do not end with the row (r % 8 != 0), the last piece of row k ends at
+// element k r + round_up(r, 8), up to seven rows on (r = 1), and has to end within
+// K r: that keeps the last (round_up(r, 8) - 1) / r rows of F out, in whichever
+// range they lie.
+__host__ __device__ inline int64_t shrink_whole_end(int64_t k_begin, int64_t k_end, int64_t K, int r,
+                                                    bool kn, int step) {
+  const int64_t last = K - (kn ? ((r + 7) / 8 * 8 - 1) / r : 0), end = k_end < last ? k_end : last;
+  return k_begin + (end > k_begin ? end - k_begin : 0) / step * step;
+}
 // Ranks of a row of V in k_expand's operand (hi, then lo).
 inline int64_t vrow_ranks(int64_t r) { return r <= 32 ? 32 : (r <= 64 ? 64 : (r <= 128 ? 128 : 256)); }
 struct ShrinkArgs {
