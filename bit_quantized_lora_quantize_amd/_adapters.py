@@ -20,6 +20,7 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _F = ctypes.c_float
 _BF16, _F32, _I32, _I8 = torch.bfloat16, torch.float32, torch.int32, torch.int8
+_SMALL_M = 16   # a layer call of so many tokens reads no saved dropout mask
 
 
 class _Packed(ctypes.Structure):
@@ -142,6 +143,9 @@ def qlora_linear_bwd_packed(q: _lib.NF4Weight, X8: Packed8, dY: torch.Tensor, A:
     _need(A, _BF16, (r, q.d_in), "A", at)
     _need(B, _BF16, (q.d_out, r), "B", at)
     _need(T_saved, _F32, (M, r), "T_saved", at)
+    if dropout is not None and M > _SMALL_M and dropout.keep_rows is not None and dropout.keep_cols is not None:
+        _need(dropout.keep_rows, _I32, (M, q.d_in // 32), "dropout.keep_rows", at)
+        _need(dropout.keep_cols, _I32, (q.d_in, (M + 31) // 32), "dropout.keep_cols", at)
     dX = _out(dX, (M, q.d_in), _BF16, dev, "dX", at) if need_dx else None
     dA = _out(dA, (r, q.d_in), _F32, dev, "dA", at)
     dB = _out(dB, (q.d_out, r), _F32, dev, "dB", at)
