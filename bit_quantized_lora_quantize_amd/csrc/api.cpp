@@ -194,27 +194,32 @@ BwdPlan plan_bwd(int64_t d_out, int64_t d_in, int64_t M, int64_t r, void* ws) {
   return p;
 }
 
-// Backward from an input kept in 8 bits, after the region of plan_bwd: U in
-// FP32, the operands of the token contractions and their partial results.
+// Backward from an input kept in 8 bits: U in FP32 and as the input gradient's
+// operand, the operands of the token contractions and their partial results, with
+// dropout the mask's words.
 struct PackedPlan {
   float* u;                     // [splits][M][r]: partial sums of U
+  int64_t rp;                   // r rounded up to 32
+  uint16_t* u_hl;               // [M][2 rp] BF16 hi | lo of U
   uint16_t *t_frags, *u_frags;
   int tps;                      // tiles a token split
   float *da_part, *db_part;     // [splits][r][d_in], [splits][d_out][r]
   float* dx;                    // few tokens: [splits][M][d_in]
+  uint32_t *keep_rows, *keep_cols;   // [M][d_in / 32], [d_in][ldw]
+  int64_t ldw;
   size_t bytes;
 };
 
-PackedPlan plan_packed(size_t base_bytes, int64_t d_out, int64_t d_in, int64_t M, int64_t r,
-                       void* ws) {
+PackedPlan plan_packed(int64_t d_out, int64_t d_in, int64_t M, int64_t r, bool dropout, void* ws) {
   PackedPlan p{};
   Carver c(ws);
-  c.off = base_bytes;
   const int64_t tiles = cdiv(M, kPlanTile);
   p.tps = plan_split_tiles(std::max<int64_t>(M, 1));
   const int64_t splits = cdiv(tiles, p.tps), parts = splits > 1 ? splits : 0;
   int64_t kper;
   p.u = c.take<float>(shrink_splits(M, d_out, &kper) * M * r);
+  p.rp = round_up(r, 32);
+  p.u_hl = c.take<uint16_t>(M * 2 * p.rp);
   p.t_frags = c.take<uint16_t>(frag_elems(tiles, r));
   p.u_frags = c.take<uint16_t>(frag_elems(tiles, r));
   p.da_part = c.take<float>(parts * r * d_in);
@@ -222,6 +227,11 @@ PackedPlan plan_packed(size_t base_bytes, int64_t d_out, int64_t d_in, int64_t M
   int64_t nper;
   const int ds = dx_few(M, d_out, d_in) ? dx_few_splits(M, d_out, d_in, &nper) : 0;
   p.dx = c.take<float>(ds > 1 ? ds * M * d_in : 0);
+  p.ldw = cdiv(std::max<int64_t>(M, 1), 32);
+  if (dropout) {
+    p.keep_rows = c.take<uint32_t>(M * (d_in / 32));
+    p.keep_cols = c.take<uint32_t>(d_in * p.ldw);
+  }
   p.bytes = c.off + 256;
   return p;
 }
@@ -617,24 +627,21 @@ int bwd_impl(const qlora_nf4_t* q, const uint16_t* XA, const uint32_t* xmask,
 int bwd_packed_impl(const qlora_nf4_t* q, const qlora_packed_t* X8, const uint16_t* dY, int64_t M,
                     const uint16_t* A, const uint16_t* B, int64_t r, float sc,
                     const qlora_dropout_t* drop, DropoutArgs& da, const float* T, uint16_t* dX,
-                    const BwdPlan& p, const DropPlan& dp, const PackedPlan& pp, GramArgs8& ga,
-                    hipStream_t st) {
+                    const PackedPlan& p, GramArgs8& ga, hipStream_t st) {
   int s = QLORA_OK;
   const int64_t d_out = q->d_out, d_in = q->d_in;
   const uint32_t *rows = nullptr, *keep = nullptr;
   if (drop) {
     // the forward's saved mask, or the same bits again
     const bool saved = M > kSmallM && drop->keep_rows && drop->keep_cols;
-    // (small M: the words fit the room that plan_drop has for a masked copy)
-    uint32_t* bits = dp.xm ? reinterpret_cast<uint32_t*>(dp.xm) : dp.rbits;
-    rows = saved ? drop->keep_rows : bits;
-    keep = saved ? drop->keep_cols : dp.keep;
+    rows = saved ? drop->keep_rows : p.keep_rows;
+    keep = saved ? drop->keep_cols : p.keep_cols;
     if (!saved) {
-      da.keep = dp.keep;
+      da.keep = p.keep_cols;
       da.M = M;
       da.d = d_in;
-      da.ldw = dp.ldw;
-      s = hip_status(launch_dropout_bits(da, bits, st));
+      da.ldw = p.ldw;
+      s = hip_status(launch_dropout_bits(da, p.keep_rows, st));
       if (s) return s;
     }
     sc /= 1.0f - drop->p;
@@ -649,7 +656,7 @@ int bwd_packed_impl(const qlora_nf4_t* q, const qlora_packed_t* X8, const uint16
   sa.kn = true;
   sa.P = dY;
   sa.F = B;
-  sa.part = pp.u;
+  sa.part = p.u;
   s = hip_status(launch_shrink(sa, st));
   if (s) return s;
   int64_t kper;
@@ -660,32 +667,32 @@ int bwd_packed_impl(const qlora_nf4_t* q, const qlora_packed_t* X8, const uint16
   fa.rp = (int)p.rp;
   fa.splits = shrink_splits(M, d_out, &kper);
   fa.one_scale = sc;
-  fa.V = pp.u;
+  fa.V = p.u;
   fa.T = T;
   fa.vrows = dX ? p.u_hl : nullptr;
-  fa.u_frags = pp.u_frags;
-  fa.t_frags = pp.t_frags;
+  fa.u_frags = p.u_frags;
+  fa.t_frags = p.t_frags;
   s = hip_status(launch_finish_v(fa, st));
   if (s) return s;
   if (dX && dx_few(M, d_out, d_in)) {
     DxFewArgs g{q->codes, q->scale_codes, q->scale2, q->scale_mean, dY, p.u_hl, A,    dX,
-                pp.dx,    M,              d_out,     d_in,          r,  p.rp,   keep, dp.ldw};
+                p.dx,    M,              d_out,     d_in,          r,  p.rp,   keep, p.ldw};
     s = hip_status(launch_dx_few(g, st));
     if (s) return s;
   } else if (dX) {
     GemmArgs g{q->codes, q->scale_codes, q->scale2, q->scale_mean, dY, p.u_hl, A, dX,
-               M,        d_out,          d_in,      r,            keep, dp.ldw};
+               M,        d_out,          d_in,      r,            keep, p.ldw};
     s = hip_status(launch_gemm_bwd(g, st));
     if (s) return s;
   }
   ga.q[0].codes = X8->codes;
   ga.q[0].scale = X8->scale;
   ga.q[0].keep = rows;
-  ga.q[0].frags = pp.u_frags;
-  ga.q[0].part = pp.da_part;
+  ga.q[0].frags = p.u_frags;
+  ga.q[0].part = p.da_part;
   ga.q[1].x = dY;
-  ga.q[1].frags = pp.t_frags;
-  ga.q[1].part = pp.db_part;
+  ga.q[1].frags = p.t_frags;
+  ga.q[1].part = p.db_part;
   return hip_status(launch_gram8(ga, st));
 }
 
@@ -744,11 +751,8 @@ size_t qlora_workspace_bytes(int op, int64_t d_out, int64_t d_in, int64_t M, int
     return plan_drop(plan_fwd(d_out, d_in, M, r, nullptr).bytes, M, d_in, false, nullptr).bytes;
   if (op == QLORA_OP_BWD_DROPOUT)
     return plan_drop(plan_bwd(d_out, d_in, M, r, nullptr).bytes, M, d_in, true, nullptr).bytes;
-  if (op == QLORA_OP_BWD_PACKED || op == QLORA_OP_BWD_PACKED_DROPOUT) {
-    size_t base = plan_bwd(d_out, d_in, M, r, nullptr).bytes;
-    if (op == QLORA_OP_BWD_PACKED_DROPOUT) base = plan_drop(base, M, d_in, true, nullptr).bytes;
-    return plan_packed(base, d_out, d_in, M, r, nullptr).bytes;
-  }
+  if (op == QLORA_OP_BWD_PACKED || op == QLORA_OP_BWD_PACKED_DROPOUT)
+    return plan_packed(d_out, d_in, M, r, op == QLORA_OP_BWD_PACKED_DROPOUT, nullptr).bytes;
   return 0;
 }
 
@@ -1035,28 +1039,21 @@ int qlora_linear_bwd_packed(const qlora_nf4_t* q, const qlora_packed_t* X8, cons
   if (!aligned16(X8->codes) || (reinterpret_cast<uintptr_t>(X8->scale) & 3u))
     return QLORA_ERR_ALIGN;
   const int64_t d_out = q->d_out, d_in = q->d_in;
-  const BwdPlan p = plan_bwd(d_out, d_in, M, r, ws);
-  DropPlan dp{};
-  size_t base = p.bytes;
-  if (drop) {
-    dp = plan_drop(base, M, d_in, true, ws);
-    base = dp.bytes;
-  }
-  const PackedPlan pp = plan_packed(base, d_out, d_in, M, r, ws);
-  if (ws_bytes < pp.bytes) return QLORA_ERR_WORKSPACE;
+  const PackedPlan p = plan_packed(d_out, d_in, M, r, drop != nullptr, ws);
+  if (ws_bytes < p.bytes) return QLORA_ERR_WORKSPACE;
   hipStream_t st = static_cast<hipStream_t>(stream);
   GramArgs8 ga{};
   ga.M = M;
   ga.slots = 1;
   ga.r = r;
-  ga.tps = pp.tps;
+  ga.tps = p.tps;
   ga.q[0].out = dA;
   ga.q[0].d = d_in;
   ga.q[1].out = dB;
   ga.q[1].d = d_out;
   if (M == 0) return hip_status(launch_gram_zero(ga, st));
-  return bwd_packed_impl(q, X8, dY, M, A, B, r, lora_alpha / (float)r, drop, da, T_saved, dX, p, dp,
-                         pp, ga, st);
+  return bwd_packed_impl(q, X8, dY, M, A, B, r, lora_alpha / (float)r, drop, da, T_saved, dX, p, ga,
+                         st);
 }
 
 int qlora_nf4_blocked_sizes(int64_t n, int64_t block, int64_t group, size_t* codes_bytes,
