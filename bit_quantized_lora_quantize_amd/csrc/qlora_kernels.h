@@ -478,14 +478,15 @@ inline int dx_few_splits(int64_t M, int64_t d_out, int64_t d_in, int64_t* nper) 
   *nper = ((d_out + s - 1) / s + 127) / 128 * 128;
   return (int)((d_out + *nper - 1) / *nper);
 }
-// Whether it takes the place of the fused GEMM: while the GEMM has fewer than 64
-// tiles of 256 x 256 (whole backward, 4096 -> 4096, rank 16: 1 token 29 us and
-// 109, 512 tokens 76 and 119, 1024 tokens, 64 tiles, 114 and 125; 2048 tokens,
-// 128 tiles, 205 and 137), and for rows of dY that are no whole 16-byte pieces,
-// which the GEMM loads by element (2048 tokens 4096 -> 4099 396 and 667, 8192
+// Whether it takes the place of the fused GEMM: while the GEMM has up to 64 tiles
+// of 256 x 256 (whole backward, rank 16, this and the GEMM: 4096 -> 4096, 32 tiles
+// 78 us and 118, 48 tiles 103 and 125, 64 tiles 113 and 126, 80 tiles 143 and 129,
+// 128 tiles 205 and 133; 64 tiles of 1024 -> 4096 121 and 137, of 4096 -> 11008 257
+// and 279, 80 of these 331 and 282), and for rows of dY that are no whole 16-byte
+// pieces, which the GEMM loads by element (2048 tokens 4096 -> 4099 396 and 667, 8192
 // tokens 1388 and 1424, 8192 tokens -> 4100 819 and 1240).
 inline bool dx_few(int64_t M, int64_t d_out, int64_t d_in) {
-  return d_out % 8 != 0 || (M + 255) / 256 * ((d_in + 255) / 256) < 64;
+  return d_out % 8 != 0 || (M + 255) / 256 * ((d_in + 255) / 256) <= 64;
 }
 struct DxFewArgs {
   const uint8_t* codes;
