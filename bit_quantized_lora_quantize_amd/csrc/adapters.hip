@@ -334,15 +334,12 @@ __global__ __launch_bounds__(64) void k_plan_place(PlanView p, const int32_t* __
 // into operands.
 // ---------------------------------------------------------------------------
 constexpr int kShrinkWaves = 4;
-// K slices of 32 per step: two, whole lines of a row, where their loads fit the
-// registers beside the sums.
-template <int NB>
-constexpr int shrink_slices() { return 2; }
+constexpr int kShrinkSlices = 2;   // K slices of 32 a step: whole lines of a row
 template <int NB, bool KN>
 constexpr int shrink_lds() {
   constexpr int CN = NB < 4 ? NB : 4;
   constexpr int red = kShrinkWaves * 16 * 16 * CN * 4;
-  constexpr int stage = KN ? kShrinkWaves * 32 * shrink_slices<NB>() * (16 * NB + 8) * 2 : 0;
+  constexpr int stage = KN ? kShrinkWaves * 32 * kShrinkSlices * (16 * NB + 8) * 2 : 0;
   return red > stage ? red : stage;
 }
 
@@ -359,7 +356,7 @@ __device__ __forceinline__ void put_vrow(uint16_t* vrows, int64_t pos, int i, in
 // more and, KN, rows of F that are whole 16-byte pieces.
 template <int NB, bool KN, bool FAST, int RB>
 __device__ __forceinline__ void shrink_item(const ShrinkArgs& a, const int4& td, int s, int i0, uint8_t* lds) {
-  constexpr int W = kShrinkWaves, CN = NB < 4 ? NB : 4, SK = shrink_slices<NB>();
+  constexpr int W = kShrinkWaves, CN = NB < 4 ? NB : 4, SK = kShrinkSlices;
   constexpr int LF = 16 * NB + 8;                  // staged row of F, elements
   constexpr int STEP = 32 * SK;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -939,7 +936,7 @@ __global__ __launch_bounds__(256, KS > 4 ? 1 : (DEEP || KS > 2 ? 2 : 3)) void k_
 // What k_shrink's partial sums become: V = scale_a * (their sum, in order) as
 // k_expand's rows (vrows), by token (v_out), and as a row operand of the
 // contractions over tokens (u_frags); the caller's T as such an operand
-// (t_frags).  Without partial sums (splits 0) V is given by token.
+// (t_frags).
 //
 // Row operands: per tile, BF16 term (hi, mid, lo: 24 bits together), 16 ranks
 // and 32 tokens one KB in the order of an MFMA's lanes; zero past the tile's
@@ -969,9 +966,7 @@ __global__ __launch_bounds__(256) void k_finish(FinishVArgs a) {
     const int first = td.y + 32 * slice, count = min(32, td.z - 32 * slice), i0 = 64 * grp;
     uint16_t* frags = is_t ? a.t_frags : a.u_frags;
     if (count <= 0 && !frags) continue;
-    const bool by_part = !is_t && a.splits > 0;
-    const float sc = by_part && a.scale ? a.scale[td.x] : a.one_scale;
-    const float* v_in = is_t ? a.T : a.V;
+    const float sc = !is_t && a.scale ? a.scale[td.x] : a.one_scale;
     const int64_t stride = a.M * r;
     const int cols = min(64, max(16 * nb, a.vrows && !is_t ? a.rp : 0) - i0);
     const int rows = frags ? 32 : (count + 15) / 16 * 16;
@@ -990,16 +985,16 @@ __global__ __launch_bounds__(256) void k_finish(FinishVArgs a) {
           on[q] = row < count && i < r;
           at[q] = on[q] ? row * r + i : 0;
           tok[q] = 0;
-          if (on[q] && (!by_part || a.v_out)) tok[q] = a.plan.head ? a.plan.order[first + row] : first + row;
+          if (on[q] && (is_t || a.v_out)) tok[q] = a.plan.head ? a.plan.order[first + row] : first + row;
         }
-        if (by_part) {
-          sum_parts<SM, Q, N>(v_in + (int64_t)first * r, at, on, a.splits, stride, v);
+        if (!is_t) {
+          sum_parts<SM, Q, N>(a.V + (int64_t)first * r, at, on, a.splits, stride, v);
         } else {
 #pragma unroll
           for (int q = 0; q < Q; ++q)
 #pragma unroll
             for (int j = 0; j < N; ++j)
-              v[q][j] = on[q] ? v_in[tok[q] * r + i0 + N * ((e0 + 256 * q) % PR) + j] : 0.0f;
+              v[q][j] = on[q] ? a.T[tok[q] * r + i0 + N * ((e0 + 256 * q) % PR) + j] : 0.0f;
         }
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
@@ -1007,7 +1002,7 @@ __global__ __launch_bounds__(256) void k_finish(FinishVArgs a) {
           if (row >= rows || i >= cols) continue;
 #pragma unroll
           for (int j = 0; j < N; ++j) {
-            const float x = on[q] ? (by_part ? v[q][j] * sc : v[q][j]) : 0.0f;
+            const float x = on[q] ? (is_t ? v[q][j] : v[q][j] * sc) : 0.0f;
             if (!is_t && on[q] && a.v_out) a.v_out[tok[q] * r + i0 + i + j] = x;
             float hi, rest, mid, lo;
             split_bf16(x, hi, rest);

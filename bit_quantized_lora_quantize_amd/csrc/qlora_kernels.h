@@ -695,10 +695,10 @@ struct FinishVArgs {
   int64_t M, slots;
   int r, nb, most;         // nb, most: set by launch_finish_v
   int rp;                  // ranks of a row of vrows; 0: vrow_ranks(r)
-  int splits;              // partial sums in V by position; 0: V by token, as it is
-  const float* scale;      // [slots], with splits; NULL: one_scale
+  int splits;              // of the partial sums
+  const float* scale;      // [slots]; NULL: one_scale
   float one_scale;
-  const float* V;
+  const float* V;          // [splits][M][r] partial sums, by position
   const float* T;          // [M][r] by token, with t_frags
   uint16_t* vrows;         // outputs, each or NULL
   float* v_out;
