@@ -24,19 +24,9 @@
 #include "qlora_kernels.h"
 #include "row_ops.h"
 
-
 namespace qlora {
 
 namespace {
-
-typedef short v4i16_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) v4i16_t lds_v4i16_t;
-
-// Four rows x 16 columns of 16-bit values in LDS, transposed: lane j of a group
-// of 16 points at columns 4 (j % 4) .. +4 of row j / 4 and gets column j.
-__device__ __forceinline__ uint2 lds_tr(const uint16_t* p) {
-  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t*)p));
-}
 
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu); }
 
@@ -77,13 +67,6 @@ __device__ __forceinline__ u32x4 only_if(bool ok, u32x4 v) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) v[j] = ok ? v[j] : 0u;
   return v;
-}
-
-// A barrier for data in LDS alone: loads from memory stay in flight.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // Ranks past 64 are worked on in groups of 64, items of their own: the groups of

@@ -119,13 +119,6 @@ __device__ __forceinline__ void weight_part(const Part<T, V>& p, const void* w, 
   rest = p.rest >= 0 ? load_w(w, w_type, p.rest) : 0.0f;
 }
 
-// A barrier for data in LDS alone: loads from memory stay in flight.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
 // Sums over the `threads` threads (whole wavefronts, at most 16) of each row of
 // a workgroup; the rows of a workgroup go through it together.
 template <int COUNT>

@@ -1,5 +1,5 @@
-// row_ops.h -- element access and reductions shared by the kernels that work
-// on rows (norm.hip, logits.hip).
+// row_ops.h -- element access, reductions and LDS helpers shared by the kernels
+// that work on rows (norm.hip, logits.hip, pack8.hip, adapters.hip, dx_few.hip).
 //
 // Rows are taken in 16-byte vectors that need not be aligned: a row of odd
 // length starts anywhere, and one wavefront's access still covers 1 KB without
@@ -54,6 +54,21 @@ __device__ __forceinline__ u32x4 load_vec_once(const T* p) {
 template <typename T>
 __device__ __forceinline__ void store_vec_once(T* p, u32x4 v) {
   __builtin_nontemporal_store(v, reinterpret_cast<typename VecAt<T>::type*>(p));
+}
+
+// Four rows x 16 columns of 16-bit values in LDS, transposed: lane j of a group
+// of 16 points at columns 4 (j % 4) .. +4 of row j / 4 and gets column j.
+__device__ __forceinline__ uint2 lds_tr(const uint16_t* p) {
+  typedef short v4i16 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)p));
+}
+
+// A barrier for data in LDS alone: loads from memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 template <typename T>
