@@ -310,8 +310,9 @@ __global__ __launch_bounds__(64) void k_plan_place(PlanView p, const int32_t* __
 // workgroup take the range's steps in turn, each all 64 tokens and all ranks:
 // no wavefront loads what another loads, and the loop has no barrier.  A step's
 // loads are 16 a wavefront and not a step ahead: two workgroups a compute unit
-// hide more than a second set of registers does (16384 x 4096, rank 64: 49 us;
-// a step ahead, one workgroup: 65; read at 5.7 TB/s it would be 24).  The sums
+// hide more than a second set of registers does (16384 x 4096, rank 64: 55 us; a
+// step ahead, with one workgroup, a third more; read at 5.7 TB/s it would be 24).
+// The sums
 // are added through LDS at the end, in wavefront order.  KN: a step's rows
 // of F go through LDS of the wavefront's own, which the transposing reads turn
 // into operands.
@@ -574,7 +575,7 @@ __device__ __forceinline__ void sum_parts(const float* part, const int (&at)[Q],
 // unit_column a lane ends up with twice eight consecutive columns of a token; LDS
 // of the wavefront's own turns them so that its loads and stores are whole
 // 128-byte lines (64 bytes of 16 rows an instruction took 164 us for the rows of
-// 16384 x 11008 alone, lines 138).
+// 16384 x 11008 alone, lines 138; the whole kernel takes 160, 158 without staging F).
 //
 // Items of up to 16 tokens (decoding) have nothing to reuse F for: there each
 // wavefront takes 64 columns and reads F from memory.
@@ -1125,9 +1126,10 @@ __device__ __forceinline__ void gram_stage(const GramSide& q, int64_t c0, int ro
 // tokens, }, `first` the split's first position.
 // AHEAD: the operands of both halves of a tile before the next tile's rows.  Loads
 // return in order, so behind those the second half's wait for memory (4096
-// tokens, 4096 to 4096 features, 64 ranks, 4 slots: 39.4 us, ahead 33.5); at 64
-// ranks the kernel for codes has no registers for it (6385 tokens, 4736 to 2605
-// features, 50 ranks 44 us, ahead, with spills, 52).
+// tokens, 4096 to 4096 features, 64 ranks, 4 slots: 39.4 us, ahead 33.5, although
+// 22 registers spill then); at 64 ranks the kernel for codes, which spills 5
+// without it, has no registers left (6385 tokens, 4736 to 2605 features, 50 ranks
+// 44 us, ahead 52).
 template <int NB, bool PACKED, bool NARROW, bool AHEAD>
 __device__ __forceinline__ void gram_item(const GramArgs8& a, const GramSide& q, int64_t c0,
                                           const int4& sp, int first, int w, int group,

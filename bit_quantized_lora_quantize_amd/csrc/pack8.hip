@@ -13,7 +13,7 @@
 //     quotient is one, and on the quotient's side of it elsewhere.
 //   FP32: within 4e-5 of a half integer the sign of |127 x - k a| - a / 2 is
 //     taken in FP64, where both products (31 and 32 bits) and their difference
-//     are exact; one vector of 500 gets there.
+//     are exact; where the quotients are spread, one vector of 1500 gets there.
 // (In FP64 for every value the kernel was bound by its arithmetic: 44 us for
 // 4096 x 11008 BF16.)
 //

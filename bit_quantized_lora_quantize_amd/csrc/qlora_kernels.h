@@ -619,7 +619,7 @@ struct PlanView {
   int32_t* head;   // [kPlanHead]; NULL (contractions only): one slot, every token, in order
   int32_t* order;  // [M] token at each position
   int32_t* begin;  // [slots + 1] first position of each slot (batches of several spans)
-  int4* tile;      // {slot (-1: none), first position, tokens, 0}
+  int4* tile;      // {slot (-1: none), first position, tokens, 0}: one load
   int4* split;     // {slot, first tile, tokens, number among its slot's splits (-1: the only one)}
   int32_t* split_first;   // their first positions
   int2* parts;     // [slots] {its splits' first partial result, its splits}
@@ -627,7 +627,7 @@ struct PlanView {
 };
 // Tiles of a token split of the weight gradients: 8 to 16 (four splits of one
 // slot where that gives them), more where one slot would have 64 splits and more.
-// Half as many (2048 tokens, 4096 x 4096, rank 64) took 26 us instead of 20 and
+// Half as many (2048 tokens, 4096 x 4096, rank 64) took 22 us instead of 18 and
 // 10 instead of 6 to add the parts.
 inline int plan_split_tiles(int64_t M) {
   const int64_t tiles = (M + kPlanTile - 1) / kPlanTile;
@@ -651,8 +651,8 @@ hipError_t launch_plan(const PlanView& p, const int32_t* index, int64_t M, int64
 
 // Ranges of the long axis K that k_shrink sums apart, for about 1024 items: two
 // workgroups a compute unit, several times over, so that one's start and end
-// overlap another's loads.  16384 tokens: K 4096, rank 64 in four ranges 49 us, in
-// two 58, in one 82; K 11008, rank 16 in four 79, in two 100.
+// overlap another's loads.  16384 tokens: K 4096, rank 64 in four ranges 55 us (and
+// 9 to add them), in two 63 (8), in one 82; K 11008, rank 16 in four 80, in two 102.
 constexpr int kShrinkSplits = 8;   // at most
 inline int shrink_splits(int64_t M, int64_t K, int64_t* kper) {
   const int64_t tiles = std::max<int64_t>(1, (M + kPlanTile - 1) / kPlanTile);

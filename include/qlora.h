@@ -736,7 +736,8 @@ int qlora_linear_bwd_packed(const qlora_nf4_t *q, const qlora_packed_t *X8,
  * workspace: 16 bytes); 16-byte aligned rows (widths and, in B, a rank that are
  * multiples of 8) are fastest.  Infinities and NaN of a token stay with that
  * token in Y, T and dX and reach its own slot's dA and dB; a slot's stay with
- * its tokens.
+ * its tokens.  An infinity (and a T or U past BF16's range) can come out of the
+ * second products as a NaN: T and U enter them as sums of BF16 terms.
  */
 typedef struct {
   int64_t slots, r, d_in, d_out;
@@ -770,7 +771,9 @@ int qlora_adapters_plan(const int32_t *index, int64_t M, int64_t slots, void *pl
  *   Y       BF16 [M, d_out] output, may be Y0
  *   T_save  FP32 [M, r] or NULL: for the backward
  * workspace (16B) >= qlora_adapters_workspace_bytes(0, bank, M).  Deterministic;
- * a token's results do not depend on the other tokens' values.
+ * a token's results do not depend on the other tokens' values and places.  M
+ * decides in how many ranges the sums over d_in are taken: in a batch of another
+ * size the last bits can differ.
  */
 int qlora_adapters_fwd(const qlora_adapters_t *bank, const void *plan, size_t plan_bytes,
                        const uint16_t *X, int64_t M, const uint16_t *Y0, uint16_t *Y,
@@ -792,7 +795,8 @@ int qlora_adapters_fwd(const qlora_adapters_t *bank, const void *plan, size_t pl
  *   dA       FP32 [slots, r, d_in], dB FP32 [slots, d_out, r]: overwritten
  *            (M = 0 writes zeros)
  * workspace (16B) >= qlora_adapters_workspace_bytes(1, bank, M).  Sums over
- * tokens have a fixed order: deterministic.
+ * tokens have a fixed order: deterministic (M decides the ranges of the sums over
+ * d_out, as in the forward).
  */
 int qlora_adapters_bwd(const qlora_adapters_t *bank, const void *plan, size_t plan_bytes,
                        const uint16_t *X, const qlora_packed_t *X8, const float *T,
